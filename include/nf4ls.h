@@ -571,6 +571,65 @@ int nf4ls_attention_bwd(const nf4ls_layer_cfg* cfg, const void* q_dev, const voi
                         const float* lse_dev, float* delta_dev, void* dq_dev, void* dk_dev, void* dv_dev,
                         nf4ls_stream stream);
 
+/* ------------------------------------------------------------------ packed batches
+ * Sequences of different lengths whose rows lie one behind the other, without padding:
+ * row cu[s] + i of every tensor is token i of sequence s.  A length may be 0.  Rows
+ * behind the last sequence (a buffer may hold more than `total` rows) are neither read
+ * nor written by any packed call.  Sequences do not see each other: a non-finite value
+ * in one sequence leaves the results of the others as they are.
+ *
+ * nf4ls_pack_layout: fills *out for n_seqs lengths (host), all but plan_dev.
+ * nf4ls_pack_fill: writes the plan (pack->plan_bytes bytes) to host memory; the caller
+ * copies it into a 256-byte aligned device buffer and sets plan_dev.  The plan serves
+ * every packed call of the batch, on any stream, and is only read.  Both are host-only.
+ * In the plan: cu int32 [n_seqs + 1] (first row of each sequence, then total), positions
+ * int32 [total] (row - cu of its sequence), seq int32 [total] (its sequence), and two
+ * lists of 128-row tiles, each sorted with the most work first. */
+#define NF4LS_PACK_MAX_SEQS (1 << 20)
+#define NF4LS_PACK_MAX_ROWS (1 << 28)
+
+typedef struct {
+    int32_t n_seqs, total, n_tiles, max_len;
+    uint64_t off_cu, off_positions, off_seq, off_query_tiles, off_key_tiles, plan_bytes;
+    const void* plan_dev;
+} nf4ls_pack;
+
+int nf4ls_pack_layout(const int32_t* lengths_host, int32_t n_seqs, nf4ls_pack* out);
+int nf4ls_pack_fill(const int32_t* lengths_host, const nf4ls_pack* pack, void* plan_host, size_t bytes);
+
+/* Causal grouped-query attention within each sequence of a packed batch:
+ *   o[i] = sum_j p[i, j] v[j],  p[i, :] = softmax over j <= i of scale q[i] . k[j],
+ * i, j in the same sequence.  q, o: bf16 [total, n_q * head_dim]; k, v: bf16 [total,
+ * n_kv * head_dim]; each with a row stride ld_* in elements (a multiple of 8, at least the
+ * row's width).  lse: fp32 [n_q, total], the log-sum-exp of each row of scaled scores.
+ * head_dim 64 or 128, n_q a multiple of n_kv, scale > 0.
+ *
+ * The backward takes o and lse of the forward and do (dL/do) and writes dq, dk, dv, the
+ * gradients with respect to q, k and v as given (dk and dv summed over the query heads
+ * that share them).  ws: nf4ls_packed_attention_ws_bytes, 256-byte aligned, free again
+ * once the call's kernels have finished.  Deterministic: no atomics, fixed reduction
+ * orders.  No output may overlap an input. */
+typedef struct {
+    int32_t n_q, n_kv, head_dim;
+    float scale;
+} nf4ls_packed_heads;
+
+typedef struct {
+    const void *q, *k, *v;
+    void* o;                          /* written by the forward, read by the backward  */
+    float* lse;                       /* written by the forward, read by the backward  */
+    const void* d_o;                  /* from here on: backward only                   */
+    void *dq, *dk, *dv;
+    int32_t ld_q, ld_k, ld_v, ld_o, ld_do, ld_dq, ld_dk, ld_dv;
+} nf4ls_packed_attention;
+
+size_t nf4ls_packed_attention_ws_bytes(const nf4ls_pack* pack, const nf4ls_packed_heads* heads);
+int nf4ls_packed_attention_fwd(const nf4ls_pack* pack, const nf4ls_packed_heads* heads,
+                               const nf4ls_packed_attention* t, nf4ls_stream stream);
+int nf4ls_packed_attention_bwd(const nf4ls_pack* pack, const nf4ls_packed_heads* heads,
+                               const nf4ls_packed_attention* t, void* ws_dev, size_t ws_bytes,
+                               nf4ls_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

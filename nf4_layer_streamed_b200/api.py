@@ -350,6 +350,168 @@ def attention_bwd(cfg: B.LayerCfg, q, k, v, ld_q: int, ld_kv: int, o, do, lse, s
     return dq, dk, dv, delta
 
 
+# ----------------------------------------------------------------------------- packed batches
+
+class PackedRows:
+    """The plan of a packed batch: sequences of the given lengths, one behind the other in
+    `total` rows (nf4ls_pack).  Made once per batch and used by every packed call on it;
+    positions, seq (int32 [total]) and cu (int32 [n_seqs + 1]) are device views of it."""
+
+    def __init__(self, lengths, device="cuda"):
+        n = np.asarray(lengths, dtype=np.int64)
+        if n.ndim != 1 or n.size == 0:
+            raise ValueError("PackedRows: expected a non-empty list of lengths")
+        if n.min() < 0 or n.max() > (1 << 28):
+            raise ValueError("PackedRows: lengths outside [0, 2^28]")
+        n32 = np.ascontiguousarray(n, dtype=np.int32)
+        self.pack = B.Pack()
+        B.call("nf4ls_pack_layout", n32.ctypes.data, n32.size, ctypes.byref(self.pack))
+        host = torch.empty(self.pack.plan_bytes, dtype=torch.uint8)
+        B.call("nf4ls_pack_fill", n32.ctypes.data, ctypes.byref(self.pack), host.data_ptr(), host.numel())
+        self.plan = host.to(device)
+        self.device = self.plan.device
+        if self.plan.is_cuda:
+            _aligned(self.plan)
+        self.pack.plan_dev = self.plan.data_ptr()
+        self.n_seqs, self.total, self.max_len = self.pack.n_seqs, self.pack.total, self.pack.max_len
+        self.cu = self._view(self.pack.off_cu, self.n_seqs + 1)
+        self.positions = self._view(self.pack.off_positions, self.total)
+        self.seq = self._view(self.pack.off_seq, self.total)
+        self._ref = ctypes.byref(self.pack)
+
+    def _view(self, off: int, n: int) -> torch.Tensor:
+        return self.plan[off:off + 4 * n].view(torch.int32)
+
+
+def _need_pack(pack) -> PackedRows:
+    if not isinstance(pack, PackedRows):
+        raise TypeError(f"pack: expected a PackedRows, got {type(pack).__name__}")
+    return pack
+
+
+def _rows2d(t, name: str, rows: int, width: int) -> int:
+    """Checks a bf16 [>= rows, width] matrix of unit column stride and returns its row
+    stride in elements (a multiple of 8, as 16-byte rows need)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[0] < rows or t.shape[1] != width:
+        raise ValueError(f"{name}: expected bf16 [>= {rows}, {width}], got {t.dtype} {tuple(t.shape)}")
+    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+    if (width > 1 and t.stride(1) != 1) or ld < width or ld % 8 or ld >= 1 << 31:
+        raise ValueError(f"{name}: strides {t.stride()} (unit column stride; row stride a multiple of 8, at least the width)")
+    if t.data_ptr() % 16:
+        raise ValueError(f"{name}: must be 16-byte aligned")
+    return ld
+
+
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether the rows of two matrices share memory (column slices of one buffer do not)."""
+    if a.numel() == 0 or b.numel() == 0 or a.untyped_storage().data_ptr() != b.untyped_storage().data_ptr():
+        return False
+    ea, eb = a.element_size(), b.element_size()
+    a0, b0 = a.data_ptr(), b.data_ptr()
+    a1 = a0 + ((a.shape[0] - 1) * a.stride(0) + a.shape[1]) * ea
+    b1 = b0 + ((b.shape[0] - 1) * b.stride(0) + b.shape[1]) * eb
+    if a1 <= b0 or b1 <= a0:
+        return False
+    ld = a.stride(0) * ea
+    if ea == eb and a.stride(0) == b.stride(0) and ld > 0:  # same rows: compare the column ranges
+        c = (b0 - a0) % ld
+        return c < a.shape[1] * ea or c + b.shape[1] * eb > ld
+    return True
+
+
+class _On:
+    """The device of a call's tensors made current, and its stream: `stream`, or the
+    device's current one.  Everything the call allocates belongs to that stream."""
+
+    def __init__(self, device, stream, **tensors):
+        for name, t in tensors.items():
+            if t is not None and t.device != device:
+                raise ValueError(f"{name}: on {t.device}, the call is on {device}")
+        if device.type != "cuda":
+            raise ValueError(f"{next(iter(tensors))}: must be a CUDA tensor")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream: on {stream.device}, the call is on {device}")
+        self.ctx = torch.cuda.stream(stream) if stream is not None else \
+            torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
+
+    def __enter__(self) -> ctypes.c_void_p:
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc) -> None:
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _heads(n_q: int, n_kv: int, head_dim: int, scale) -> B.PackedHeads:
+    if head_dim not in (64, 128):
+        raise ValueError(f"head_dim {head_dim}: 64 or 128")
+    if n_kv < 1 or n_q < 1 or n_q % n_kv:
+        raise ValueError(f"{n_q} query heads are not a multiple of {n_kv} key/value heads")
+    scale = head_dim ** -0.5 if scale is None else float(scale)
+    if not 0.0 < scale < 1e30:
+        raise ValueError(f"scale {scale}: must be positive")
+    return B.PackedHeads(n_q, n_kv, head_dim, scale)
+
+
+def packed_attention_fwd(pack: PackedRows, q, k, v, n_q: int, n_kv: int, head_dim: int, scale: float | None = None,
+                         out: torch.Tensor | None = None, stream=None):
+    """Causal attention within each sequence of the pack -> (o bf16 [total, n_q * head_dim],
+    lse fp32 [n_q, total]).  scale: 1 / sqrt(head_dim) unless given.  out: rows to write o to
+    (rows behind the pack's last stay as they are)."""
+    pack = _need_pack(pack)
+    heads = _heads(n_q, n_kv, head_dim, scale)
+    rows, qd, kvd = pack.total, n_q * head_dim, n_kv * head_dim
+    ld_q, ld_k, ld_v = _rows2d(q, "q", rows, qd), _rows2d(k, "k", rows, kvd), _rows2d(v, "v", rows, kvd)
+    if out is not None:
+        ld_o = _rows2d(out, "out", rows, qd)
+        if any(_overlap(out, t) for t in (q, k, v)):
+            raise ValueError("out: overlaps an input")
+    with _On(pack.device, stream, q=q, k=k, v=v, out=out) as s:
+        if out is None:
+            out, ld_o = torch.empty(rows, qd, dtype=torch.bfloat16, device=pack.device), qd
+        lse = torch.empty(n_q, rows, dtype=torch.float32, device=pack.device)
+        if rows:
+            t = B.PackedAttention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), None, None,
+                                  None, None, ld_q, ld_k, ld_v, ld_o, 0, 0, 0, 0)
+            B.call("nf4ls_packed_attention_fwd", pack._ref, ctypes.byref(heads), ctypes.byref(t), s)
+    return out, lse
+
+
+def packed_attention_bwd(pack: PackedRows, q, k, v, o, do, lse, n_q: int, n_kv: int, head_dim: int,
+                         scale: float | None = None, out=None, stream=None):
+    """Gradients (dq, dk, dv) of packed_attention_fwd with respect to q, k and v, from its
+    outputs o and lse and do = dL/do.  out: (dq, dk, dv) to write to, for instance column
+    slices of one buffer."""
+    pack = _need_pack(pack)
+    heads = _heads(n_q, n_kv, head_dim, scale)
+    rows, qd, kvd = pack.total, n_q * head_dim, n_kv * head_dim
+    ld_q, ld_k, ld_v = _rows2d(q, "q", rows, qd), _rows2d(k, "k", rows, kvd), _rows2d(v, "v", rows, kvd)
+    ld_o, ld_do = _rows2d(o, "o", rows, qd), _rows2d(do, "do", rows, qd)
+    _need(lse, "lse", torch.float32, n_q * rows)
+    dq, dk, dv = out if out is not None else (None, None, None)
+    if out is not None:
+        ld_dq, ld_dk, ld_dv = _rows2d(dq, "dq", rows, qd), _rows2d(dk, "dk", rows, kvd), _rows2d(dv, "dv", rows, kvd)
+        if any(_overlap(a, b) for a in out for b in (q, k, v, o, do)) or _overlap(dq, dk) or _overlap(dq, dv) or \
+                _overlap(dk, dv):
+            raise ValueError("out: overlaps an input or another output")
+    with _On(pack.device, stream, q=q, k=k, v=v, o=o, do=do, lse=lse, dq=dq, dk=dk, dv=dv) as s:
+        if out is None:
+            dq, dk, dv = (torch.empty(rows, w, dtype=torch.bfloat16, device=pack.device) for w in (qd, kvd, kvd))
+            ld_dq, ld_dk, ld_dv = qd, kvd, kvd
+        if rows:
+            nb = B.lib().nf4ls_packed_attention_ws_bytes(pack._ref, ctypes.byref(heads))
+            ws = _buffer(nb, pack.device)
+            t = B.PackedAttention(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                  do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ld_q, ld_k, ld_v, ld_o,
+                                  ld_do, ld_dq, ld_dk, ld_dv)
+            B.call("nf4ls_packed_attention_bwd", pack._ref, ctypes.byref(heads), ctypes.byref(t), _p(ws), nb, s)
+    return dq, dk, dv
+
+
 # ----------------------------------------------------------------------------- streaming pool
 
 class Pool:

@@ -74,6 +74,23 @@ class DiskInfo(ctypes.Structure):
                 ("rotational", ctypes.c_int32), ("direct_io", ctypes.c_int32)]
 
 
+class Pack(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("total", ctypes.c_int32), ("n_tiles", ctypes.c_int32),
+                ("max_len", ctypes.c_int32), ("off_cu", ctypes.c_uint64), ("off_positions", ctypes.c_uint64),
+                ("off_seq", ctypes.c_uint64), ("off_query_tiles", ctypes.c_uint64),
+                ("off_key_tiles", ctypes.c_uint64), ("plan_bytes", ctypes.c_uint64), ("plan_dev", ctypes.c_void_p)]
+
+
+class PackedHeads(ctypes.Structure):
+    _fields_ = [("n_q", ctypes.c_int32), ("n_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class PackedAttention(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "lse", "d_o", "dq", "dk", "dv")] + \
+               [("ld_" + n, ctypes.c_int32) for n in ("q", "k", "v", "o", "do", "dq", "dk", "dv")]
+
+
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
 SZ = ctypes.c_size_t
@@ -150,6 +167,13 @@ SIGNATURES = {
     "nf4ls_attention_fwd": (ctypes.c_int, [ctypes.POINTER(LayerCfg), P, P, P, ctypes.c_int, ctypes.c_int, P, P, P]),
     "nf4ls_attention_bwd": (ctypes.c_int, [ctypes.POINTER(LayerCfg), P, P, P, ctypes.c_int, ctypes.c_int, P, P, P, P,
                                            P, P, P, P]),
+    "nf4ls_pack_layout": (ctypes.c_int, [P, I32, ctypes.POINTER(Pack)]),
+    "nf4ls_pack_fill": (ctypes.c_int, [P, ctypes.POINTER(Pack), P, SZ]),
+    "nf4ls_packed_attention_ws_bytes": (SZ, [ctypes.POINTER(Pack), ctypes.POINTER(PackedHeads)]),
+    "nf4ls_packed_attention_fwd": (ctypes.c_int, [ctypes.POINTER(Pack), ctypes.POINTER(PackedHeads),
+                                                  ctypes.POINTER(PackedAttention), P]),
+    "nf4ls_packed_attention_bwd": (ctypes.c_int, [ctypes.POINTER(Pack), ctypes.POINTER(PackedHeads),
+                                                  ctypes.POINTER(PackedAttention), P, SZ, P]),
 }
 
 _LIB = None

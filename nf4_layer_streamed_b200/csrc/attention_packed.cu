@@ -1,0 +1,1010 @@
+// Causal grouped-query attention over a packed batch (forward and gradients) on the
+// 5th-generation tensor cores: the sequences lie one behind the other and have any length.
+#include <cstring>
+
+#include "attention_tile.cuh"
+#include "common.cuh"
+#include "internal.h"
+
+namespace nf4ls {
+
+namespace {
+
+struct FwdParams {
+  CUtensorMap tq, tk, tv, to;  // [total, cols] bf16, box 64 cols x 128 rows, 128-byte swizzle (to: output)
+  const PackTile* tiles;
+  __nv_bfloat16* o;
+  float* lse;
+  int ldo, total, nq, nkv;
+  float scale_log2;
+  int* err;
+};
+
+struct BwdParams {
+  CUtensorMap tq, tk, tv, tdo, to;  // inputs (to: the output O of the forward)
+  CUtensorMap tdq, tdk, tdv;        // the gradients, same boxes (TMA stores)
+  const PackTile* tiles;            // query tiles or key tiles, most work first
+  const float* lse;
+  float* stats;  // [nq, n_tiles, 2, 128]: lse log2(e) and delta, by the query side for the key side
+  __nv_bfloat16 *dq, *dk, *dv;
+  int ld_dq, ld_dk, ld_dv, total, n_tiles, nq, nkv;
+  float scale, scale_log2;
+  int* err;
+};
+
+// Zeros row r of a tile of NA 64-dim atoms (a whole row is the same under any swizzle).
+template <int NA>
+__device__ __forceinline__ void zero_row(uint32_t tile, int r) {
+#pragma unroll
+  for (int j = 0; j < NA; ++j)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) st_shared_v4(tile + j * ATOM + r * 128 + c * 16, 0u, 0u, 0u, 0u);
+}
+
+// The staged tile at `tile` to rows row .. row + n_rows - 1 and columns col .. col + D - 1 of
+// the output: one TMA store per atom where the tile is whole, else 16 bytes a thread, so
+// that the rows behind the sequence's end stay as they are.  All `threads` threads call.
+template <int D>
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, __nv_bfloat16* out, int ld, uint32_t tile, int row,
+                                           int col, int n_rows, int tid, int threads) {
+  if (n_rows == TT) {
+    if (tid == 0) {
+      for (int j = 0; j < D / 64; ++j) tma_store_2d(map, tile + j * ATOM, col + 64 * j, row);
+      tma_store_drain();
+    }
+    return;
+  }
+  for (int i = tid; i < n_rows * (D / 8); i += threads) {
+    const int r = i / (D / 8), c = i % (D / 8);
+    const uint4 v = ld_shared_v4(tile + (c >> 3) * ATOM + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    *reinterpret_cast<uint4*>(out + (size_t)(row + r) * ld + col + c * 8) = v;
+  }
+}
+
+// warps 0-3: softmax and epilogue (warp w owns TMEM lanes 32 w .. 32 w + 31, one query
+// row per thread); warp 4: TMA producer; warp 5: MMA issuer
+constexpr int F_THREADS = 192, F_PROD = 4, F_MMA = 5;
+constexpr int F_OFF_Q = 0, F_OFF_K = TILE_BYTES, F_OFF_V = 2 * TILE_BYTES, F_OFF_BAR = 3 * TILE_BYTES;
+constexpr int SMEM_TC = 1024 + F_OFF_BAR + 128;
+constexpr float kRescaleLog2 = 8.0f;  // the reference maximum may trail the true one by this much
+
+template <int D>
+__global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_constant__ FwdParams p) {
+  constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM;  // swizzle atoms, k-steps and bytes of a tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + F_OFF_BAR);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = bars + 1;
+  uint64_t* k_empty = bars + 2;
+  uint64_t* v_full = bars + 3;
+  uint64_t* v_empty = bars + 4;
+  uint64_t* s_full = bars + 5;
+  uint64_t* p_full = bars + 6;
+  uint64_t* o_full = bars + 7;   // one phase per key tile: the P V product of that tile is done
+  uint64_t* drain = bars + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 9);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // heads fastest, then the plan's tiles, most key tiles first
+  const int h = blockIdx.x % p.nq;
+  const PackTile pt = p.tiles[blockIdx.x / p.nq];
+  const int qt = pt.tile, row0 = pt.row0;
+  const int n_rows = min(TT, pt.len - qt * TT);  // rows of this tile (keys of the diagonal tile)
+  const int kvh = h / (p.nq / p.nkv);
+  const int nk = qt + 1;  // key tiles at or before the diagonal
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(k_full, 1);
+    mbar_init(k_empty, 1);
+    mbar_init(v_full, 1);
+    mbar_init(v_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, 4);
+    mbar_init(o_full, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == F_MMA) {
+    tmem_alloc(tmem_slot, 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // [0, 128) S then P, [128, 256) O
+
+  if (warp == F_PROD) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      tma_prefetch_desc(&p.tq);
+      tma_prefetch_desc(&p.tk);
+      tma_prefetch_desc(&p.tv);
+      mbar_arrive_expect_tx(q_full, TB);
+      for (int j = 0; j < NA; ++j) tma_load_2d(base + F_OFF_Q + j * ATOM, &p.tq, q_full, h * D + 64 * j, row0 + qt * TT);
+      int issued_k = 0, issued_v = 0;
+      for (int kt = 0; kt < nk; ++kt) {
+        if (kt > 0 && !mbar_wait(k_empty, (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 21)) break;
+        mbar_arrive_expect_tx(k_full, TB);
+        for (int j = 0; j < NA; ++j)
+          tma_load_2d(base + F_OFF_K + j * ATOM, &p.tk, k_full, kvh * D + 64 * j, row0 + kt * TT);
+        issued_k = kt + 1;
+        if (kt > 0 && !mbar_wait(v_empty, (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 22)) break;
+        mbar_arrive_expect_tx(v_full, TB);
+        for (int j = 0; j < NA; ++j)
+          tma_load_2d(base + F_OFF_V + j * ATOM, &p.tv, v_full, kvh * D + 64 * j, row0 + kt * TT);
+        issued_v = kt + 1;
+      }
+      if (*abort_flag) {  // let the copies already issued land before the CTA exits
+        mbar_wait_drain(q_full, 0);
+        if (issued_k > 0) mbar_wait_drain(k_full, (issued_k - 1) & 1);
+        if (issued_v > 0) mbar_wait_drain(v_full, (issued_v - 1) & 1);
+      }
+    }
+  } else if (warp == F_MMA) {
+    // ------------------------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc_s = idesc_bf16(128, 128, false);  // Q K^T: both K-major
+    constexpr uint32_t idesc_o = idesc_bf16(128, D, true);     // P V: V N-major
+    const uint32_t sQ = smem_u32(base + F_OFF_Q), sK = smem_u32(base + F_OFF_K), sV = smem_u32(base + F_OFF_V);
+    // every wait is agreed on by the whole warp (__all_sync), so that no lane goes on alone
+    bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag, p.err, KID_PACKED, 23));
+    for (int kt = 0; ok && kt < nk; ++kt) {
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(k_full, kt & 1, abort_flag, p.err, KID_PACKED, 24)))) break;
+      tc_fence_after();
+      if (lane == 0) {
+        // tcgen05.mma of one thread run in issue order, so S may overwrite the P that
+        // the previous tile's P V product reads
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t off = (ks >> 2) * ATOM + (ks & 3) * 32;
+          umma_bf16(tmem, sdesc_sw128(sQ + off, 16, 1024), sdesc_sw128(sK + off, 16, 1024), idesc_s, ks ? 1u : 0u);
+        }
+        umma_commit(s_full);
+        umma_commit(k_empty);
+      }
+      __syncwarp();
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(p_full, kt & 1, abort_flag, p.err, KID_PACKED, 25)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(v_full, kt & 1, abort_flag, p.err, KID_PACKED, 26)))) break;
+      tc_fence_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)  // 16 keys per step: P columns 8 ks .., V rows 16 ks ..
+          umma_bf16_ta(tmem + 128, tmem + ks * 8, sdesc_sw128(sV + ks * 2048, ATOM, 1024), idesc_o,
+                       (kt | ks) ? 1u : 0u);
+        umma_commit(v_empty);
+        umma_commit(o_full);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax + epilogue
+    const int r = warp * 32 + lane;  // query row in the tile = TMEM lane
+    const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+    const float sl = p.scale_log2;
+    float m_run = -INFINITY, l_run = 0.f;
+    bool ok = true;
+    for (int kt = 0; kt < nk; ++kt) {
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full, kt & 1, abort_flag, p.err, KID_PACKED, 27)))) break;
+      tc_fence_after();
+      const bool diag = kt == qt;
+      // the row of scores, held in registers; masked ones (on the diagonal tile, which is
+      // also the only one that the sequence may end in) become -inf whatever they were
+      uint32_t v[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(trow + c * 32, v[c]);
+      tmem_wait_ld();
+      if (diag) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[c][i] = c * 32 + i <= r ? v[c][i] : 0xFF800000u;
+      }
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // independent chains
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(v[c][i + e]), __uint_as_float(v[c][i + 4 + e])));
+      float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      mx *= sl;
+      const float m_new = (kt == 0 || mx > m_run + kRescaleLog2) ? fmaxf(mx, m_run) : m_run;
+      const bool resc = kt > 0 && m_new != m_run;
+      if (__any_sync(0xffffffffu, resc)) {
+        // the previous tile's P V product must be in O before O is scaled
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(o_full, (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 28)))) break;
+        tc_fence_after();
+        const float alpha = resc ? fast_exp2(m_run - m_new) : 1.0f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {  // 16 columns at a time: the scores hold the registers
+          uint32_t o[16];
+          tmem_ld16(trow + 128 + c * 16, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st16(trow + 128 + c * 16, o);
+        }
+        tmem_wait_st();
+        l_run *= alpha;
+      }
+      m_run = m_new;
+      float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float p0 = fast_exp2(fmaf(__uint_as_float(v[c][2 * j]), sl, -m_run));
+          const float p1 = fast_exp2(fmaf(__uint_as_float(v[c][2 * j + 1]), sl, -m_run));
+          s4[2 * (j & 1)] += p0;
+          s4[2 * (j & 1) + 1] += p1;
+          pk[j] = pack_bf16x2(p0, p1);
+        }
+        tmem_st16(trow + c * 16, pk);
+      }
+      if (diag && n_rows < TT) {
+        // rows of V behind the sequence's end belong to others: zeros, so that a
+        // non-finite value there times a probability of 0 stays out of O
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(v_full, kt & 1, abort_flag, p.err, KID_PACKED, 30)))) break;
+        if (r >= n_rows) zero_row<NA>(smem_u32(base + F_OFF_V), r);
+        fence_proxy_async_smem();
+      }
+      tmem_wait_st();
+      l_run += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+    }
+    // O / sum through the freed Q tile's shared memory and two TMA stores (coalesced rows);
+    // all four warps reach the barrier, the store is issued only when no wait failed
+    if (ok && __all_sync(0xffffffffu, mbar_wait(o_full, (nk - 1) & 1, abort_flag, p.err, KID_PACKED, 29))) {
+      tc_fence_after();
+      const float inv = 1.0f / l_run;
+      const uint32_t tile = smem_u32(base + F_OFF_Q);
+#pragma unroll
+      for (int c = 0; c < D / 32; c += 2) {
+        uint32_t v[2][32];
+        tmem_ld32(trow + 128 + c * 32, v[0]);
+        tmem_ld32(trow + 128 + c * 32 + 32, v[1]);
+        tmem_wait_ld();
+        stage_row32(tile, r, c, v[0], inv);
+        stage_row32(tile, r, c + 1, v[1], inv);
+      }
+      if (r < n_rows)
+        p.lse[(size_t)h * p.total + row0 + qt * TT + r] = (m_run + log2f(l_run)) * 0.6931471805599453f;
+    }
+    fence_proxy_async_smem();
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (!*abort_flag)
+      store_tile<D>(&p.to, p.o, p.ldo, smem_u32(base + F_OFF_Q), row0 + qt * TT, h * D, n_rows, threadIdx.x, 128);
+  }
+
+  // On an aborted run the products already issued must finish before TMEM is freed.
+  __syncthreads();
+  if (warp == F_MMA && *abort_flag) {
+    if (lane == 0) umma_commit(drain);
+    __syncwarp();
+    mbar_wait_drain(drain, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == F_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// ------------------------------------------------------------------------------ backward
+// warps 0-7: elementwise and epilogue (warp w: TMEM lane quarter w % 4, column half
+// w / 4); warp 8: TMA producer; warp 9: MMA issuer
+constexpr int B_THREADS = 320, B_PROD = 8, B_MMA = 9, B_EW = 256;
+constexpr int B_OFF_A = 0;                              // Q, dO (query side) or K, V (key side)
+constexpr int B_OFF_RING = 2 * TILE_BYTES;              // 2 stages x (two 32 KB tiles)
+constexpr int B_OFF_X = B_OFF_RING + 4 * TILE_BYTES;    // query side: O tile and delta halves [2][128];
+                                                        // key side: 2 stages x (128 lse + 128 delta floats)
+constexpr int B_OFF_BAR = B_OFF_X + TILE_BYTES + 1024;
+constexpr int SMEM_BWD = 1024 + B_OFF_BAR + 256;
+
+__device__ __forceinline__ void bar_ew() { asm volatile("bar.sync 1, %0;" ::"n"(B_EW) : "memory"); }
+
+template <int D>
+__global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constant__ BwdParams p) {
+  // swizzle atoms, k-steps and bytes of a Q / dO / O / K / V tile; dims per column half
+  constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM, DH = D / 2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + B_OFF_BAR);
+  uint64_t* q_full = bars;          // Q, dO (copied into TMEM first)
+  uint64_t* kv_full = bars + 1;     // 2 stages
+  uint64_t* kv_empty = bars + 3;    // 2
+  uint64_t* sd_full = bars + 5;     // S and dP of the item are in TMEM
+  uint64_t* p_half = bars + 6;      // 2: dS chunk hc of the item is in TMEM (one arrival per warp)
+  uint64_t* acc_full = bars + 9;
+  uint64_t* drain = bars + 10;
+  uint64_t* qa_full = bars + 11;    // Q and dO are in TMEM (one arrival per elementwise warp)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 12);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint64_t* o_full = bars + 13;     // the O tile (for delta)
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.x % p.nq;
+  const PackTile pt = p.tiles[blockIdx.x / p.nq];
+  const int qt = pt.tile, row0 = pt.row0;
+  const int n_rows = min(TT, pt.len - qt * TT);
+  const int kvh = h / (p.nq / p.nkv);
+  const int n_kt = qt + 1;  // key tiles at or before the diagonal
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(o_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    mbar_init(sd_full, 1);
+    mbar_init(&p_half[0], B_EW / 32);
+    mbar_init(&p_half[1], B_EW / 32);
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    mbar_init(qa_full, B_EW / 32);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == B_MMA) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // S [0,128), dP [128,256) (dS packed over it), dQ [256,384), Q [384,448), dO [448,512)
+  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t T_Q = 384, T_DO = 448;
+
+  if (warp == B_PROD) {
+    if (lane == 0) {
+      tma_prefetch_desc(&p.tq);
+      tma_prefetch_desc(&p.tk);
+      tma_prefetch_desc(&p.tv);
+      tma_prefetch_desc(&p.tdo);
+      tma_prefetch_desc(&p.to);
+      mbar_arrive_expect_tx(q_full, 2 * TB);
+      for (int j = 0; j < NA; ++j) {
+        tma_load_2d(base + B_OFF_A + j * ATOM, &p.tq, q_full, h * D + 64 * j, row0 + qt * TT);
+        tma_load_2d(base + B_OFF_A + TILE_BYTES + j * ATOM, &p.tdo, q_full, h * D + 64 * j, row0 + qt * TT);
+      }
+      mbar_arrive_expect_tx(o_full, TB);
+      for (int j = 0; j < NA; ++j)
+        tma_load_2d(base + B_OFF_X + j * ATOM, &p.to, o_full, h * D + 64 * j, row0 + qt * TT);
+      int issued = 0;
+      for (int kt = 0; kt < n_kt; ++kt) {
+        const int st = kt & 1;
+        if (kt >= 2 && !mbar_wait(&kv_empty[st], ((kt >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 41)) break;
+        uint8_t* buf = base + B_OFF_RING + st * 2 * TILE_BYTES;
+        mbar_arrive_expect_tx(&kv_full[st], 2 * TB);
+        for (int j = 0; j < NA; ++j) {
+          tma_load_2d(buf + j * ATOM, &p.tk, &kv_full[st], kvh * D + 64 * j, row0 + kt * TT);
+          tma_load_2d(buf + TILE_BYTES + j * ATOM, &p.tv, &kv_full[st], kvh * D + 64 * j, row0 + kt * TT);
+        }
+        issued = kt + 1;
+      }
+      if (*abort_flag) {  // let the copies already issued land before the CTA exits
+        mbar_wait_drain(q_full, 0);
+        mbar_wait_drain(o_full, 0);
+        for (int kt = (issued > 2 ? issued - 2 : 0); kt < issued; ++kt) mbar_wait_drain(&kv_full[kt & 1], (kt >> 1) & 1);
+      }
+    }
+  } else if (warp == B_MMA) {
+    constexpr uint32_t idesc_s = idesc_bf16(128, 128, false);  // S, dP: N = 128 keys
+    constexpr uint32_t idesc_a = idesc_bf16(128, D, true);     // dQ += dS K: K N-major
+    bool ok = __all_sync(0xffffffffu, mbar_wait(qa_full, 0, abort_flag, p.err, KID_PACKED, 42)) && !*abort_flag;
+    // dQ += dS_kt K_kt, each half as soon as its dS chunks are in TMEM (chunk hc holds the
+    // k-steps with ks & 2 == 2 hc); then the K/V stage is free
+    auto dq_product = [&](int kt) -> bool {
+      const uint32_t sK = smem_u32(base + B_OFF_RING + (kt & 1) * 2 * TILE_BYTES);
+      for (int hc = 0; hc < 2; ++hc) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&p_half[hc], kt & 1, abort_flag, p.err, KID_PACKED, 44))) return false;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // 16 keys per step
+            const int ks = (i >> 1) * 4 + hc * 2 + (i & 1);
+            umma_bf16_ta(tmem + 256, tmem + packed_col(128, ks), sdesc_sw128(sK + ks * 2048, ATOM, 1024), idesc_a,
+                         (kt | hc | i) ? 1u : 0u);
+          }
+          if (hc == 1) umma_commit(&kv_empty[kt & 1]);
+        }
+        __syncwarp();
+      }
+      return true;
+    };
+    for (int kt = 0; ok && kt < n_kt; ++kt) {
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[kt & 1], (kt >> 1) & 1, abort_flag, p.err, KID_PACKED,
+                                                   43))))
+        break;
+      // the previous item's dS is read (issue order) before S and dP overwrite it
+      if (kt >= 1 && !(ok = dq_product(kt - 1))) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t sK = smem_u32(base + B_OFF_RING + (kt & 1) * 2 * TILE_BYTES), sV = sK + TILE_BYTES;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {  // over the head dim: Q, dO columns 8 ks .. in TMEM
+          const uint32_t off = (ks >> 2) * ATOM + (ks & 3) * 32;
+          umma_bf16_ta(tmem, tmem + T_Q + ks * 8, sdesc_sw128(sK + off, 16, 1024), idesc_s, ks ? 1u : 0u);
+          umma_bf16_ta(tmem + 128, tmem + T_DO + ks * 8, sdesc_sw128(sV + off, 16, 1024), idesc_s, ks ? 1u : 0u);
+        }
+        umma_commit(sd_full);
+      }
+      __syncwarp();
+    }
+    if (ok) ok = dq_product(n_kt - 1);
+    if (ok && lane == 0) umma_commit(acc_full);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ elementwise + epilogue
+    const int wq = warp & 3, g = warp >> 2;
+    const int r = wq * 32 + lane;  // query row = TMEM lane
+    const int qpos = qt * TT + r;
+    const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
+    // First Q and dO into TMEM (the MMA warp starts on them), then delta = rowsum(dO * O)
+    // over this thread's DH dims (dims g DH .. of its row: 16-byte chunks c0 + c of swizzle
+    // atom g DH / 64 of the dO and O tiles), the two halves added through smem.  TMEM
+    // column g DH / 2 + 4 c + i holds the pair i of chunk c.
+    float* red = reinterpret_cast<float*>(base + B_OFF_X + TILE_BYTES);
+    const int atom = (g * DH) / 64, c0 = ((g * DH) % 64) / 8;
+    const uint8_t* q_row = base + B_OFF_A + atom * ATOM + r * 128;
+    const uint8_t* dO_row = base + B_OFF_A + TILE_BYTES + atom * ATOM + r * 128;
+    const uint8_t* o_row = base + B_OFF_X + atom * ATOM + r * 128;
+    bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag, p.err, KID_PACKED, 45));
+    if (ok) {
+      uint32_t qv[DH / 2], dv[DH / 2];
+#pragma unroll
+      for (int c = 0; c < DH / 8; ++c) {
+        const uint32_t off = (uint32_t)(((c0 + c) ^ (r & 7)) << 4);
+        const uint4 d = *reinterpret_cast<const uint4*>(dO_row + off);
+        const uint4 q = *reinterpret_cast<const uint4*>(q_row + off);
+        qv[4 * c] = q.x, qv[4 * c + 1] = q.y, qv[4 * c + 2] = q.z, qv[4 * c + 3] = q.w;
+        dv[4 * c] = d.x, dv[4 * c + 1] = d.y, dv[4 * c + 2] = d.z, dv[4 * c + 3] = d.w;
+      }
+      tmem_st_cols(trow + T_Q + g * (DH / 2), qv);
+      tmem_st_cols(trow + T_DO + g * (DH / 2), dv);
+      tmem_wait_st();
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(qa_full);  // also on failure: the MMA warp then sees the abort
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_full, 0, abort_flag, p.err, KID_PACKED, 48));
+    if (ok) {
+      float s = 0.f;
+#pragma unroll
+      for (int c = 0; c < DH / 8; ++c) {
+        const uint32_t off = (uint32_t)(((c0 + c) ^ (r & 7)) << 4);
+        const uint4 a = *reinterpret_cast<const uint4*>(o_row + off);
+        const uint4 d = *reinterpret_cast<const uint4*>(dO_row + off);
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, dw[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s += bf16_lo(aw[j]) * bf16_lo(dw[j]) + bf16_hi(aw[j]) * bf16_hi(dw[j]);
+      }
+      red[g * 128 + r] = s;
+    }
+    bar_ew();
+    const float dl = ok ? red[r] + red[128 + r] : 0.f;
+    // rows behind the sequence's end: no lse to read; their lanes compute values that
+    // nothing stores
+    const float lse2 = r < n_rows ? p.lse[(size_t)h * p.total + row0 + qpos] * 1.4426950408889634f : 0.f;
+    if (ok && g == 0) {
+      float* st = p.stats + ((size_t)h * p.n_tiles + pt.index) * (2 * TT);
+      st[r] = lse2;
+      st[TT + r] = dl;
+    }
+    const float sl = p.scale_log2;
+    for (int kt = 0; ok && kt < n_kt; ++kt) {
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(sd_full, kt & 1, abort_flag, p.err, KID_PACKED, 46)))) break;
+      tc_fence_after();
+      const bool diag = kt == qt;
+      if (diag && n_rows < TT) {
+        // rows of K behind the sequence's end: zeros for the product dS K (S is done with them)
+        if (r >= n_rows && g == 0) zero_row<NA>(smem_u32(base + B_OFF_RING + (kt & 1) * 2 * TILE_BYTES), r);
+        fence_proxy_async_smem();
+      }
+      // both 32-key chunks in one TMEM round trip
+      uint32_t sv[2][32], dpv[2][32];
+#pragma unroll
+      for (int hc = 0; hc < 2; ++hc) {
+        tmem_ld32(trow + g * 64 + hc * 32, sv[hc]);
+        tmem_ld32(trow + 128 + g * 64 + hc * 32, dpv[hc]);
+      }
+      tmem_wait_ld();
+#pragma unroll
+      for (int hc = 0; hc < 2; ++hc) {  // keys 64 g + 32 hc .. of the tile
+        uint32_t dd[16];
+        const int last = diag ? r - (g * 64 + hc * 32) : 32;  // columns c <= last are not masked
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float ds[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int c = 2 * j + e;
+            const float pe = fast_exp2(fmaf(__uint_as_float(sv[hc][c]), sl, -lse2));
+            ds[e] = c <= last ? pe * (__uint_as_float(dpv[hc][c]) - dl) : 0.f;
+          }
+          dd[j] = pack_bf16x2(ds[0], ds[1]);
+        }
+        tmem_st16(trow + 128 + g * 64 + hc * 16, dd);  // over dP values this warp has read
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_half[hc]);
+      }
+    }
+    // dQ through the freed ring's shared memory and two TMA stores (coalesced rows); every
+    // elementwise warp reaches the barrier, the store is issued only when no wait failed
+    if (ok && __all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag, p.err, KID_PACKED, 47))) {
+      tc_fence_after();
+      uint32_t v[DH / 32][32];
+#pragma unroll
+      for (int i = 0; i < DH / 32; ++i) tmem_ld32(trow + 256 + g * DH + 32 * i, v[i]);
+      tmem_wait_ld();
+      const uint32_t tile = smem_u32(base + B_OFF_RING);
+#pragma unroll
+      for (int i = 0; i < DH / 32; ++i) stage_row32(tile, r, g * (DH / 32) + i, v[i], p.scale);
+    }
+    fence_proxy_async_smem();
+    bar_ew();
+    if (!*abort_flag)
+      store_tile<D>(&p.tdq, p.dq, p.ld_dq, smem_u32(base + B_OFF_RING), row0 + qt * TT, h * D, n_rows, threadIdx.x,
+                    B_EW);
+  }
+  __syncthreads();
+  if (warp == B_MMA && *abort_flag) {  // products already issued finish before TMEM is freed
+    if (lane == 0) umma_commit(drain);
+    __syncwarp();
+    mbar_wait_drain(drain, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == B_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
+    k_packed_dkv(const __grid_constant__ BwdParams p) {
+  // swizzle atoms, k-steps and bytes of a K / V / Q / dO tile; dims per column half
+  constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM, DH = D / 2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + B_OFF_BAR);
+  uint64_t* kv_full = bars;         // K, V
+  uint64_t* qd_full = bars + 1;     // 2 stages (Q, dO, lse, delta of one (head, query tile))
+  uint64_t* qd_empty = bars + 3;    // 2
+  uint64_t* sd_full = bars + 5;     // S^T and dP^T of the item are in TMEM
+  uint64_t* p_half = bars + 6;      // 2: P^T, dS^T chunk hc of the item are in TMEM (one arrival per warp)
+  uint64_t* acc_full = bars + 9;
+  uint64_t* drain = bars + 10;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 11);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint64_t* peer_full = bars + 12;  // the peer CTA's partial sums of this CTA's tensor have landed
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int item = blockIdx.x >> 1, kvh = item % p.nkv;
+  const PackTile pt = p.tiles[item / p.nkv];
+  const int kt = pt.tile, row0 = pt.row0;
+  const int n_keys = min(TT, pt.len - kt * TT);
+  const uint32_t crank = cluster_ctarank();
+  const int grp = p.nq / p.nkv, n_qt = (pt.len + TT - 1) / TT;
+  const int hpc = (grp + 1) / 2, h_begin = (int)crank * hpc, h_count = min(grp, h_begin + hpc) - h_begin;
+  // (head, query tile) items of this CTA
+  const int per_head = n_qt - kt, n_st = h_count * per_head;
+  const int n_last = pt.len - (n_qt - 1) * TT;  // rows of the sequence's last query tile
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&qd_full[i], 1);
+      mbar_init(&qd_empty[i], 1);
+    }
+    mbar_init(sd_full, 1);
+    mbar_init(&p_half[0], B_EW / 32);
+    mbar_init(&p_half[1], B_EW / 32);
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    mbar_init(peer_full, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == B_MMA) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // S^T [0,128), dP^T [128,256) (P^T, dS^T packed over them), dV, dK
+
+  if (warp == B_PROD) {
+    if (lane == 0) {
+      tma_prefetch_desc(&p.tq);
+      tma_prefetch_desc(&p.tk);
+      tma_prefetch_desc(&p.tv);
+      tma_prefetch_desc(&p.tdo);
+      mbar_arrive_expect_tx(kv_full, 2 * TB);
+      for (int j = 0; j < NA; ++j) {
+        tma_load_2d(base + B_OFF_A + j * ATOM, &p.tk, kv_full, kvh * D + 64 * j, row0 + kt * TT);
+        tma_load_2d(base + B_OFF_A + TILE_BYTES + j * ATOM, &p.tv, kv_full, kvh * D + 64 * j, row0 + kt * TT);
+      }
+      int issued = 0;
+      for (int sti = 0; sti < n_st; ++sti) {
+        const int bf = sti & 1;
+        if (sti >= 2 && !mbar_wait(&qd_empty[bf], ((sti >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 31)) break;
+        const int h = kvh * grp + h_begin + sti / per_head, qt = kt + sti % per_head;
+        uint8_t* buf = base + B_OFF_RING + bf * 2 * TILE_BYTES;
+        float* ld = reinterpret_cast<float*>(base + B_OFF_X + bf * 1024);
+        mbar_arrive_expect_tx(&qd_full[bf], 2 * TB + 1024);
+        for (int j = 0; j < NA; ++j) {
+          tma_load_2d(buf + j * ATOM, &p.tq, &qd_full[bf], h * D + 64 * j, row0 + qt * TT);
+          tma_load_2d(buf + TILE_BYTES + j * ATOM, &p.tdo, &qd_full[bf], h * D + 64 * j, row0 + qt * TT);
+        }
+        bulk_load(ld, p.stats + ((size_t)h * p.n_tiles + pt.index - kt + qt) * (2 * TT), 1024, &qd_full[bf]);
+        issued = sti + 1;
+      }
+      if (*abort_flag) {  // let the copies already issued land before the CTA exits
+        mbar_wait_drain(kv_full, 0);
+        for (int i = (issued > 2 ? issued - 2 : 0); i < issued; ++i) mbar_wait_drain(&qd_full[i & 1], (i >> 1) & 1);
+      }
+    }
+  } else if (warp == B_MMA) {
+    constexpr uint32_t idesc_s = idesc_bf16(128, 128, false);  // S^T, dP^T: N = 128 queries
+    constexpr uint32_t idesc_a = idesc_bf16(128, D, true);     // dV, dK: dO, Q N-major
+    const uint32_t sK = smem_u32(base + B_OFF_A), sV = sK + TILE_BYTES;
+    bool ok = n_st > 0 && __all_sync(0xffffffffu, mbar_wait(kv_full, 0, abort_flag, p.err, KID_PACKED, 32));
+    // dV += P^T dO, dK += dS^T Q, each half as soon as its chunks are in TMEM (chunk hc holds
+    // the k-steps with ks & 2 == 2 hc); then the stage is free
+    auto kv_products = [&](int sti) -> bool {
+      const uint32_t sQ = smem_u32(base + B_OFF_RING + (sti & 1) * 2 * TILE_BYTES), sO = sQ + TILE_BYTES;
+      for (int hc = 0; hc < 2; ++hc) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&p_half[hc], sti & 1, abort_flag, p.err, KID_PACKED, 34))) return false;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // 16 queries per step
+            const int ks = (i >> 1) * 4 + hc * 2 + (i & 1);
+            const uint32_t acc = (sti | hc | i) ? 1u : 0u;
+            umma_bf16_ta(tmem + 256, tmem + packed_col(0, ks), sdesc_sw128(sO + ks * 2048, ATOM, 1024), idesc_a, acc);
+            umma_bf16_ta(tmem + 384, tmem + packed_col(128, ks), sdesc_sw128(sQ + ks * 2048, ATOM, 1024), idesc_a,
+                         acc);
+          }
+          if (hc == 1) umma_commit(&qd_empty[sti & 1]);
+        }
+        __syncwarp();
+      }
+      return true;
+    };
+    for (int sti = 0; ok && sti < n_st; ++sti) {
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&qd_full[sti & 1], (sti >> 1) & 1, abort_flag, p.err, KID_PACKED,
+                                                   33))))
+        break;
+      // the previous item's P^T and dS^T are read (issue order) before S^T, dP^T overwrite them
+      if (sti >= 1 && !(ok = kv_products(sti - 1))) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t sQ = smem_u32(base + B_OFF_RING + (sti & 1) * 2 * TILE_BYTES), sO = sQ + TILE_BYTES;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {  // S^T = K Q^T, dP^T = V dO^T over the head dim
+          const uint32_t off = (ks >> 2) * ATOM + (ks & 3) * 32;
+          umma_bf16(tmem, sdesc_sw128(sK + off, 16, 1024), sdesc_sw128(sQ + off, 16, 1024), idesc_s, ks ? 1u : 0u);
+          umma_bf16(tmem + 128, sdesc_sw128(sV + off, 16, 1024), sdesc_sw128(sO + off, 16, 1024), idesc_s,
+                    ks ? 1u : 0u);
+        }
+        umma_commit(sd_full);
+      }
+      __syncwarp();
+    }
+    if (ok) ok = kv_products(n_st - 1);
+    if (ok && lane == 0) umma_commit(acc_full);
+    __syncwarp();
+  } else {
+    const int wq = warp & 3, g = warp >> 2;
+    const int r = wq * 32 + lane;  // key row = TMEM lane
+    const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
+    const float sl = p.scale_log2;
+    bool ok = true;
+    for (int sti = 0; sti < n_st; ++sti) {
+      const int qt = kt + sti % per_head;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(sd_full, sti & 1, abort_flag, p.err, KID_PACKED, 35)))) break;
+      tc_fence_after();
+      const bool diag = qt == kt, ragged = qt == n_qt - 1 && n_last < TT;
+      if (ragged) {
+        // rows of Q and dO behind the sequence's end: zeros for the products dS^T Q and P^T dO
+        // (S^T and dP^T are done with them)
+        if (r >= n_last) zero_row<NA>(smem_u32(base + B_OFF_RING + (sti & 1) * 2 * TILE_BYTES + g * TILE_BYTES), r);
+        fence_proxy_async_smem();
+      }
+      const float* ld = reinterpret_cast<const float*>(base + B_OFF_X + (sti & 1) * 1024);
+#pragma unroll
+      for (int hc = 0; hc < 2; ++hc) {  // queries 64 g + 32 hc .. of the tile
+        uint32_t sv[32], dpv[32], pp[16], dd[16];
+        tmem_ld32(trow + g * 64 + hc * 32, sv);
+        tmem_ld32(trow + 128 + g * 64 + hc * 32, dpv);
+        tmem_wait_ld();
+        const int qi0 = g * 64 + hc * 32;     // query within the tile
+        const int lo = diag ? r - qi0 : 0;             // columns c < lo (queries before the key) are masked,
+        const int hi = ragged ? n_last - qi0 : 32;     // and those from hi on (behind the sequence's end)
+#pragma unroll
+        for (int j4 = 0; j4 < 8; ++j4) {  // four columns: their lse and delta in one vector load each
+          const float4 l4 = *reinterpret_cast<const float4*>(ld + qi0 + 4 * j4);
+          const float4 d4 = *reinterpret_cast<const float4*>(ld + 128 + qi0 + 4 * j4);
+          const float lv[4] = {l4.x, l4.y, l4.z, l4.w}, dl[4] = {d4.x, d4.y, d4.z, d4.w};
+          float pv[4], ds[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int c = 4 * j4 + e;
+            const bool keep = c >= lo && c < hi;
+            const float pe = fast_exp2(fmaf(__uint_as_float(sv[c]), sl, -lv[e]));
+            pv[e] = keep ? pe : 0.f;
+            ds[e] = keep ? pe * (__uint_as_float(dpv[c]) - dl[e]) : 0.f;
+          }
+          pp[2 * j4] = pack_bf16x2(pv[0], pv[1]);
+          pp[2 * j4 + 1] = pack_bf16x2(pv[2], pv[3]);
+          dd[2 * j4] = pack_bf16x2(ds[0], ds[1]);
+          dd[2 * j4 + 1] = pack_bf16x2(ds[2], ds[3]);
+        }
+        tmem_st16(trow + g * 64 + hc * 16, pp);  // over scores this warp has read
+        tmem_st16(trow + 128 + g * 64 + hc * 16, dd);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_half[hc]);
+      }
+    }
+    const bool have = n_st > 0 && ok && __all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag, p.err, KID_PACKED, 36));
+    if (have) tc_fence_after();
+    // The partial sums cross over: the first CTA finishes dV and the second dK, so each sends
+    // the other tensor (fp32 rows of D floats, 16-byte chunks swizzled by row) from the start
+    // of its freed ring into the back half of the peer's ring.
+    constexpr uint32_t PB = 128u * D * 4u;  // one tensor's partial sums
+    const uint32_t ring = smem_u32(base + B_OFF_RING);
+    const uint32_t t_send = trow + (crank == 0 ? 384u : 256u), t_keep = trow + (crank == 0 ? 256u : 384u);
+    const uint32_t prow = (uint32_t)r * (D * 4);
+#pragma unroll
+    for (int c = 0; c < DH / 32; ++c) {
+      uint32_t v[32];
+      if (have) {
+        tmem_ld32(t_send + g * DH + c * 32, v);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int q4 = 0; q4 < 8; ++q4) {
+        const uint32_t o = ring + prow + ((uint32_t)(((g * DH + c * 32) / 4 + q4) ^ (r & 7)) << 4);
+        if (have)
+          st_shared_v4(o, v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
+        else
+          st_shared_v4(o, 0u, 0u, 0u, 0u);
+      }
+    }
+    fence_proxy_async_smem();
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(peer_full, PB);
+    bar_ew();
+    // both CTAs have finished their products: both rings are free
+    cluster_sync_all();
+    if (threadIdx.x == 0) {
+      const uint32_t other = crank ^ 1u;
+      bulk_copy_to_peer(mapa_shared(ring + PB, other), ring, PB, mapa_shared(smem_u32(peer_full), other));
+    }
+    (void)__all_sync(0xffffffffu, mbar_wait(peer_full, 0, abort_flag, p.err, KID_PACKED, 37));
+    // this CTA's tensor (its sums plus the peer's) through the freed K tile's shared memory
+    // and NA TMA stores; dK takes the softmax scale
+    const uint32_t tile = smem_u32(base + B_OFF_A);
+    const float sc = crank == 0 ? 1.0f : p.scale;
+#pragma unroll
+    for (int c = 0; c < DH / 32; ++c) {
+      float v[32];
+      uint32_t vr[32];
+      if (have) {
+        tmem_ld32(t_keep + g * DH + c * 32, vr);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int q4 = 0; q4 < 8; ++q4) {
+        const uint4 in = ld_shared_v4(ring + PB + prow + ((uint32_t)(((g * DH + c * 32) / 4 + q4) ^ (r & 7)) << 4));
+        const float iv[4] = {__uint_as_float(in.x), __uint_as_float(in.y), __uint_as_float(in.z), __uint_as_float(in.w)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * q4 + e] = ((have ? __uint_as_float(vr[4 * q4 + e]) : 0.f) + iv[e]) * sc;
+      }
+      stage_row32(tile, r, g * (DH / 32) + c, v);
+    }
+    fence_proxy_async_smem();
+    bar_ew();
+    if (!*abort_flag)
+      store_tile<D>(crank == 0 ? &p.tdv : &p.tdk, crank == 0 ? p.dv : p.dk, crank == 0 ? p.ld_dv : p.ld_dk, tile,
+                    row0 + kt * TT, kvh * D, n_keys, threadIdx.x, B_EW);
+    // the peer has its copy of this CTA's partial sums before this shared memory goes
+    cluster_sync_all();
+  }
+  if (warp >= B_EW / 32) {  // the TMA and MMA warps join the two cluster barriers too
+    __syncwarp();
+    cluster_sync_all();
+    cluster_sync_all();
+  }
+  __syncthreads();
+  if (warp == B_MMA && *abort_flag) {  // products already issued finish before TMEM is freed
+    if (lane == 0) umma_commit(drain);
+    __syncwarp();
+    mbar_wait_drain(drain, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == B_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+
+template <typename K>
+int allow_smem(K kernel, int bytes, int (&configured)[64]) {
+  int dev = 0;
+  NF4_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev >= 64 || !configured[dev]) {
+    NF4_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    if (dev < 64) configured[dev] = 1;
+  }
+  return NF4LS_OK;
+}
+
+template <int D>
+int launch_fwd(const FwdParams& p, int n_tiles, cudaStream_t s) {
+  static int configured[64] = {0};
+  NF4_TRY(allow_smem(k_packed_fwd<D>, SMEM_TC, configured));
+  k_packed_fwd<D><<<(unsigned)n_tiles * p.nq, F_THREADS, SMEM_TC, s>>>(p);
+  note_launch();
+  NF4_CUDA_TRY(cudaGetLastError());
+  return NF4LS_OK;
+}
+
+template <int D>
+int launch_bwd(BwdParams& p, const PackTile* query_tiles, const PackTile* key_tiles, cudaStream_t s) {
+  static int conf_q[64] = {0}, conf_k[64] = {0};
+  NF4_TRY(allow_smem(k_packed_dq<D>, SMEM_BWD, conf_q));
+  NF4_TRY(allow_smem(k_packed_dkv<D>, SMEM_BWD, conf_k));
+  // the query side writes the statistics that the key side reads
+  p.tiles = query_tiles;
+  k_packed_dq<D><<<(unsigned)p.n_tiles * p.nq, B_THREADS, SMEM_BWD, s>>>(p);
+  note_launch();
+  NF4_CUDA_TRY(cudaGetLastError());
+  p.tiles = key_tiles;
+  k_packed_dkv<D><<<(unsigned)p.n_tiles * p.nkv * 2, B_THREADS, SMEM_BWD, s>>>(p);
+  note_launch();
+  NF4_CUDA_TRY(cudaGetLastError());
+  return NF4LS_OK;
+}
+
+int check_heads(const nf4ls_pack* pack, const nf4ls_packed_heads* h, const char* who) {
+  if (!h) return fail(NF4LS_INVALID_ARG, "%s: null heads", who);
+  if (h->head_dim != 64 && h->head_dim != 128) return fail(NF4LS_SHAPE, "%s: head_dim must be 64 or 128", who);
+  if (h->n_q < 1 || h->n_kv < 1 || h->n_q % h->n_kv || h->n_q > 1024)
+    return fail(NF4LS_SHAPE, "%s: n_q %d, n_kv %d (n_q a multiple of n_kv, at most 1024)", who, h->n_q, h->n_kv);
+  if (!(h->scale > 0.0f) || !(h->scale < 1e30f)) return fail(NF4LS_INVALID_ARG, "%s: scale must be positive", who);
+  if ((int64_t)pack->n_tiles * h->n_q * 2 > 0x7FFFFFFF) return fail(NF4LS_SHAPE, "%s: too many tiles for one launch", who);
+  return NF4LS_OK;
+}
+
+int check_rows(const void* p, int ld, int width, const char* name, const char* who) {
+  if (!p) return fail(NF4LS_INVALID_ARG, "%s: null %s", who, name);
+  if (!aligned(p, 16)) return fail(NF4LS_ALIGN, "%s: %s must be 16-byte aligned", who, name);
+  if (ld < width || ld % 8) return fail(NF4LS_SHAPE, "%s: row stride %d of %s (a multiple of 8, at least %d)", who, ld, name, width);
+  return NF4LS_OK;
+}
+
+int tile_map(CUtensorMap* map, const void* p, int width, int total, int ld) {
+  return tma_map_bf16(map, p, (uint64_t)width, (uint64_t)total, (uint64_t)ld * 2, 64, TT);
+}
+
+const PackTile* tile_list(const nf4ls_pack* p, uint64_t off) {
+  return reinterpret_cast<const PackTile*>(static_cast<const uint8_t*>(p->plan_dev) + off);
+}
+
+}  // namespace
+
+}  // namespace nf4ls
+
+using namespace nf4ls;
+
+extern "C" size_t nf4ls_packed_attention_ws_bytes(const nf4ls_pack* pack, const nf4ls_packed_heads* heads) {
+  if (!pack || !heads || pack->n_tiles < 0 || heads->n_q < 1) return 0;
+  return (size_t)heads->n_q * pack->n_tiles * 2 * TT * sizeof(float);
+}
+
+extern "C" int nf4ls_packed_attention_fwd(const nf4ls_pack* pack, const nf4ls_packed_heads* heads,
+                                          const nf4ls_packed_attention* t, nf4ls_stream stream) {
+  static_assert(SMEM_TC <= 232448, "shared memory of the packed attention");
+  const char* who = "nf4ls_packed_attention_fwd";
+  clear_error();
+  NF4_TRY(check_pack(pack, who));
+  NF4_TRY(check_heads(pack, heads, who));
+  if (!t) return fail(NF4LS_INVALID_ARG, "%s: null tensors", who);
+  const int d = heads->head_dim, qd = heads->n_q * d, kvd = heads->n_kv * d;
+  NF4_TRY(check_rows(t->q, t->ld_q, qd, "q", who));
+  NF4_TRY(check_rows(t->k, t->ld_k, kvd, "k", who));
+  NF4_TRY(check_rows(t->v, t->ld_v, kvd, "v", who));
+  NF4_TRY(check_rows(t->o, t->ld_o, qd, "o", who));
+  if (!t->lse) return fail(NF4LS_INVALID_ARG, "%s: null lse", who);
+  if (!aligned(t->lse, 16)) return fail(NF4LS_ALIGN, "%s: lse must be 16-byte aligned", who);
+  if (pack->total == 0) return NF4LS_OK;
+  FwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  NF4_TRY(tile_map(&p.tq, t->q, qd, pack->total, t->ld_q));
+  NF4_TRY(tile_map(&p.tk, t->k, kvd, pack->total, t->ld_k));
+  NF4_TRY(tile_map(&p.tv, t->v, kvd, pack->total, t->ld_v));
+  NF4_TRY(tile_map(&p.to, t->o, qd, pack->total, t->ld_o));
+  p.tiles = tile_list(pack, pack->off_query_tiles);
+  p.o = static_cast<__nv_bfloat16*>(t->o);
+  p.lse = t->lse;
+  p.ldo = t->ld_o;
+  p.total = pack->total;
+  p.nq = heads->n_q;
+  p.nkv = heads->n_kv;
+  p.scale_log2 = heads->scale * 1.4426950408889634f;
+  p.err = device_error_ptr();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return d == 64 ? launch_fwd<64>(p, pack->n_tiles, s) : launch_fwd<128>(p, pack->n_tiles, s);
+}
+
+extern "C" int nf4ls_packed_attention_bwd(const nf4ls_pack* pack, const nf4ls_packed_heads* heads,
+                                          const nf4ls_packed_attention* t, void* ws_dev, size_t ws_bytes,
+                                          nf4ls_stream stream) {
+  static_assert(SMEM_BWD <= 232448, "shared memory of the packed attention backward");
+  const char* who = "nf4ls_packed_attention_bwd";
+  clear_error();
+  NF4_TRY(check_pack(pack, who));
+  NF4_TRY(check_heads(pack, heads, who));
+  if (!t) return fail(NF4LS_INVALID_ARG, "%s: null tensors", who);
+  const int d = heads->head_dim, qd = heads->n_q * d, kvd = heads->n_kv * d;
+  NF4_TRY(check_rows(t->q, t->ld_q, qd, "q", who));
+  NF4_TRY(check_rows(t->k, t->ld_k, kvd, "k", who));
+  NF4_TRY(check_rows(t->v, t->ld_v, kvd, "v", who));
+  NF4_TRY(check_rows(t->o, t->ld_o, qd, "o", who));
+  NF4_TRY(check_rows(t->d_o, t->ld_do, qd, "do", who));
+  NF4_TRY(check_rows(t->dq, t->ld_dq, qd, "dq", who));
+  NF4_TRY(check_rows(t->dk, t->ld_dk, kvd, "dk", who));
+  NF4_TRY(check_rows(t->dv, t->ld_dv, kvd, "dv", who));
+  if (!t->lse) return fail(NF4LS_INVALID_ARG, "%s: null lse", who);
+  if (pack->total == 0) return NF4LS_OK;
+  if (!ws_dev || ws_bytes < nf4ls_packed_attention_ws_bytes(pack, heads))
+    return fail(NF4LS_INVALID_ARG, "%s: workspace too small", who);
+  if (!aligned(ws_dev, 256)) return fail(NF4LS_ALIGN, "%s: the workspace must be 256-byte aligned", who);
+  BwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  NF4_TRY(tile_map(&p.tq, t->q, qd, pack->total, t->ld_q));
+  NF4_TRY(tile_map(&p.tk, t->k, kvd, pack->total, t->ld_k));
+  NF4_TRY(tile_map(&p.tv, t->v, kvd, pack->total, t->ld_v));
+  NF4_TRY(tile_map(&p.to, t->o, qd, pack->total, t->ld_o));
+  NF4_TRY(tile_map(&p.tdo, t->d_o, qd, pack->total, t->ld_do));
+  NF4_TRY(tile_map(&p.tdq, t->dq, qd, pack->total, t->ld_dq));
+  NF4_TRY(tile_map(&p.tdk, t->dk, kvd, pack->total, t->ld_dk));
+  NF4_TRY(tile_map(&p.tdv, t->dv, kvd, pack->total, t->ld_dv));
+  p.lse = t->lse;
+  p.stats = static_cast<float*>(ws_dev);
+  p.dq = static_cast<__nv_bfloat16*>(t->dq);
+  p.dk = static_cast<__nv_bfloat16*>(t->dk);
+  p.dv = static_cast<__nv_bfloat16*>(t->dv);
+  p.ld_dq = t->ld_dq;
+  p.ld_dk = t->ld_dk;
+  p.ld_dv = t->ld_dv;
+  p.total = pack->total;
+  p.n_tiles = pack->n_tiles;
+  p.nq = heads->n_q;
+  p.nkv = heads->n_kv;
+  p.scale = heads->scale;
+  p.scale_log2 = heads->scale * 1.4426950408889634f;
+  p.err = device_error_ptr();
+  const PackTile *qt = tile_list(pack, pack->off_query_tiles), *kt = tile_list(pack, pack->off_key_tiles);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return d == 64 ? launch_bwd<64>(p, qt, kt, s) : launch_bwd<128>(p, qt, kt, s);
+}

@@ -23,38 +23,13 @@
 // reads the current one.  The output is O / sum in bf16 and the log-sum-exp
 // (m + log2 sum) ln 2.  P is rounded to bf16 for the P V product, as in the mma.sync
 // kernel; the results match that kernel up to rounding.  Every mbarrier wait is bounded.
+#include "attention_tile.cuh"
 #include "common.cuh"
 #include "internal.h"
 
 namespace nf4ls {
 
 namespace {
-
-constexpr int TT = 128;                   // query / key tile
-constexpr int TILE_BYTES = TT * 128 * 2;  // 128 rows x 128 dims bf16 = 32 KB
-constexpr int ATOM = TILE_BYTES / 2;      // one 64-dim (or 64-key) swizzle atom: 16 KB
-
-// One thread's 32 fp32 values (columns 32 c .. 32 c + 31 of its row r of a 128 x 128 tile),
-// times sc, as bf16 into the tile's two 128-byte swizzled 64-column atoms at tile.
-__device__ __forceinline__ void stage_row32(uint32_t tile, int r, int c, const uint32_t (&v)[32], float sc) {
-  const uint32_t row = tile + (uint32_t)(c >> 1) * (TT * 128) + (uint32_t)r * 128;
-#pragma unroll
-  for (int q4 = 0; q4 < 4; ++q4) {
-    const int chunk = (c & 1) * 4 + q4;  // 16-byte chunk of the 128-byte row
-    st_shared_v4(row + ((uint32_t)(chunk ^ (r & 7)) << 4),
-                 pack_bf16x2(__uint_as_float(v[8 * q4]) * sc, __uint_as_float(v[8 * q4 + 1]) * sc),
-                 pack_bf16x2(__uint_as_float(v[8 * q4 + 2]) * sc, __uint_as_float(v[8 * q4 + 3]) * sc),
-                 pack_bf16x2(__uint_as_float(v[8 * q4 + 4]) * sc, __uint_as_float(v[8 * q4 + 5]) * sc),
-                 pack_bf16x2(__uint_as_float(v[8 * q4 + 6]) * sc, __uint_as_float(v[8 * q4 + 7]) * sc));
-  }
-}
-
-__device__ __forceinline__ void stage_row32(uint32_t tile, int r, int c, const float (&v)[32]) {
-  uint32_t u[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i]);
-  stage_row32(tile, r, c, u, 1.0f);
-}
 
 struct AttnTcParams {
   CUtensorMap tq, tk, tv, to;  // [rows, cols] bf16, box 64 cols x 128 rows, 128-byte swizzle (to: output)
@@ -71,49 +46,6 @@ constexpr int F_THREADS = 192, F_PROD = 4, F_MMA = 5;
 constexpr int F_OFF_Q = 0, F_OFF_K = TILE_BYTES, F_OFF_V = 2 * TILE_BYTES, F_OFF_BAR = 3 * TILE_BYTES;
 constexpr int SMEM_TC = 1024 + F_OFF_BAR + 128;
 constexpr float kRescaleLog2 = 8.0f;  // the reference maximum may trail the true one by this much
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32(taddr, r); }
-__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[16]) { tmem_st16(taddr, r); }
-
-// 2^x by the hardware approximation (ex2.approx, flush-to-zero): its relative error is
-// far below the bf16 rounding that every probability gets next.
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// D[tmem] (+)= A[tmem] * B[smem desc]: A of M = 128 lanes x 16 bf16 (8 columns).
-__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 
 template <int D>
 __global__ void __launch_bounds__(F_THREADS, 2) k_attn_fwd_tc(const __grid_constant__ AttnTcParams p) {
@@ -390,10 +322,6 @@ constexpr int SMEM_BWD = 1024 + B_OFF_BAR + 256;
 
 __device__ __forceinline__ void bar_ew() { asm volatile("bar.sync 1, %0;" ::"n"(B_EW) : "memory"); }
 
-// TMEM column of the A operand of 16-row step ks (0-7) of a block whose first column is
-// c0: warp half g packed its 64 rows' values to columns c0 + 64 g .. c0 + 64 g + 31.
-__device__ __forceinline__ uint32_t packed_col(uint32_t c0, int ks) { return c0 + (ks >> 2) * 64 + (ks & 3) * 8; }
-
 // QUERY side: dQ of one 128-query tile of one query head.  The Q and dO tiles are
 // copied once into TMEM (bf16 pairs, one query row per lane), so that S = Q K^T and
 // dP = dO V^T take their A operand from TMEM and read only K and V from shared memory
@@ -648,17 +576,6 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_attn_dq_tc(const __grid_consta
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-}
-
-// Bulk copy of bytes (a multiple of 16) from this CTA's shared memory to another CTA's of
-// the cluster, completing transaction bytes on that CTA's mbarrier (both given by their
-// shared::cluster addresses).
-__device__ __forceinline__ void bulk_copy_to_peer(uint32_t dst_cluster, uint32_t src, uint32_t bytes,
-                                                  uint32_t bar_cluster) {
-  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   dst_cluster),
-               "r"(src), "r"(bytes), "r"(bar_cluster)
-               : "memory");
 }
 
 // KEY side: dK, dV of one 128-key tile of one kv head, by a cluster of two CTAs that split

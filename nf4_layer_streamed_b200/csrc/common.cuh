@@ -16,7 +16,7 @@ namespace nf4ls {
 // wait expired), [1] = kernel id, [2] = block, [3] = site.  The record lives in a
 // file-scope __device__ array of device.cu; its address is looked up per device.
 
-enum KernelId : int { KID_GEMM = 1, KID_ATTN = 2, KID_WAIT_PROBE = 3, KID_NORM = 4 };
+enum KernelId : int { KID_GEMM = 1, KID_ATTN = 2, KID_WAIT_PROBE = 3, KID_NORM = 4, KID_PACKED = 5 };
 
 // A bounded wait gives up after this many nanoseconds of global time.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;

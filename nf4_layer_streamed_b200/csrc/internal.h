@@ -277,6 +277,16 @@ int attention_bwd(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfl
                   __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, int ld_dq, int ld_dkv, int batch,
                   int seq, int nq, int nkv, int d, cudaStream_t s);
 
+// ----------------------------------------------------------------------------- packed batches
+// One 128-row tile of a sequence of a packed batch (an entry of the plan's tile lists).
+struct PackTile {
+  int32_t row0;   // first row of its sequence
+  int32_t len;    // length of its sequence
+  int32_t tile;   // tile number within the sequence
+  int32_t index;  // tile number within the batch, in row order
+};
+int check_pack(const nf4ls_pack* p, const char* who);
+
 // LoRA backward (lora.cu); the forward's t comes from rmsnorm_lora_fwd (body.cu).
 // dB_q, dB_v, dA_q, dA_v (fp32, written) and dt into dtpad [M, 64] (bf16, zeros in
 // columns 32-63) from dq (columns [0, qd) of dqkv) and dv (columns [vcol, vcol + kvd));

@@ -1,0 +1,250 @@
+"""Packed causal attention against the formula in 64 bits (GPU).
+
+Tolerances: a probability and a score gradient are rounded once to bf16 for their
+product (relative 2^-8 at most), an output once more; sums, statistics and exponentials
+are 32-bit, whose share is bounded by 2^-13 of the sums of magnitudes (a score of d
+products is off by at most (d + 2) 2^-24 of its magnitudes, which moves p by that much
+in nats: below 6e-5 for N(0, 1) operands of 128 dims).
+"""
+import math
+
+import pytest
+import torch
+
+from nf4_layer_streamed_b200 import api
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+R = 2.0 ** -8   # a rounding to bf16
+F = 2.0 ** -13  # what 32-bit arithmetic adds, relative to sums of magnitudes
+
+LENGTHS = [[1], [2, 1], [127], [128], [129], [1, 1, 1, 1], [0, 5, 0, 257, 1, 0], [640, 33, 255, 128], [16] * 40]
+HEADS = [(9, 3, 64), (4, 1, 128), (2, 2, 128), (8, 1, 64), (3, 1, 128)]
+
+
+def make(lengths, n_q, n_kv, d, seed=0, extra_rows=0):
+    """q, k, v as column slices of one buffer whose rows behind the last sequence are NaN."""
+    g = torch.Generator(device=DEV).manual_seed(seed + sum(lengths) + n_q * d)
+    total = sum(lengths)
+    buf = torch.full((total + extra_rows, (n_q + 2 * n_kv) * d), math.nan, dtype=torch.bfloat16, device=DEV)
+    buf[:total] = torch.randn(total, buf.shape[1], generator=g, device=DEV).to(torch.bfloat16)
+    do = torch.randn(total, n_q * d, generator=g, device=DEV).to(torch.bfloat16)
+    return buf[:, :n_q * d], buf[:, n_q * d:(n_q + n_kv) * d], buf[:, (n_q + n_kv) * d:], do
+
+
+def reference(lengths, q, k, v, n_q, n_kv, d, scale):
+    """(o, lse, bound of o) in float64."""
+    o, lse, tol, a = [], [], [], 0
+    for n in lengths:
+        qh, kh, vh = heads64(q, k, v, a, n, n_q, n_kv, d)
+        s = (qh @ kh.transpose(1, 2) * scale).masked_fill(torch.ones(n, n, dtype=torch.bool, device=DEV).triu(1), -math.inf)
+        p = torch.softmax(s, 2)
+        out = p @ vh
+        o.append(out.transpose(0, 1).flatten(1))
+        lse.append(torch.logsumexp(s, 2))
+        tol.append((((R + F) * (p @ vh.abs())) + R * out.abs()).transpose(0, 1).flatten(1))
+        a += n
+    return torch.cat(o), torch.cat(lse, 1), torch.cat(tol)
+
+
+def heads64(q, k, v, a, n, n_q, n_kv, d):
+    qh = q[a:a + n].double().reshape(n, n_q, d).transpose(0, 1)
+    kh, vh = (x[a:a + n].double().reshape(n, n_kv, d).transpose(0, 1).repeat_interleave(n_q // n_kv, 0) for x in (k, v))
+    return qh, kh, vh
+
+
+def reference_grad(lengths, q, k, v, o, do, lse, n_q, n_kv, d, scale):
+    """Gradients and their bounds in float64, from the given o and lse."""
+    out, a = [], 0
+    for n in lengths:
+        qh, kh, vh = heads64(q, k, v, a, n, n_q, n_kv, d)
+        oh, dh, _ = heads64(o, do, do, a, n, n_q, n_q, d)
+        s = (qh @ kh.transpose(1, 2) * scale).masked_fill(torch.ones(n, n, dtype=torch.bool, device=DEV).triu(1), -math.inf)
+        p = torch.exp(s - lse[:, a:a + n, None].double())
+        ds = p * (dh @ vh.transpose(1, 2) - (dh * oh).sum(2, keepdim=True))
+        mag = p * (dh.abs() @ vh.abs().transpose(1, 2) + (dh * oh).abs().sum(2, keepdim=True))
+
+        def shared(x):  # the query heads that share a key head
+            return x.reshape(n_kv, n_q // n_kv, n, d).sum(1)
+        dq, tq = scale * ds @ kh, scale * (R * ds.abs() + F * mag) @ kh.abs()
+        dk, tk = shared(scale * ds.transpose(1, 2) @ qh), shared(scale * (R * ds.abs() + F * mag).transpose(1, 2) @ qh.abs())
+        dv, tv = shared(p.transpose(1, 2) @ dh), shared((R + F) * p.transpose(1, 2) @ dh.abs())
+        out.append([x.transpose(0, 1).flatten(1) for x in (dq, dk, dv, tq + R * dq.abs(), tk + R * dk.abs(), tv + R * dv.abs())])
+        a += n
+    return [torch.cat(x) for x in zip(*out)]
+
+
+def within(got, want, tol, what):
+    off = (got.double() - want).abs() - tol
+    assert torch.isfinite(got).all() and off.max().item() <= 1e-7, (what, off.max().item())
+
+
+@pytest.mark.parametrize("heads", HEADS, ids=str)
+@pytest.mark.parametrize("lengths", LENGTHS, ids=lambda n: "-".join(map(str, n[:7])))
+def test_forward_and_gradients(lengths, heads):
+    n_q, n_kv, d = heads
+    q, k, v, do = make(lengths, n_q, n_kv, d, extra_rows=70)
+    pack = api.PackedRows(lengths)
+    scale = d ** -0.5
+    o, lse = api.packed_attention_fwd(pack, q, k, v, n_q, n_kv, d)
+    want, wl, tol = reference(lengths, q, k, v, n_q, n_kv, d, scale)
+    within(o, want, tol, "o")
+    within(lse, wl, 6e-5 + 2.0 ** -22 * wl.abs(), "lse")
+    got = api.packed_attention_bwd(pack, q, k, v, o, do, lse, n_q, n_kv, d)
+    ref = reference_grad(lengths, q, k, v, o, do, lse, n_q, n_kv, d, scale)
+    for name, g, w, t in zip(("dq", "dk", "dv"), got, ref[:3], ref[3:]):
+        within(g, w, t, name)
+
+
+def test_many_short_sequences_and_a_long_one():
+    lengths = [1] * 700 + [2500] + [3] * 300
+    n_q, n_kv, d = 4, 2, 64
+    q, k, v, do = make(lengths, n_q, n_kv, d)
+    pack = api.PackedRows(lengths)
+    o, lse = api.packed_attention_fwd(pack, q, k, v, n_q, n_kv, d)
+    ones = [1] * 700
+    torch.testing.assert_close(o[:700].reshape(700, n_kv, 2, d), v[:700].reshape(700, n_kv, 1, d).expand(-1, -1, 2, -1),
+                               rtol=0, atol=0)  # one token: p = 1
+    want, wl, tol = reference(lengths[700:], q[700:], k[700:], v[700:], n_q, n_kv, d, d ** -0.5)
+    within(o[700:], want, tol, "o")
+    within(lse[:, 700:], wl, 6e-5 + 2.0 ** -22 * wl.abs(), "lse")
+    dq, dk, dv = api.packed_attention_bwd(pack, q, k, v, o, do, lse, n_q, n_kv, d)
+    ref = reference_grad(ones + lengths[700:], q, k, v, o, do, lse, n_q, n_kv, d, d ** -0.5)
+    for name, g, w, t in zip(("dq", "dk", "dv"), (dq, dk, dv), ref[:3], ref[3:]):
+        within(g, w, t, name)
+
+
+@pytest.mark.parametrize("factor", [0.01, 30.0])
+def test_flat_and_sharp_rows(factor):
+    """Scores all alike, and scores of hundreds of nats that grow along the keys (the
+    running maximum moves at almost every tile)."""
+    lengths, n_q, n_kv, d = [700, 260], 2, 1, 64
+    q, k, v, do = make(lengths, n_q, n_kv, d, seed=3)
+    q, v = q.contiguous(), v.contiguous()
+    ramp = torch.linspace(0.1, 1.0, sum(lengths), device=DEV)[:, None]
+    q = (q.float().abs() * factor).to(torch.bfloat16)
+    k = (k.float().abs() * ramp).to(torch.bfloat16)
+    pack = api.PackedRows(lengths)
+    o, lse = api.packed_attention_fwd(pack, q, k, v, n_q, n_kv, d)
+    want, wl, tol = reference(lengths, q, k, v, n_q, n_kv, d, d ** -0.5)
+    # a score is off by (d + 2) 2^-24 of its magnitude, here up to hundreds of nats
+    shift = (d + 2) * 2.0 ** -24 * wl.abs().max().item()
+    within(o, want, tol * (1 + shift / R), "o")
+    within(lse, wl, 6e-5 + shift + 2.0 ** -22 * wl.abs(), "lse")
+
+
+def test_scale_argument_and_gradient_against_differences():
+    lengths, n_q, n_kv, d, scale = [5, 131], 2, 1, 64, 0.3
+    q, k, v, do = make(lengths, n_q, n_kv, d, seed=9)
+    pack = api.PackedRows(lengths)
+    o, lse = api.packed_attention_fwd(pack, q, k, v, n_q, n_kv, d, scale=scale)
+    grads = api.packed_attention_bwd(pack, q, k, v, o, do, lse, n_q, n_kv, d, scale=scale)
+    x = [t.double().contiguous() for t in (q, k, v)]
+
+    def loss(x):
+        return (reference(lengths, *x, n_q, n_kv, d, scale)[0] * do.double()).sum().item()
+    g = torch.Generator(device=DEV).manual_seed(1)
+    for i in range(3):
+        step = torch.randn(x[i].shape, generator=g, device=DEV, dtype=torch.float64)
+        step /= step.norm()
+        up, down = list(x), list(x)
+        up[i], down[i] = x[i] + 1e-4 * step, x[i] - 1e-4 * step
+        diff = (loss(up) - loss(down)) / 2e-4
+        got = (grads[i].double() * step).sum().item()
+        # o is rounded to bf16 before delta: every element of the gradient is off by about R of its size
+        assert abs(got - diff) <= 4 * R * grads[i].double().norm().item() * 1.0, (i, got, diff)
+
+
+def test_other_sequences_and_rows_behind_are_left_alone():
+    lengths, n_q, n_kv, d = [200, 77, 130], 4, 2, 128
+    q, k, v, do = make(lengths, n_q, n_kv, d, extra_rows=9)
+    q, k, v = q.clone(), k.clone(), v.clone()
+    pack = api.PackedRows(lengths)
+    o0, l0 = api.packed_attention_fwd(pack, q, k, v, n_q, n_kv, d)
+    g0 = api.packed_attention_bwd(pack, q, k, v, o0, do, l0, n_q, n_kv, d)
+    rows = torch.ones(sum(lengths), dtype=torch.bool, device=DEV)
+    rows[200:277] = False
+    for bad in (math.nan, math.inf, torch.finfo(torch.bfloat16).min):
+        q1, k1, v1, do1 = (t.clone() for t in (q, k, v, do))
+        for t in (q1, k1, v1, do1):
+            t[200:277] = bad
+        out = torch.full((sum(lengths) + 9, n_q * d), 7.0, dtype=torch.bfloat16, device=DEV)
+        o1, l1 = api.packed_attention_fwd(pack, q1, k1, v1, n_q, n_kv, d, out=out)
+        assert torch.equal(o1[:407][rows], o0[rows]) and torch.equal(l1[:, rows], l0[:, rows])
+        assert (out[407:] == 7.0).all()
+        o1 = torch.where(rows[:, None], o0, torch.full_like(o0, bad))
+        l1 = torch.where(rows, l0, torch.full_like(l0, bad))
+        buf = torch.full((sum(lengths) + 9, (n_q + 2 * n_kv) * d), 7.0, dtype=torch.bfloat16, device=DEV)
+        outs = (buf[:, :n_q * d], buf[:, n_q * d:(n_q + n_kv) * d], buf[:, (n_q + n_kv) * d:])
+        g1 = api.packed_attention_bwd(pack, q1, k1, v1, o1, do1, l1, n_q, n_kv, d, out=outs)
+        for a, b in zip(g1, g0):
+            assert torch.equal(a[:407][rows], b[rows])
+        assert (buf[407:] == 7.0).all()
+
+
+def test_no_rows():
+    pack = api.PackedRows([0, 0])
+    z = torch.zeros(4, 128, dtype=torch.bfloat16, device=DEV)
+    o, lse = api.packed_attention_fwd(pack, z, z, z, 2, 2, 64)
+    assert o.shape == (0, 128) and lse.shape == (2, 0)
+    g = api.packed_attention_bwd(pack, z, z, z, o, o, lse, 2, 2, 64)
+    assert all(x.shape == (0, 128) for x in g)
+
+
+def test_deterministic_on_another_stream_and_in_a_graph():
+    lengths, n_q, n_kv, d = [300, 1, 129, 514], 8, 2, 128
+    q, k, v, do = make(lengths, n_q, n_kv, d)
+    pack = api.PackedRows(lengths)
+
+    def both(stream=None):
+        o, lse = api.packed_attention_fwd(pack, q, k, v, n_q, n_kv, d, stream=stream)
+        return (o, lse) + api.packed_attention_bwd(pack, q, k, v, o, do, lse, n_q, n_kv, d, stream=stream)
+    want = both()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = both(side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(both())
+        graphs.append(g)
+    # two captured steps in flight at once do not share a workspace
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            graphs[0].replay()
+        with torch.cuda.stream(s2):
+            graphs[1].replay()
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(a, b) for a, b in zip(o, want))
+    assert api.device_error()[0] == 0
+
+
+def test_row_offsets_beyond_32_bits():
+    """Rows 2^16 elements apart: the last ones start more than 2^31 elements into the buffer."""
+    n_q, n_kv, d, ld = 2, 1, 64, 1 << 16
+    lengths = [32760, 200, 1]
+    total = sum(lengths)
+    buf = torch.empty(total, ld, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    w = (n_q + 2 * n_kv) * d
+    at = (0, ld // 2, ld - w)  # q, k, v spread over the row
+    buf[:, :n_q * d] = torch.randn(total, n_q * d, generator=g, device=DEV).to(torch.bfloat16)
+    for a in at[1:]:
+        buf[:, a:a + n_kv * d] = torch.randn(total, n_kv * d, generator=g, device=DEV).to(torch.bfloat16)
+    q, k, v = buf[:, :n_q * d], buf[:, at[1]:at[1] + n_kv * d], buf[:, at[2]:at[2] + n_kv * d]
+    pack = api.PackedRows(lengths)
+    o, lse = api.packed_attention_fwd(pack, q, k, v, n_q, n_kv, d, out=buf[:, 4096:4096 + n_q * d])
+    tail = slice(32760, total)
+    want, wl, tol = reference(lengths[1:], q[tail], k[tail], v[tail], n_q, n_kv, d, d ** -0.5)
+    within(o[tail], want, tol, "o")
+    do = torch.randn(total, n_q * d, generator=g, device=DEV).to(torch.bfloat16)
+    outs = (buf[:, 8192:8192 + n_q * d], buf[:, 12288:12288 + n_kv * d], buf[:, 16384:16384 + n_kv * d])
+    api.packed_attention_bwd(pack, q, k, v, o, do, lse, n_q, n_kv, d, out=outs)
+    ref = reference_grad(lengths[1:], q[tail], k[tail], v[tail], o[tail], do[tail], lse[:, tail], n_q, n_kv, d, d ** -0.5)
+    for name, x, w, t in zip(("dq", "dk", "dv"), outs, ref[:3], ref[3:]):
+        within(x[tail], w, t, name)
