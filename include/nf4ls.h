@@ -630,6 +630,116 @@ int nf4ls_packed_attention_bwd(const nf4ls_pack* pack, const nf4ls_packed_heads*
                                const nf4ls_packed_attention* t, void* ws_dev, size_t ws_bytes,
                                nf4ls_stream stream);
 
+/* ------------------------------------------------------------------ rotary positions
+ * Rotation of the pairs of each query and key head by angle = position * frequency:
+ *   (a, b) -> m (a cos - b sin, b cos + a sin);  inverse = 1 turns the other way, which is
+ * the backward pass (the transposed map).  A pair i < rot_dim / 2 is dims (i, i + rot_dim/2)
+ * of the head (interleaved = 0) or (2 i, 2 i + 1) (interleaved = 1); dims from rot_dim on
+ * are copied.  rot_dim and head_dim are multiples of 16, head_dim at most 512.
+ * Frequencies theta^(-2 i / rot_dim), then by `scaling`:
+ *   NONE    as they are (m = 1);
+ *   LINEAR  divided by factor;
+ *   BANDED  by the turns t of a pair over the original context: kept for t >= high,
+ *           divided by factor for t <= low, blended linearly in t between;
+ *   YARN    (YaRN, Peng et al. 2023) blended linearly in the pair number between the pair
+ *           that turns `high` times (kept) and the one that turns `low` times (divided),
+ *           and m = 0.1 ln(factor) + 1.
+ * nf4ls_rope_table (host only) returns them as 64-bit fractions of a turn per position
+ * (turns_host [rot_dim / 2]) and m; the caller copies the table to the device.
+ * nf4ls_rope_apply rotates q [rows, n_q * head_dim] and k [rows, n_kv * head_dim] (bf16,
+ * row strides ld_* in elements, multiples of 8) into q_out and k_out in one launch; an
+ * output may be its input itself (in place) but may not overlap one otherwise.  Either of
+ * n_q and n_kv may be 0.  Positions may be negative and of any size.  The angle is exact
+ * to 2^-32 turns at every position. */
+#define NF4LS_ROPE_NONE   0
+#define NF4LS_ROPE_LINEAR 1
+#define NF4LS_ROPE_BANDED 2
+#define NF4LS_ROPE_YARN   3
+
+typedef struct {
+    int32_t head_dim, rot_dim, interleaved, scaling;
+    double theta;
+    double factor;          /* LINEAR, BANDED, YARN: >= 1                       */
+    double low, high;       /* BANDED, YARN: turns over the original context    */
+    double original;        /* BANDED, YARN: tokens of the original context     */
+} nf4ls_rope_cfg;
+
+typedef struct {
+    const uint64_t* turns_dev;
+    const int32_t* positions_dev;   /* [rows] */
+    const void *q, *k;
+    void *q_out, *k_out;
+    int32_t rows, n_q, n_kv, ld_q, ld_k, ld_q_out, ld_k_out, inverse;
+    float mscale;
+} nf4ls_rope_rows;
+
+int nf4ls_rope_table(const nf4ls_rope_cfg* cfg, uint64_t* turns_host, float* mscale);
+int nf4ls_rope_apply(const nf4ls_rope_cfg* cfg, const nf4ls_rope_rows* t, nf4ls_stream stream);
+
+/* ------------------------------------------------------------------ preference and policy losses
+ * Losses on token logits (bf16 [rows, vocab], row stride ld in elements, any alignment of
+ * an element) and the target of each row (int32; a value outside [0, vocab) is a row
+ * without a loss: a prompt row, the last row of a sequence).  logp_t is the log
+ * probability of row t's target, 0 for a row without one.  Logits of -inf or of the type's
+ * lowest value are tokens of probability 0; a NaN or +inf makes its row's results NaN.
+ *
+ * Preference loss over pairs of sequences of a packed batch, 2 i preferred to 2 i + 1:
+ *   S_s = sum of logp over sequence s;  gap_i = (S_2i - S_2i+1) - (R_2i - R_2i+1) with R the
+ *   reference model's sums (ref_logp_dev fp32 [n_seqs]; the adapter-off pass);  h = beta gap;
+ *   SIGMOID  -(1 - e) log sigmoid(h) - e log sigmoid(-h), e = label_smoothing;
+ *   HINGE    max(0, 1 - h);
+ *   SQUARED  (gap - 1 / (2 beta))^2;
+ * loss = mean over the pairs.  The forward writes loss [1], seq_logp [n_seqs], margin
+ * [n_pairs] (h), coef [n_seqs] (d loss / d S), logp [total] and row_stats [total, 4] (each
+ * row's maximum, sum of exp(x - max), what the rounding of logp left out, and 0; 16-byte
+ * aligned).  The backward reads row_stats and coef and
+ * writes dlogits = grad_scale coef (onehot(target) - softmax) (bf16, zero rows without a
+ * target); dlogits may be the logits themselves (in place), not overlap them otherwise.
+ *
+ * Clipped policy loss with a KL term over independent rows:
+ *   r = exp(logp - old_logp);  d = ref_logp - logp;
+ *   row loss = w (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (e^d - d - 1));
+ * loss = sum of the row losses over the rows with a target (w carries the 1 / count).  One
+ * launch reads a row, and, unless dlogits_dev is NULL, writes its gradient times
+ * grad_scale; on the border of the clip range the gradient flows.  ref_logp may be NULL
+ * when kl_coef is 0.  logp_dev and row_loss_dev: fp32 [rows], written.
+ * Sums run in a fixed order: the same inputs give the same bits. */
+#define NF4LS_PREF_SIGMOID 0
+#define NF4LS_PREF_HINGE   1
+#define NF4LS_PREF_SQUARED 2
+
+typedef struct {
+    const void* logits_dev;
+    int64_t ld;
+    int32_t vocab;
+    const int32_t* targets_dev;
+} nf4ls_logits;
+
+typedef struct {
+    int32_t kind;
+    float beta, label_smoothing;
+} nf4ls_preference_cfg;
+
+typedef struct {
+    float *loss, *seq_logp, *margin, *coef, *logp, *row_stats;
+} nf4ls_preference_out;
+
+typedef struct {
+    float clip_low, clip_high, kl_coef, grad_scale;
+} nf4ls_policy_cfg;
+
+typedef struct {
+    const float *old_logp, *ref_logp, *advantages, *weights;   /* [rows] */
+} nf4ls_policy_rows;
+
+int nf4ls_preference_fwd(const nf4ls_pack* pack, const nf4ls_preference_cfg* cfg, const nf4ls_logits* logits,
+                         const float* ref_logp_dev, const nf4ls_preference_out* out, nf4ls_stream stream);
+int nf4ls_preference_bwd(const nf4ls_pack* pack, const nf4ls_logits* logits, const nf4ls_preference_out* saved,
+                         float grad_scale, void* dlogits_dev, int64_t ld_d, nf4ls_stream stream);
+int nf4ls_policy_loss(const nf4ls_policy_cfg* cfg, int32_t rows, const nf4ls_logits* logits,
+                      const nf4ls_policy_rows* in, float* loss_dev, float* logp_dev, float* row_loss_dev,
+                      void* dlogits_dev, int64_t ld_d, nf4ls_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

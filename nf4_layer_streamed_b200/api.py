@@ -512,6 +512,197 @@ def packed_attention_bwd(pack: PackedRows, q, k, v, o, do, lse, n_q: int, n_kv: 
     return dq, dk, dv
 
 
+# ----------------------------------------------------------------------------- rotary positions
+
+ROPE_SCALINGS = {"linear": 1, "banded": 2, "yarn": 3}
+
+
+class Rope:
+    """Rotary frequencies of a model (nf4ls_rope_table) on the device.  scaling: None, or a
+    dict with "kind" ("linear", "banded" or "yarn"), "factor" and, for the latter two, the
+    original context "original" and the turns over it between which frequencies are
+    blended: "low" and "high" (banded), "beta_slow" and "beta_fast" (yarn)."""
+
+    def __init__(self, head_dim: int, theta: float, rot_dim: int | None = None, interleaved: bool = False,
+                 scaling: dict | None = None, device="cuda"):
+        rot_dim = head_dim if rot_dim is None else rot_dim
+        kind, factor, low, high, original = 0, 1.0, 0.0, 0.0, 0.0
+        if scaling is not None:
+            if scaling.get("kind") not in ROPE_SCALINGS:
+                raise ValueError(f"scaling kind {scaling.get('kind')!r}: one of {', '.join(ROPE_SCALINGS)}")
+            kind = ROPE_SCALINGS[scaling["kind"]]
+            names = ("low", "high") if kind == 2 else ("beta_slow", "beta_fast") if kind == 3 else ()
+            need = ("factor",) + names + (("original",) if names else ())
+            if set(scaling) != set(need) | {"kind"}:
+                raise ValueError(f"scaling {scaling['kind']}: expected {', '.join(need)}, got {sorted(scaling)}")
+            factor = float(scaling["factor"])
+            if names:
+                low, high, original = (float(scaling[n]) for n in names + ("original",))
+        self.cfg = B.RopeCfg(head_dim, rot_dim, int(bool(interleaved)), kind, theta, factor, low, high, original)
+        turns = np.zeros(max(rot_dim // 2, 1), np.uint64)
+        m = ctypes.c_float()
+        B.call("nf4ls_rope_table", ctypes.byref(self.cfg), turns.ctypes.data, ctypes.byref(m))
+        self.mscale = m.value
+        self.turns_host = turns
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self.device = self.turns.device
+
+
+def rope_apply(rope: Rope, positions: torch.Tensor, q, k, n_q: int, n_kv: int, inverse: bool = False, out=None,
+               stream=None):
+    """Queries [rows, n_q * head_dim] and keys [rows, n_kv * head_dim] rotated to their
+    positions (int32 [rows]) -> (q, k).  inverse: the transposed rotation (backward pass).
+    out: (q, k) to write to; (q, k) themselves rotate in place."""
+    if not isinstance(rope, Rope):
+        raise TypeError(f"rope: expected a Rope, got {type(rope).__name__}")
+    _need(positions, "positions", torch.int32)
+    rows, d = positions.numel(), rope.cfg.head_dim
+    if n_q < 1 or n_kv < 1:
+        raise ValueError(f"{n_q} query and {n_kv} key heads")
+    ld_q, ld_k = _rows2d(q, "q", rows, n_q * d), _rows2d(k, "k", rows, n_kv * d)
+    qo, ko = out if out is not None else (None, None)
+    if out is not None:
+        ld_qo, ld_ko = _rows2d(qo, "out q", rows, n_q * d), _rows2d(ko, "out k", rows, n_kv * d)
+
+        def clash(a, b):  # sharing memory other than being the same rows
+            return _overlap(a, b) and not (a.data_ptr() == b.data_ptr() and a.stride() == b.stride())
+        if clash(qo, q) or clash(ko, k) or _overlap(qo, k) or _overlap(ko, q) or _overlap(qo, ko):
+            raise ValueError("out: overlaps an input or another output")
+    with _On(rope.device, stream, positions=positions, q=q, k=k, out_q=qo, out_k=ko) as s:
+        if out is None:
+            qo = torch.empty(rows, n_q * d, dtype=torch.bfloat16, device=q.device)
+            ko = torch.empty(rows, n_kv * d, dtype=torch.bfloat16, device=q.device)
+            ld_qo, ld_ko = n_q * d, n_kv * d
+        if rows:
+            t = B.RopeRows(rope.turns.data_ptr(), positions.data_ptr(), q.data_ptr(), k.data_ptr(), qo.data_ptr(),
+                           ko.data_ptr(), rows, n_q, n_kv, ld_q, ld_k, ld_qo, ld_ko, int(bool(inverse)), rope.mscale)
+            B.call("nf4ls_rope_apply", ctypes.byref(rope.cfg), ctypes.byref(t), s)
+    return qo, ko
+
+
+# ----------------------------------------------------------------------------- preference and policy losses
+
+PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
+
+
+@dataclass
+class PreferenceForward:
+    """What preference_loss_fwd returns: the loss [1], each sequence's log probability, each
+    pair's margin beta * gap, each row's log probability, and what the backward needs."""
+    loss: torch.Tensor
+    seq_logp: torch.Tensor
+    margin: torch.Tensor
+    logp: torch.Tensor
+    coef: torch.Tensor
+    row_stats: torch.Tensor
+
+
+def _logits2d(t, name: str, rows: int) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[0] < rows or t.shape[1] < 1:
+        raise ValueError(f"{name}: expected bf16 [>= {rows}, vocab], got {t.dtype} {tuple(t.shape)}")
+    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    if (t.shape[1] > 1 and t.stride(1) != 1) or ld < t.shape[1]:
+        raise ValueError(f"{name}: strides {t.stride()} (unit column stride; row stride at least the vocab)")
+    return ld
+
+
+def _grad_rows(out, logits, rows: int) -> int:
+    ld = _logits2d(out, "out", rows)
+    if out.shape[1] != logits.shape[1]:
+        raise ValueError(f"out: {out.shape[1]} columns, the logits have {logits.shape[1]}")
+    if _overlap(out, logits) and not (out.data_ptr() == logits.data_ptr() and out.stride() == logits.stride()):
+        raise ValueError("out: overlaps the logits other than in place")
+    return ld
+
+
+def preference_loss_fwd(pack: PackedRows, logits: torch.Tensor, targets: torch.Tensor, ref_logp: torch.Tensor,
+                        beta: float, kind: str = "sigmoid", label_smoothing: float = 0.0,
+                        stream=None) -> PreferenceForward:
+    """Preference loss over the pairs of sequences (2 i preferred to 2 i + 1) of a pack from
+    its logits [total, vocab], the rows' targets (int32 [total], negative: no loss) and the
+    reference model's log probability of each sequence (fp32 [n_seqs])."""
+    pack = _need_pack(pack)
+    if kind not in PREFERENCE_KINDS:
+        raise ValueError(f"kind {kind!r}: one of {', '.join(PREFERENCE_KINDS)}")
+    if pack.n_seqs % 2:
+        raise ValueError(f"pack: {pack.n_seqs} sequences are not pairs")
+    n = pack.total
+    ld = _logits2d(logits, "logits", n)
+    _need(targets, "targets", torch.int32, n)
+    _need(ref_logp, "ref_logp", torch.float32, pack.n_seqs)
+    cfg = B.PreferenceCfg(PREFERENCE_KINDS[kind], beta, label_smoothing)
+    with _On(pack.device, stream, logits=logits, targets=targets, ref_logp=ref_logp) as s:
+        # row_stats first: 16-byte rows
+        m = pack.n_seqs
+        buf = torch.empty(5 * n + 2 * m + m // 2 + 1, dtype=torch.float32, device=pack.device)
+        stats, logp, seq_logp, coef, margin, loss = buf.split((4 * n, n, m, m, m // 2, 1))
+        o = B.PreferenceOut(loss.data_ptr(), seq_logp.data_ptr(), margin.data_ptr(), coef.data_ptr(), logp.data_ptr(),
+                            stats.data_ptr())
+        t = B.Logits(logits.data_ptr(), ld, logits.shape[1], targets.data_ptr())
+        B.call("nf4ls_preference_fwd", pack._ref, ctypes.byref(cfg), ctypes.byref(t), _p(ref_logp), ctypes.byref(o), s)
+    return PreferenceForward(loss, seq_logp, margin, logp, coef, stats)
+
+
+def preference_loss_bwd(pack: PackedRows, logits: torch.Tensor, targets: torch.Tensor, fwd: PreferenceForward,
+                        grad_scale: float = 1.0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of the logits (bf16 [total, vocab]) of the loss that fwd is of.  out: rows to
+    write to; the logits themselves for a gradient in place."""
+    pack = _need_pack(pack)
+    n = pack.total
+    ld = _logits2d(logits, "logits", n)
+    _need(targets, "targets", torch.int32, n)
+    if not isinstance(fwd, PreferenceForward):
+        raise TypeError(f"fwd: expected a PreferenceForward, got {type(fwd).__name__}")
+    _need(fwd.row_stats, "row_stats", torch.float32, 4 * n)
+    _need(fwd.coef, "coef", torch.float32, pack.n_seqs)
+    ld_d = _grad_rows(out, logits, n) if out is not None else logits.shape[1]
+    with _On(pack.device, stream, logits=logits, targets=targets, row_stats=fwd.row_stats, coef=fwd.coef,
+             out=out) as s:
+        if out is None:
+            out = torch.empty(n, ld_d, dtype=torch.bfloat16, device=pack.device)
+        if n:
+            o = B.PreferenceOut(None, None, None, fwd.coef.data_ptr(), None, fwd.row_stats.data_ptr())
+            t = B.Logits(logits.data_ptr(), ld, logits.shape[1], targets.data_ptr())
+            B.call("nf4ls_preference_bwd", pack._ref, ctypes.byref(t), ctypes.byref(o), grad_scale, _p(out), ld_d, s)
+    return out
+
+
+def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Tensor, ref_logp: torch.Tensor | None,
+                advantages: torch.Tensor, weights: torch.Tensor, clip_low: float, clip_high: float,
+                kl_coef: float = 0.0, grad: bool = True, grad_scale: float = 1.0, out: torch.Tensor | None = None,
+                stream=None):
+    """Clipped policy loss with a KL term over the rows with a target -> (loss [1], logp
+    [rows], dlogits bf16 [rows, vocab] or None without grad).  old_logp, ref_logp,
+    advantages, weights: fp32 [rows] (ref_logp None when kl_coef is 0); the weights carry the
+    normalisation, for instance 1 / the number of rows with a target.  out: rows to write the
+    gradient to; the logits themselves for a gradient in place."""
+    _need(targets, "targets", torch.int32)
+    n = targets.numel()
+    ld = _logits2d(logits, "logits", n)
+    rows = {"old_logp": old_logp, "ref_logp": ref_logp, "advantages": advantages, "weights": weights}
+    for name, t in rows.items():
+        if t is None and name == "ref_logp" and kl_coef == 0.0:
+            continue
+        _need(t, name, torch.float32, n)
+    if out is not None and not grad:
+        raise ValueError("out: without grad there is no gradient to write")
+    ld_d = _grad_rows(out, logits, n) if out is not None else logits.shape[1]
+    cfg = B.PolicyCfg(clip_low, clip_high, kl_coef, grad_scale)
+    with _On(logits.device, stream, logits=logits, targets=targets, out=out, **rows) as s:
+        buf = torch.empty(2 * n + 1, dtype=torch.float32, device=logits.device)
+        logp, row_loss, loss = buf.split((n, n, 1))
+        if grad and out is None:
+            out = torch.empty(n, ld_d, dtype=torch.bfloat16, device=logits.device)
+        t = B.Logits(logits.data_ptr(), ld, logits.shape[1], targets.data_ptr())
+        r = B.PolicyRows(old_logp.data_ptr(), 0 if ref_logp is None else ref_logp.data_ptr(), advantages.data_ptr(),
+                         weights.data_ptr())
+        B.call("nf4ls_policy_loss", ctypes.byref(cfg), n, ctypes.byref(t), ctypes.byref(r), loss.data_ptr(),
+               logp.data_ptr(), row_loss.data_ptr(), _p(out), ld_d, s)
+    return loss, logp, out
+
+
 # ----------------------------------------------------------------------------- streaming pool
 
 class Pool:

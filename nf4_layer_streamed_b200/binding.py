@@ -91,6 +91,39 @@ class PackedAttention(ctypes.Structure):
                [("ld_" + n, ctypes.c_int32) for n in ("q", "k", "v", "o", "do", "dq", "dk", "dv")]
 
 
+class RopeCfg(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("original", ctypes.c_double)]
+
+
+class RopeRows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("turns_dev", "positions_dev", "q", "k", "q_out", "k_out")] + \
+               [(n, ctypes.c_int32) for n in ("rows", "n_q", "n_kv", "ld_q", "ld_k", "ld_q_out", "ld_k_out",
+                                              "inverse")] + [("mscale", ctypes.c_float)]
+
+
+class Logits(ctypes.Structure):
+    _fields_ = [("logits_dev", ctypes.c_void_p), ("ld", ctypes.c_int64), ("vocab", ctypes.c_int32),
+                ("targets_dev", ctypes.c_void_p)]
+
+
+class PreferenceCfg(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("beta", ctypes.c_float), ("label_smoothing", ctypes.c_float)]
+
+
+class PreferenceOut(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("loss", "seq_logp", "margin", "coef", "logp", "row_stats")]
+
+
+class PolicyCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_float) for n in ("clip_low", "clip_high", "kl_coef", "grad_scale")]
+
+
+class PolicyRows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("old_logp", "ref_logp", "advantages", "weights")]
+
+
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
 SZ = ctypes.c_size_t
@@ -174,6 +207,14 @@ SIGNATURES = {
                                                   ctypes.POINTER(PackedAttention), P]),
     "nf4ls_packed_attention_bwd": (ctypes.c_int, [ctypes.POINTER(Pack), ctypes.POINTER(PackedHeads),
                                                   ctypes.POINTER(PackedAttention), P, SZ, P]),
+    "nf4ls_rope_table": (ctypes.c_int, [ctypes.POINTER(RopeCfg), P, ctypes.POINTER(ctypes.c_float)]),
+    "nf4ls_rope_apply": (ctypes.c_int, [ctypes.POINTER(RopeCfg), ctypes.POINTER(RopeRows), P]),
+    "nf4ls_preference_fwd": (ctypes.c_int, [ctypes.POINTER(Pack), ctypes.POINTER(PreferenceCfg),
+                                            ctypes.POINTER(Logits), P, ctypes.POINTER(PreferenceOut), P]),
+    "nf4ls_preference_bwd": (ctypes.c_int, [ctypes.POINTER(Pack), ctypes.POINTER(Logits),
+                                            ctypes.POINTER(PreferenceOut), ctypes.c_float, P, ctypes.c_int64, P]),
+    "nf4ls_policy_loss": (ctypes.c_int, [ctypes.POINTER(PolicyCfg), I32, ctypes.POINTER(Logits),
+                                         ctypes.POINTER(PolicyRows), P, P, P, P, ctypes.c_int64, P]),
 }
 
 _LIB = None

@@ -1,0 +1,445 @@
+// Losses of preference and policy training on token logits, with the gradient of the logits.
+//
+// Both are functions of the log probability of each row's target token,
+//   logp_t = x[target] - max - log(sum exp(x - max)),
+// so the gradient of a row of logits is a coefficient times (onehot - softmax):
+//   preference: the coefficient is that of the row's sequence, known only after every row of
+//     both sequences of the pair: one pass that reads the logits for the statistics, one
+//     that reads them again and writes the gradient;
+//   policy: the coefficient follows from the row alone: statistics and gradient in one launch.
+// What bounds them is memory: rows of up to 128 k logits are read and written once per pass.
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace nf4ls {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int LT = 512;  // threads of a row's block
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// (m, s): the maximum of some values and the sum of exp(value - m); s = 0 and m = -inf for
+// none.  Values of -inf (masked tokens) add nothing; NaN and +inf make s NaN.
+struct Stat {
+  float m, s;
+};
+__device__ __forceinline__ float safe_ref(float m) { return m == -INFINITY ? 0.0f : m; }
+__device__ __forceinline__ Stat merge(Stat a, Stat b) {
+  const float m = fmaxf(a.m, b.m), ref = safe_ref(m);
+  return {m, a.s * exp2_fast((a.m - ref) * kLog2e) + b.s * exp2_fast((b.m - ref) * kLog2e)};
+}
+
+// The difference to the maximum is taken before the scaling by log2(e): a row whose values
+// are all the type's lowest would overflow the other way round.
+__device__ __forceinline__ void add8(Stat& st, const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  float x[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[2 * k] = bf16_lo(w[k]);
+    x[2 * k + 1] = bf16_hi(w[k]);
+  }
+  const float cm = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+  if (cm > st.m) {
+    st.s *= exp2_fast((st.m - cm) * kLog2e);
+    st.m = cm;
+  }
+  const float ref = safe_ref(st.m);
+  float e[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) e[k] = exp2_fast((x[k] - ref) * kLog2e);
+  st.s += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+}
+__device__ __forceinline__ void add1(Stat& st, float x) {
+  if (x > st.m) {
+    st.s *= exp2_fast((st.m - x) * kLog2e);
+    st.m = x;
+  }
+  st.s += exp2_fast((x - safe_ref(st.m)) * kLog2e);
+}
+
+// A row of V bf16 values: `head` of them before the first 16-byte boundary, n16 pieces of
+// eight, then a tail.
+struct RowSplit {
+  int head, n16, tail0;
+  __device__ RowSplit(const __nv_bfloat16* row, int V) {
+    head = min(V, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / 2);
+    n16 = (V - head) / 8;
+    tail0 = head + n16 * 8;
+  }
+};
+
+// Statistics of a row by the whole block (fixed order: reruns give the same bits).
+__device__ __forceinline__ Stat block_stats(const __nv_bfloat16* row, int V) {
+  __shared__ Stat red[LT / 32];
+  const int t = threadIdx.x;
+  const RowSplit sp(row, V);
+  Stat st = {-INFINITY, 0.0f};
+  if (t < sp.head) add1(st, __bfloat162float(row[t]));
+  const uint4* v = reinterpret_cast<const uint4*>(row + sp.head);
+  int j = t;
+  for (; j + 3 * LT < sp.n16; j += 4 * LT) {
+    const uint4 a = v[j], b = v[j + LT], c = v[j + 2 * LT], d = v[j + 3 * LT];
+    add8(st, a);
+    add8(st, b);
+    add8(st, c);
+    add8(st, d);
+  }
+  for (; j < sp.n16; j += LT) add8(st, v[j]);
+  if (sp.tail0 + t < V) add1(st, __bfloat162float(row[sp.tail0 + t]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    st = merge(st, {__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o)});
+  if ((t & 31) == 0) red[t >> 5] = st;
+  __syncthreads();
+  st = red[0];
+  for (int i = 1; i < LT / 32; ++i) st = merge(st, red[i]);
+  return st;
+}
+
+// out = coef (onehot(target) - exp(x - m) / s) for the row; in may be out.
+__device__ __forceinline__ void block_grad(const __nv_bfloat16* in, __nv_bfloat16* out, int V, Stat st, int target,
+                                           float coef) {
+  const int t = threadIdx.x;
+  const float ref = safe_ref(st.m), k = -coef / st.s;
+  auto g = [&](float x, int i) {
+    const float v = exp2_fast((x - ref) * kLog2e) * k;
+    return i == target ? v + coef : v;
+  };
+  const RowSplit sp(in, V);
+  if (((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
+    // rows that start at different places within 16 bytes: element by element
+    for (int i = t; i < V; i += LT) out[i] = __float2bfloat16_rn(g(__bfloat162float(in[i]), i));
+    return;
+  }
+  if (t < sp.head) out[t] = __float2bfloat16_rn(g(__bfloat162float(in[t]), t));
+  const uint4* v = reinterpret_cast<const uint4*>(in + sp.head);
+  uint4* o = reinterpret_cast<uint4*>(out + sp.head);
+  auto piece = [&](const uint4& u, int j) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const int i0 = sp.head + j * 8;
+    uint32_t r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = pack_bf16x2(g(bf16_lo(w[e]), i0 + 2 * e), g(bf16_hi(w[e]), i0 + 2 * e + 1));
+    o[j] = make_uint4(r[0], r[1], r[2], r[3]);
+  };
+  int j = t;
+  for (; j + 3 * LT < sp.n16; j += 4 * LT) {
+    const uint4 a = v[j], b = v[j + LT], c = v[j + 2 * LT], d = v[j + 3 * LT];
+    piece(a, j);
+    piece(b, j + LT);
+    piece(c, j + 2 * LT);
+    piece(d, j + 3 * LT);
+  }
+  for (; j < sp.n16; j += LT) piece(v[j], j);
+  const int i = sp.tail0 + t;
+  if (i < V) out[i] = __float2bfloat16_rn(g(__bfloat162float(in[i]), i));
+}
+
+__device__ __forceinline__ void block_zero(__nv_bfloat16* out, int V) {
+  const RowSplit sp(out, V);
+  const int t = threadIdx.x;
+  if (t < sp.head) out[t] = __float2bfloat16_rn(0.f);
+  uint4* o = reinterpret_cast<uint4*>(out + sp.head);
+  for (int j = t; j < sp.n16; j += LT) o[j] = make_uint4(0u, 0u, 0u, 0u);
+  if (sp.tail0 + t < V) out[sp.tail0 + t] = __float2bfloat16_rn(0.f);
+}
+
+// x[target] and m are bf16 values: the difference and the logarithm in 64 bits lose
+// nothing that sums over long sequences would miss.
+__device__ __forceinline__ double target_logp(float xt, Stat st) {
+  return (double)xt - (double)st.m - log((double)st.s);
+}
+
+__global__ void __launch_bounds__(LT) k_token_logp(const __nv_bfloat16* __restrict__ logits, int64_t ld, int V,
+                                                   const int32_t* __restrict__ targets, float4* __restrict__ stats,
+                                                   float* __restrict__ logp) {
+  const int row = blockIdx.x;
+  const int target = targets[row];
+  if (target < 0 || target >= V) {
+    if (threadIdx.x == 0) {
+      stats[row] = make_float4(0.f, 1.f, 0.f, 0.f);
+      logp[row] = 0.f;
+    }
+    return;
+  }
+  const __nv_bfloat16* x = logits + (size_t)row * ld;
+  const Stat st = block_stats(x, V);
+  if (threadIdx.x == 0) {
+    const double lp = target_logp(__bfloat162float(x[target]), st);
+    const float hi = (float)lp;
+    // what the rounding of logp leaves out, for the sums over a sequence
+    stats[row] = make_float4(st.m, st.s, isfinite(hi) ? (float)(lp - (double)hi) : 0.f, 0.f);
+    logp[row] = hi;
+  }
+}
+
+// One block: sums of each sequence's log probabilities (a warp per sequence, in 64 bits),
+// then every pair's loss and the coefficients of its two sequences.
+constexpr int PT = 1024;
+__global__ void __launch_bounds__(PT) k_preference(const int32_t* __restrict__ cu, int n_seqs,
+                                                   const float* __restrict__ logp, const float4* __restrict__ stats,
+                                                   const float* __restrict__ ref_logp,
+                                                   float beta, float smoothing, int kind, float* __restrict__ seq_logp,
+                                                   float* __restrict__ margin, float* __restrict__ coef,
+                                                   float* __restrict__ loss) {
+  __shared__ double red[PT / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_pairs = n_seqs / 2;
+  double total = 0.0;
+  for (int pair = warp; pair < n_pairs; pair += PT / 32) {
+    double sum[2];
+    for (int e = 0; e < 2; ++e) {
+      const int a = cu[2 * pair + e], b = cu[2 * pair + e + 1];
+      double v = 0.0;
+      for (int i = a + lane; i < b; i += 32) v += (double)logp[i] + (double)stats[i].z;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      sum[e] = v;
+    }
+    if (lane == 0) {
+      const double gap = (sum[0] - sum[1]) - ((double)ref_logp[2 * pair] - (double)ref_logp[2 * pair + 1]);
+      const double h = (double)beta * gap;
+      double l, slope;  // of this pair's loss, and its derivative by gap
+      if (kind == NF4LS_PREF_SIGMOID) {
+        // -log sigmoid(h) = max(-h, 0) + log1p(exp(-|h|)); sigmoid(-h) without overflow
+        const double e = exp(-fabs(h)), soft = log1p(e);
+        const double away = h >= 0.0 ? e / (1.0 + e) : 1.0 / (1.0 + e);  // sigmoid(-h)
+        l = (1.0 - smoothing) * (fmax(-h, 0.0) + soft) + smoothing * (fmax(h, 0.0) + soft);
+        slope = beta * (smoothing * (1.0 - away) - (1.0 - smoothing) * away);
+        if (isnan(h)) l = slope = h;
+      } else if (kind == NF4LS_PREF_HINGE) {
+        l = h < 1.0 ? 1.0 - h : 0.0;
+        slope = h < 1.0 ? -(double)beta : 0.0;
+        if (isnan(h)) l = slope = h;
+      } else {
+        const double z = gap - 0.5 / (double)beta;
+        l = z * z;
+        slope = 2.0 * z;
+      }
+      total += l;
+      seq_logp[2 * pair] = (float)sum[0];
+      seq_logp[2 * pair + 1] = (float)sum[1];
+      margin[pair] = (float)h;
+      coef[2 * pair] = (float)(slope / n_pairs);
+      coef[2 * pair + 1] = (float)(-slope / n_pairs);
+    }
+  }
+  if (lane == 0) red[warp] = total;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double v = 0.0;
+    for (int i = 0; i < PT / 32; ++i) v += red[i];
+    *loss = (float)(v / n_pairs);
+  }
+}
+
+__global__ void __launch_bounds__(LT) k_logits_grad(const __nv_bfloat16* logits, int64_t ld, int V,
+                                                    const int32_t* __restrict__ targets,
+                                                    const float4* __restrict__ stats, const int32_t* __restrict__ seq,
+                                                    const float* __restrict__ coef, float scale, __nv_bfloat16* dlogits,
+                                                    int64_t ld_d) {
+  const int row = blockIdx.x;
+  const int target = targets[row];
+  __nv_bfloat16* out = dlogits + (size_t)row * ld_d;
+  const float c = target >= 0 && target < V ? coef[seq[row]] * scale : 0.0f;
+  if (c == 0.0f) {
+    block_zero(out, V);
+    return;
+  }
+  const float4 st = stats[row];
+  block_grad(logits + (size_t)row * ld, out, V, {st.x, st.y}, target, c);
+}
+
+struct PolicyParams {
+  const __nv_bfloat16* logits;
+  __nv_bfloat16* dlogits;
+  int64_t ld, ld_d;
+  int V;
+  const int32_t* targets;
+  const float *old_logp, *ref_logp, *adv, *weights;
+  float clip_low, clip_high, kl, scale;
+  float *logp, *row_loss;
+};
+
+__global__ void __launch_bounds__(LT) k_policy(const PolicyParams p) {
+  __shared__ float c_sh;
+  const int row = blockIdx.x;
+  const int target = p.targets[row];
+  __nv_bfloat16* out = p.dlogits ? p.dlogits + (size_t)row * p.ld_d : nullptr;
+  if (target < 0 || target >= p.V) {
+    if (threadIdx.x == 0) {
+      p.logp[row] = 0.f;
+      p.row_loss[row] = 0.f;
+    }
+    if (out) block_zero(out, p.V);
+    return;
+  }
+  const __nv_bfloat16* x = p.logits + (size_t)row * p.ld;
+  const Stat st = block_stats(x, p.V);
+  if (threadIdx.x == 0) {
+    const double lp = target_logp(__bfloat162float(x[target]), st);
+    const float a = p.adv[row], w = p.weights[row];
+    const float r = expf((float)(lp - (double)p.old_logp[row]));
+    const float held_r = fminf(fmaxf(r, 1.0f - p.clip_low), 1.0f + p.clip_high);
+    const float free_s = r * a, held = held_r * a;
+    const bool passes = free_s <= held;  // the gradient flows through the unclipped term
+    // no KL term where its coefficient is 0 (ref_logp may then be null)
+    const float gap = p.kl > 0.0f ? (float)((double)p.ref_logp[row] - lp) : 0.0f, e1 = expm1f(gap);
+    const float surrogate = isnan(r) ? r : (passes ? free_s : held);
+    p.logp[row] = (float)lp;
+    p.row_loss[row] = w * (p.kl * (e1 - gap) - surrogate);
+    c_sh = w * (-p.kl * e1 - (passes ? free_s : 0.0f)) * p.scale;
+  }
+  if (!out) return;
+  __syncthreads();
+  const float c = c_sh;
+  if (c == 0.0f)
+    block_zero(out, p.V);
+  else
+    block_grad(x, out, p.V, st, target, c);
+}
+
+__global__ void __launch_bounds__(PT) k_sum_rows(const float* __restrict__ v, int n, float* __restrict__ out) {
+  __shared__ double red[PT / 32];
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += PT) s += (double)v[i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+    for (int i = 0; i < PT / 32; ++i) t += red[i];
+    *out = (float)t;
+  }
+}
+
+int check_logits(const nf4ls_logits* t, int rows, const char* who) {
+  if (!t) return fail(NF4LS_INVALID_ARG, "%s: null logits", who);
+  if (t->vocab < 1 || t->vocab > (1 << 28)) return fail(NF4LS_SHAPE, "%s: vocab %d", who, t->vocab);
+  if (t->ld < t->vocab || t->ld > (1ll << 40)) return fail(NF4LS_SHAPE, "%s: row stride %lld < vocab %d", who, (long long)t->ld, t->vocab);
+  if (rows > 0 && (!t->logits_dev || !t->targets_dev)) return fail(NF4LS_INVALID_ARG, "%s: null logits or targets", who);
+  if (!aligned(t->logits_dev, 2) || !aligned(t->targets_dev, 4)) return fail(NF4LS_ALIGN, "%s: misaligned logits or targets", who);
+  return NF4LS_OK;
+}
+
+int check_grad(const nf4ls_logits* t, const void* d, int64_t ld, const char* who) {
+  if (ld < t->vocab || ld > (1ll << 40)) return fail(NF4LS_SHAPE, "%s: row stride %lld of the gradient", who, (long long)ld);
+  if (!aligned(d, 2)) return fail(NF4LS_ALIGN, "%s: misaligned gradient", who);
+  if (d == t->logits_dev && ld != t->ld) return fail(NF4LS_INVALID_ARG, "%s: in place with another row stride", who);
+  return NF4LS_OK;
+}
+
+}  // namespace
+
+}  // namespace nf4ls
+
+using namespace nf4ls;
+
+extern "C" int nf4ls_preference_fwd(const nf4ls_pack* pack, const nf4ls_preference_cfg* c, const nf4ls_logits* t,
+                                    const float* ref_logp_dev, const nf4ls_preference_out* out, nf4ls_stream stream) {
+  const char* who = "nf4ls_preference_fwd";
+  clear_error();
+  NF4_TRY(check_pack(pack, who));
+  if (!c || !out) return fail(NF4LS_INVALID_ARG, "%s: null config or outputs", who);
+  if (pack->n_seqs % 2) return fail(NF4LS_SHAPE, "%s: %d sequences are not pairs", who, pack->n_seqs);
+  if (c->kind < NF4LS_PREF_SIGMOID || c->kind > NF4LS_PREF_SQUARED) return fail(NF4LS_INVALID_ARG, "%s: unknown kind %d", who, c->kind);
+  if (!(c->beta > 0.0f) || !std::isfinite(c->beta)) return fail(NF4LS_INVALID_ARG, "%s: beta must be positive", who);
+  if (!(c->label_smoothing >= 0.0f && c->label_smoothing < 0.5f))
+    return fail(NF4LS_INVALID_ARG, "%s: label_smoothing outside [0, 0.5)", who);
+  if (c->label_smoothing != 0.0f && c->kind != NF4LS_PREF_SIGMOID)
+    return fail(NF4LS_INVALID_ARG, "%s: label_smoothing belongs to the sigmoid loss", who);
+  NF4_TRY(check_logits(t, pack->total, who));
+  if (!ref_logp_dev || !out->loss || !out->seq_logp || !out->margin || !out->coef ||
+      (pack->total > 0 && (!out->logp || !out->row_stats)))
+    return fail(NF4LS_INVALID_ARG, "%s: null reference or output", who);
+  if (!aligned(out->row_stats, 16)) return fail(NF4LS_ALIGN, "%s: row_stats must be 16-byte aligned", who);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (pack->total > 0) {
+    k_token_logp<<<(unsigned)pack->total, LT, 0, s>>>(static_cast<const __nv_bfloat16*>(t->logits_dev), t->ld, t->vocab,
+                                                      t->targets_dev, reinterpret_cast<float4*>(out->row_stats),
+                                                      out->logp);
+    note_launch();
+    NF4_CUDA_TRY(cudaGetLastError());
+  }
+  const int32_t* cu = reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(pack->plan_dev) + pack->off_cu);
+  k_preference<<<1, PT, 0, s>>>(cu, pack->n_seqs, out->logp, reinterpret_cast<const float4*>(out->row_stats), ref_logp_dev, c->beta, c->label_smoothing, c->kind,
+                                out->seq_logp, out->margin, out->coef, out->loss);
+  note_launch();
+  NF4_CUDA_TRY(cudaGetLastError());
+  return NF4LS_OK;
+}
+
+extern "C" int nf4ls_preference_bwd(const nf4ls_pack* pack, const nf4ls_logits* t, const nf4ls_preference_out* saved,
+                                    float grad_scale, void* dlogits_dev, int64_t ld_d, nf4ls_stream stream) {
+  const char* who = "nf4ls_preference_bwd";
+  clear_error();
+  NF4_TRY(check_pack(pack, who));
+  NF4_TRY(check_logits(t, pack->total, who));
+  if (pack->total == 0) return NF4LS_OK;
+  if (!saved || !saved->row_stats || !saved->coef || !dlogits_dev) return fail(NF4LS_INVALID_ARG, "%s: null argument", who);
+  if (!aligned(saved->row_stats, 16)) return fail(NF4LS_ALIGN, "%s: row_stats must be 16-byte aligned", who);
+  NF4_TRY(check_grad(t, dlogits_dev, ld_d, who));
+  const int32_t* seq = reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(pack->plan_dev) + pack->off_seq);
+  k_logits_grad<<<(unsigned)pack->total, LT, 0, static_cast<cudaStream_t>(stream)>>>(
+      static_cast<const __nv_bfloat16*>(t->logits_dev), t->ld, t->vocab, t->targets_dev,
+      reinterpret_cast<const float4*>(saved->row_stats), seq, saved->coef, grad_scale,
+      static_cast<__nv_bfloat16*>(dlogits_dev), ld_d);
+  note_launch();
+  NF4_CUDA_TRY(cudaGetLastError());
+  return NF4LS_OK;
+}
+
+extern "C" int nf4ls_policy_loss(const nf4ls_policy_cfg* c, int32_t rows, const nf4ls_logits* t, const nf4ls_policy_rows* in,
+                                 float* loss_dev, float* logp_dev, float* row_loss_dev, void* dlogits_dev, int64_t ld_d,
+                                 nf4ls_stream stream) {
+  const char* who = "nf4ls_policy_loss";
+  clear_error();
+  if (!c || !loss_dev) return fail(NF4LS_INVALID_ARG, "%s: null config or loss", who);
+  if (rows < 0) return fail(NF4LS_INVALID_ARG, "%s: %d rows", who, rows);
+  if (!(c->clip_low >= 0.0f && c->clip_low <= 1.0f) || !(c->clip_high >= 0.0f) || !std::isfinite(c->clip_high))
+    return fail(NF4LS_INVALID_ARG, "%s: clip range %g, %g", who, c->clip_low, c->clip_high);
+  if (!(c->kl_coef >= 0.0f) || !std::isfinite(c->kl_coef)) return fail(NF4LS_INVALID_ARG, "%s: kl_coef %g", who, c->kl_coef);
+  if (!std::isfinite(c->grad_scale)) return fail(NF4LS_INVALID_ARG, "%s: grad_scale %g", who, c->grad_scale);
+  NF4_TRY(check_logits(t, rows, who));
+  if (rows > 0 && (!in || !in->old_logp || (c->kl_coef > 0.0f && !in->ref_logp) || !in->advantages || !in->weights || !logp_dev || !row_loss_dev))
+    return fail(NF4LS_INVALID_ARG, "%s: null row argument", who);
+  if (dlogits_dev) NF4_TRY(check_grad(t, dlogits_dev, ld_d, who));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows > 0) {
+    PolicyParams p;
+    p.logits = static_cast<const __nv_bfloat16*>(t->logits_dev);
+    p.dlogits = static_cast<__nv_bfloat16*>(dlogits_dev);
+    p.ld = t->ld;
+    p.ld_d = ld_d;
+    p.V = t->vocab;
+    p.targets = t->targets_dev;
+    p.old_logp = in->old_logp;
+    p.ref_logp = in->ref_logp;
+    p.adv = in->advantages;
+    p.weights = in->weights;
+    p.clip_low = c->clip_low;
+    p.clip_high = c->clip_high;
+    p.kl = c->kl_coef;
+    p.scale = c->grad_scale;
+    p.logp = logp_dev;
+    p.row_loss = row_loss_dev;
+    k_policy<<<(unsigned)rows, LT, 0, s>>>(p);
+    note_launch();
+    NF4_CUDA_TRY(cudaGetLastError());
+  }
+  k_sum_rows<<<1, PT, 0, s>>>(row_loss_dev, rows, loss_dev);
+  note_launch();
+  NF4_CUDA_TRY(cudaGetLastError());
+  return NF4LS_OK;
+}
