@@ -80,7 +80,7 @@ int nf4ls_profile_read(int sel, double out[3]);
 int nf4ls_profile_reset(void);
 
 /* Reads and clears the device error flag of the current device: out[0] = code
- * (0 none, 1 barrier timeout), out[1] = kernel id, out[2] = block, out[3] = site.
+ * (0 none, 1 barrier timeout, 2 shared memory not laid out as the kernel needs), out[1] = kernel id, out[2] = block, out[3] = site.
  * Synchronises the device. */
 int nf4ls_device_error(int32_t out[4]);
 

@@ -299,36 +299,100 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
 }
 
 // ------------------------------------------------------------------------------ backward
-// warps 0-7: elementwise and epilogue (warp w: TMEM lane quarter w % 4, column half
-// w / 4); warp 8: TMA producer; warp 9: MMA issuer
+// dQ (per query tile and head) and dK, dV (per key tile and kv head), one 128 x 128 block
+// ("item") at a time:
+//   query side, item = one key tile:   S = Q K^T, dP = dO V^T; then dQ += dS K;
+//   key side, item = one query tile:   S^T = K Q^T, dP^T = V dO^T; then dV += P^T dO and
+//     dK += dS^T Q,
+// P = 2^(S scale log2e - lse log2e), dS = P (dP - delta).  P and dS are written back as bf16
+// (two per 32-bit column) over the scores they came from and are the A operand of their
+// products from TMEM.  S, dP and the accumulators fill TMEM, so no second item fits
+// beside them; what keeps the tensor core busy is the order of the products within the
+// one that is there:
+//   query side:  S(i+1) | dQ(i) | dP(i+1)          key side:  dV(i) | S(i+1) | dK(i) | dP(i+1)
+// The exponentials of item i + 1 need only S(i+1) and run under the two products behind
+// it, and dS(i), which needs dP(i), under the product behind that.  The tiles come
+// through two rings: those that the first and the last product of an item read (K; Q)
+// live longest and have three stages, the others (V; dO) two.
+// The query side also forms delta = rowsum(dO * O) and writes it beside lse log2e for the
+// key side, which runs after it.  Accumulation runs in a fixed order (query side: key
+// tiles in order; key side: query heads of the group, then query tiles), so results are
+// bit-reproducible.
+
+// warps 0-7: elementwise and epilogue (warp w: TMEM lane quarter w % 4, columns 64 (w / 4) ..
+// of a block); warp 8: TMA producer; warp 9: MMA issuer
 constexpr int B_THREADS = 320, B_PROD = 8, B_MMA = 9, B_EW = 256;
 constexpr int B_OFF_A = 0;                              // Q, dO (query side) or K, V (key side)
-constexpr int B_OFF_RING = 2 * TILE_BYTES;              // 2 stages x (two 32 KB tiles)
-constexpr int B_OFF_X = B_OFF_RING + 4 * TILE_BYTES;    // query side: O tile and delta halves [2][128];
-                                                        // key side: 2 stages x (128 lse + 128 delta floats)
-constexpr int B_OFF_BAR = B_OFF_X + TILE_BYTES + 1024;
-constexpr int SMEM_BWD = 1024 + B_OFF_BAR + 256;
+constexpr int B_OFF_R3 = 2 * TILE_BYTES;                // 3 stages: K (query side) or Q (key side)
+constexpr int B_OFF_R2 = B_OFF_R3 + 3 * TILE_BYTES;     // 2 stages: V (query side) or dO (key side)
+constexpr int B_OFF_X = B_OFF_R2 + 2 * TILE_BYTES;      // query side: delta halves [2][128]; key side: 2 stages
+                                                        // x (128 lse + 128 delta floats)
+constexpr int B_OFF_BAR = B_OFF_X + 2048;
+constexpr int SMEM_BWD = 232448;  // all of it: what lies behind the barriers is slack for the alignment
+static_assert(B_OFF_BAR + 256 + 512 <= SMEM_BWD, "shared memory of the packed attention backward");
 
 __device__ __forceinline__ void bar_ew() { asm volatile("bar.sync 1, %0;" ::"n"(B_EW) : "memory"); }
 
+// The 1024-byte aligned start of the shared memory; false where the slack does not hold it
+// (recorded, the same for every thread and block).
+__device__ __forceinline__ bool smem_base(uint8_t* raw, uint8_t** base, int* err) {
+  *base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  if (*base - raw + B_OFF_BAR + 256 <= SMEM_BWD) return true;
+  if (threadIdx.x == 0) record_error(err, 2, KID_PACKED, 1);
+  return false;
+}
+
+// (a0, a1) * (b0, b1) + (c0, c1) and its parts, two to an instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  return (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32);
+}
+__device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) { return (uint64_t)a | ((uint64_t)b << 32); }
+
+// QUERY side: dQ of one query tile of one head.  The Q and dO tiles are copied into TMEM
+// (bf16 pairs, one query row per lane), so that S and dP read only K and V from shared
+// memory (4 KB per 64 tensor-core cycles instead of 8 KB, which is all that shared memory
+// delivers, while the next tiles land in it).
 template <int D>
 __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constant__ BwdParams p) {
-  // swizzle atoms, k-steps and bytes of a Q / dO / O / K / V tile; dims per column half
+  // swizzle atoms, k-steps and bytes of a tile; dims per column half
   constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM, DH = D / 2;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* base;
+  if (!smem_base(smem_raw, &base, p.err)) return;
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + B_OFF_BAR);
-  uint64_t* q_full = bars;          // Q, dO (copied into TMEM first)
-  uint64_t* kv_full = bars + 1;     // 2 stages
-  uint64_t* kv_empty = bars + 3;    // 2
-  uint64_t* sd_full = bars + 5;     // S and dP of the item are in TMEM
-  uint64_t* p_half = bars + 6;      // 2: dS chunk hc of the item is in TMEM (one arrival per warp)
-  uint64_t* acc_full = bars + 9;
-  uint64_t* drain = bars + 10;
-  uint64_t* qa_full = bars + 11;    // Q and dO are in TMEM (one arrival per elementwise warp)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 12);
+  uint64_t* q_full = bars;          // Q, dO
+  uint64_t* o_full = bars + 1;      // the O tile (for delta), in the third K stage
+  uint64_t* o_read = bars + 2;      // ... and it has been read (one arrival per elementwise warp)
+  uint64_t* qa_full = bars + 3;     // Q and dO are in TMEM (one arrival per elementwise warp)
+  uint64_t* k_full = bars + 4;      // 3
+  uint64_t* k_empty = bars + 7;     // 3
+  uint64_t* v_full = bars + 10;     // 2
+  uint64_t* v_empty = bars + 12;    // 2
+  uint64_t* s_full = bars + 14;
+  uint64_t* s_read = bars + 15;     // S is in registers (one arrival per elementwise warp)
+  uint64_t* dp_full = bars + 16;
+  uint64_t* ds_full = bars + 17;    // dS is in TMEM (one arrival per elementwise warp)
+  uint64_t* acc_full = bars + 18;
+  uint64_t* drain = bars + 19;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint64_t* o_full = bars + 13;     // the O tile (for delta)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.x % p.nq;
@@ -341,16 +405,22 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(o_full, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+    mbar_init(o_read, B_EW / 32);
+    mbar_init(qa_full, B_EW / 32);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
     }
-    mbar_init(sd_full, 1);
-    mbar_init(&p_half[0], B_EW / 32);
-    mbar_init(&p_half[1], B_EW / 32);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_read, B_EW / 32);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, B_EW / 32);
     mbar_init(acc_full, 1);
     mbar_init(drain, 1);
-    mbar_init(qa_full, B_EW / 32);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -361,9 +431,8 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // S [0,128), dP [128,256) (dS packed over it), dQ [256,384), Q [384,448), dO [448,512)
   const uint32_t tmem = *tmem_slot;
-  constexpr uint32_t T_Q = 384, T_DO = 448;
+  constexpr uint32_t T_S = 0, T_DP = 128, T_DQ = 256, T_Q = 384, T_DO = 448;  // dS packed over dP
 
   if (warp == B_PROD) {
     if (lane == 0) {
@@ -377,89 +446,110 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
         tma_load_2d(base + B_OFF_A + j * ATOM, &p.tq, q_full, h * D + 64 * j, row0 + qt * TT);
         tma_load_2d(base + B_OFF_A + TILE_BYTES + j * ATOM, &p.tdo, q_full, h * D + 64 * j, row0 + qt * TT);
       }
-      mbar_arrive_expect_tx(o_full, TB);
-      for (int j = 0; j < NA; ++j)
-        tma_load_2d(base + B_OFF_X + j * ATOM, &p.to, o_full, h * D + 64 * j, row0 + qt * TT);
-      int issued = 0;
+      int issued_k = 0, issued_v = 0;
       for (int kt = 0; kt < n_kt; ++kt) {
-        const int st = kt & 1;
-        if (kt >= 2 && !mbar_wait(&kv_empty[st], ((kt >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 41)) break;
-        uint8_t* buf = base + B_OFF_RING + st * 2 * TILE_BYTES;
-        mbar_arrive_expect_tx(&kv_full[st], 2 * TB);
-        for (int j = 0; j < NA; ++j) {
-          tma_load_2d(buf + j * ATOM, &p.tk, &kv_full[st], kvh * D + 64 * j, row0 + kt * TT);
-          tma_load_2d(buf + TILE_BYTES + j * ATOM, &p.tv, &kv_full[st], kvh * D + 64 * j, row0 + kt * TT);
+        const int sk = kt % 3, sv = kt & 1;
+        if (kt == 2 && !mbar_wait(o_read, 0, abort_flag, p.err, KID_PACKED, 40)) break;
+        if (kt >= 3 && !mbar_wait(&k_empty[sk], (kt / 3 - 1) & 1, abort_flag, p.err, KID_PACKED, 41)) break;
+        mbar_arrive_expect_tx(&k_full[sk], TB);
+        for (int j = 0; j < NA; ++j)
+          tma_load_2d(base + B_OFF_R3 + sk * TILE_BYTES + j * ATOM, &p.tk, &k_full[sk], kvh * D + 64 * j, row0 + kt * TT);
+        issued_k = kt + 1;
+        if (kt >= 2 && !mbar_wait(&v_empty[sv], ((kt >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 42)) break;
+        mbar_arrive_expect_tx(&v_full[sv], TB);
+        for (int j = 0; j < NA; ++j)
+          tma_load_2d(base + B_OFF_R2 + sv * TILE_BYTES + j * ATOM, &p.tv, &v_full[sv], kvh * D + 64 * j, row0 + kt * TT);
+        issued_v = kt + 1;
+        if (kt == 0) {
+          mbar_arrive_expect_tx(o_full, TB);
+          for (int j = 0; j < NA; ++j)
+            tma_load_2d(base + B_OFF_R3 + 2 * TILE_BYTES + j * ATOM, &p.to, o_full, h * D + 64 * j, row0 + qt * TT);
         }
-        issued = kt + 1;
       }
       if (*abort_flag) {  // let the copies already issued land before the CTA exits
         mbar_wait_drain(q_full, 0);
-        mbar_wait_drain(o_full, 0);
-        for (int kt = (issued > 2 ? issued - 2 : 0); kt < issued; ++kt) mbar_wait_drain(&kv_full[kt & 1], (kt >> 1) & 1);
+        if (issued_v > 0) mbar_wait_drain(o_full, 0);
+        for (int i = max(0, issued_k - 3); i < issued_k; ++i) mbar_wait_drain(&k_full[i % 3], (i / 3) & 1);
+        for (int i = max(0, issued_v - 2); i < issued_v; ++i) mbar_wait_drain(&v_full[i & 1], (i >> 1) & 1);
       }
     }
   } else if (warp == B_MMA) {
     constexpr uint32_t idesc_s = idesc_bf16(128, 128, false);  // S, dP: N = 128 keys
     constexpr uint32_t idesc_a = idesc_bf16(128, D, true);     // dQ += dS K: K N-major
-    bool ok = __all_sync(0xffffffffu, mbar_wait(qa_full, 0, abort_flag, p.err, KID_PACKED, 42)) && !*abort_flag;
-    // dQ += dS_kt K_kt, each half as soon as its dS chunks are in TMEM (chunk hc holds the
-    // k-steps with ks & 2 == 2 hc); then the K/V stage is free
-    auto dq_product = [&](int kt) -> bool {
-      const uint32_t sK = smem_u32(base + B_OFF_RING + (kt & 1) * 2 * TILE_BYTES);
-      for (int hc = 0; hc < 2; ++hc) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&p_half[hc], kt & 1, abort_flag, p.err, KID_PACKED, 44))) return false;
-        tc_fence_after();
-        if (lane == 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {  // 16 keys per step
-            const int ks = (i >> 1) * 4 + hc * 2 + (i & 1);
-            umma_bf16_ta(tmem + 256, tmem + packed_col(128, ks), sdesc_sw128(sK + ks * 2048, ATOM, 1024), idesc_a,
-                         (kt | hc | i) ? 1u : 0u);
-          }
-          if (hc == 1) umma_commit(&kv_empty[kt & 1]);
-        }
-        __syncwarp();
-      }
-      return true;
-    };
-    for (int kt = 0; ok && kt < n_kt; ++kt) {
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[kt & 1], (kt >> 1) & 1, abort_flag, p.err, KID_PACKED,
-                                                   43))))
-        break;
-      // the previous item's dS is read (issue order) before S and dP overwrite it
-      if (kt >= 1 && !(ok = dq_product(kt - 1))) break;
+    const uint32_t s3 = smem_u32(base + B_OFF_R3), s2 = smem_u32(base + B_OFF_R2);
+    // every wait is agreed on by the whole warp, so that no lane goes on alone
+    auto wait = [&](uint64_t* bar, int parity, int site) -> bool {
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, abort_flag, p.err, KID_PACKED, site));
       tc_fence_after();
+      return ok;
+    };
+    auto scores = [&](int i) {  // S(i): over the head dim, Q in TMEM
       if (lane == 0) {
-        const uint32_t sK = smem_u32(base + B_OFF_RING + (kt & 1) * 2 * TILE_BYTES), sV = sK + TILE_BYTES;
+        const uint32_t sK = s3 + (i % 3) * TILE_BYTES;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {  // over the head dim: Q, dO columns 8 ks .. in TMEM
-          const uint32_t off = (ks >> 2) * ATOM + (ks & 3) * 32;
-          umma_bf16_ta(tmem, tmem + T_Q + ks * 8, sdesc_sw128(sK + off, 16, 1024), idesc_s, ks ? 1u : 0u);
-          umma_bf16_ta(tmem + 128, tmem + T_DO + ks * 8, sdesc_sw128(sV + off, 16, 1024), idesc_s, ks ? 1u : 0u);
-        }
-        umma_commit(sd_full);
+        for (int ks = 0; ks < KS; ++ks)
+          umma_bf16_ta(tmem + T_S, tmem + T_Q + ks * 8, sdesc_sw128(sK + (ks >> 2) * ATOM + (ks & 3) * 32, 16, 1024),
+                       idesc_s, ks ? 1u : 0u);
+        umma_commit(s_full);
       }
       __syncwarp();
+    };
+    auto dprobs = [&](int i) {  // dP(i)
+      if (lane == 0) {
+        const uint32_t sV = s2 + (i & 1) * TILE_BYTES;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+          umma_bf16_ta(tmem + T_DP, tmem + T_DO + ks * 8, sdesc_sw128(sV + (ks >> 2) * ATOM + (ks & 3) * 32, 16, 1024),
+                       idesc_s, ks ? 1u : 0u);
+        umma_commit(dp_full);
+        umma_commit(&v_empty[i & 1]);
+      }
+      __syncwarp();
+    };
+    bool ok = wait(qa_full, 0, 43) && !*abort_flag;
+    if (ok && (ok = wait(&k_full[0], 0, 44))) scores(0);
+    if (ok && (ok = wait(&v_full[0], 0, 45))) dprobs(0);
+    for (int i = 0; ok && i < n_kt; ++i) {
+      if (i + 1 < n_kt) {
+        if (!(ok = wait(&k_full[(i + 1) % 3], (i + 1) / 3, 44))) break;
+        if (!(ok = wait(s_read, i, 46))) break;
+        scores(i + 1);
+      }
+      if (!(ok = wait(ds_full, i, 47))) break;
+      if (lane == 0) {
+        const uint32_t sK = s3 + (i % 3) * TILE_BYTES;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)  // 16 keys per step
+          umma_bf16_ta(tmem + T_DQ, tmem + packed_col(T_DP, ks), sdesc_sw128(sK + ks * 2048, ATOM, 1024), idesc_a,
+                       (i | ks) ? 1u : 0u);
+        umma_commit(&k_empty[i % 3]);
+      }
+      __syncwarp();
+      if (i + 1 < n_kt) {
+        if (!(ok = wait(&v_full[(i + 1) & 1], (i + 1) >> 1, 45))) break;
+        dprobs(i + 1);
+      }
     }
-    if (ok) ok = dq_product(n_kt - 1);
     if (ok && lane == 0) umma_commit(acc_full);
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ elementwise + epilogue
     const int wq = warp & 3, g = warp >> 2;
     const int r = wq * 32 + lane;  // query row = TMEM lane
-    const int qpos = qt * TT + r;
     const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
     // First Q and dO into TMEM (the MMA warp starts on them), then delta = rowsum(dO * O)
     // over this thread's DH dims (dims g DH .. of its row: 16-byte chunks c0 + c of swizzle
     // atom g DH / 64 of the dO and O tiles), the two halves added through smem.  TMEM
     // column g DH / 2 + 4 c + i holds the pair i of chunk c.
-    float* red = reinterpret_cast<float*>(base + B_OFF_X + TILE_BYTES);
+    float* red = reinterpret_cast<float*>(base + B_OFF_X);
     const int atom = (g * DH) / 64, c0 = ((g * DH) % 64) / 8;
     const uint8_t* q_row = base + B_OFF_A + atom * ATOM + r * 128;
     const uint8_t* dO_row = base + B_OFF_A + TILE_BYTES + atom * ATOM + r * 128;
-    const uint8_t* o_row = base + B_OFF_X + atom * ATOM + r * 128;
-    bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag, p.err, KID_PACKED, 45));
+    const uint8_t* o_row = base + B_OFF_R3 + 2 * TILE_BYTES + atom * ATOM + r * 128;
+    // rows behind the sequence's end: no lse to read; their lanes compute values that
+    // nothing stores
+    const float lse2 = r < n_rows ? p.lse[(size_t)h * p.total + row0 + qt * TT + r] * 1.4426950408889634f : 0.f;
+    bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag, p.err, KID_PACKED, 50));
     if (ok) {
       uint32_t qv[DH / 2], dv[DH / 2];
 #pragma unroll
@@ -477,7 +567,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(qa_full);  // also on failure: the MMA warp then sees the abort
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_full, 0, abort_flag, p.err, KID_PACKED, 48));
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_full, 0, abort_flag, p.err, KID_PACKED, 51));
     if (ok) {
       float s = 0.f;
 #pragma unroll
@@ -491,73 +581,84 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
       }
       red[g * 128 + r] = s;
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(o_read);
     bar_ew();
     const float dl = ok ? red[r] + red[128 + r] : 0.f;
-    // rows behind the sequence's end: no lse to read; their lanes compute values that
-    // nothing stores
-    const float lse2 = r < n_rows ? p.lse[(size_t)h * p.total + row0 + qpos] * 1.4426950408889634f : 0.f;
     if (ok && g == 0) {
       float* st = p.stats + ((size_t)h * p.n_tiles + pt.index) * (2 * TT);
       st[r] = lse2;
       st[TT + r] = dl;
     }
-    const float sl = p.scale_log2;
+    const uint64_t sl2 = pack2(p.scale_log2, p.scale_log2), nlse2 = pack2(-lse2, -lse2), ndl2 = pack2(-dl, -dl);
     for (int kt = 0; ok && kt < n_kt; ++kt) {
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(sd_full, kt & 1, abort_flag, p.err, KID_PACKED, 46)))) break;
-      tc_fence_after();
       const bool diag = kt == qt;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full, kt & 1, abort_flag, p.err, KID_PACKED, 52)))) break;
+      tc_fence_after();
+      uint32_t sv[2][32];
+      tmem_ld32(trow + T_S + g * 64, sv[0]);
+      tmem_ld32(trow + T_S + g * 64 + 32, sv[1]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_read);
       if (diag && n_rows < TT) {
         // rows of K behind the sequence's end: zeros for the product dS K (S is done with them)
-        if (r >= n_rows && g == 0) zero_row<NA>(smem_u32(base + B_OFF_RING + (kt & 1) * 2 * TILE_BYTES), r);
+        if (r >= n_rows && g == 0) zero_row<NA>(smem_u32(base + B_OFF_R3 + (kt % 3) * TILE_BYTES), r);
         fence_proxy_async_smem();
       }
-      // both 32-key chunks in one TMEM round trip
-      uint32_t sv[2][32], dpv[2][32];
 #pragma unroll
-      for (int hc = 0; hc < 2; ++hc) {
-        tmem_ld32(trow + g * 64 + hc * 32, sv[hc]);
-        tmem_ld32(trow + 128 + g * 64 + hc * 32, dpv[hc]);
-      }
+      for (int hc = 0; hc < 2; ++hc)
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          const uint64_t x = fma2(pack2(sv[hc][j], sv[hc][j + 1]), sl2, nlse2);
+          sv[hc][j] = __float_as_uint(fast_exp2(lo2(x)));
+          sv[hc][j + 1] = __float_as_uint(fast_exp2(hi2(x)));
+        }
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(dp_full, kt & 1, abort_flag, p.err, KID_PACKED, 53)))) break;
+      tc_fence_after();
+      uint32_t dp[2][32];
+      tmem_ld32(trow + T_DP + g * 64, dp[0]);
+      tmem_ld32(trow + T_DP + g * 64 + 32, dp[1]);
       tmem_wait_ld();
 #pragma unroll
       for (int hc = 0; hc < 2; ++hc) {  // keys 64 g + 32 hc .. of the tile
         uint32_t dd[16];
-        const int last = diag ? r - (g * 64 + hc * 32) : 32;  // columns c <= last are not masked
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          float ds[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int c = 2 * j + e;
-            const float pe = fast_exp2(fmaf(__uint_as_float(sv[hc][c]), sl, -lse2));
-            ds[e] = c <= last ? pe * (__uint_as_float(dpv[hc][c]) - dl) : 0.f;
+          const uint64_t ds = mul2(pack2(sv[hc][2 * j], sv[hc][2 * j + 1]),
+                                   add2(pack2(dp[hc][2 * j], dp[hc][2 * j + 1]), ndl2));
+          float d0 = lo2(ds), d1 = hi2(ds);
+          if (diag) {
+            const int c = g * 64 + hc * 32 + 2 * j;
+            d0 = c <= r ? d0 : 0.f;
+            d1 = c + 1 <= r ? d1 : 0.f;
           }
-          dd[j] = pack_bf16x2(ds[0], ds[1]);
+          dd[j] = pack_bf16x2(d0, d1);
         }
-        tmem_st16(trow + 128 + g * 64 + hc * 16, dd);  // over dP values this warp has read
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_half[hc]);
+        tmem_st16(trow + T_DP + g * 64 + hc * 16, dd);  // over dP values this warp has read
       }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
     }
-    // dQ through the freed ring's shared memory and two TMA stores (coalesced rows); every
-    // elementwise warp reaches the barrier, the store is issued only when no wait failed
-    if (ok && __all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag, p.err, KID_PACKED, 47))) {
+    // dQ through the Q tile's shared memory (Q is in TMEM) and TMA stores; every elementwise
+    // warp reaches the barrier, the store is issued only when no wait failed
+    if (ok && __all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag, p.err, KID_PACKED, 54))) {
       tc_fence_after();
       uint32_t v[DH / 32][32];
 #pragma unroll
-      for (int i = 0; i < DH / 32; ++i) tmem_ld32(trow + 256 + g * DH + 32 * i, v[i]);
+      for (int i = 0; i < DH / 32; ++i) tmem_ld32(trow + T_DQ + g * DH + 32 * i, v[i]);
       tmem_wait_ld();
-      const uint32_t tile = smem_u32(base + B_OFF_RING);
+      const uint32_t tile = smem_u32(base + B_OFF_A);
 #pragma unroll
       for (int i = 0; i < DH / 32; ++i) stage_row32(tile, r, g * (DH / 32) + i, v[i], p.scale);
     }
     fence_proxy_async_smem();
     bar_ew();
     if (!*abort_flag)
-      store_tile<D>(&p.tdq, p.dq, p.ld_dq, smem_u32(base + B_OFF_RING), row0 + qt * TT, h * D, n_rows, threadIdx.x,
-                    B_EW);
+      store_tile<D>(&p.tdq, p.dq, p.ld_dq, smem_u32(base + B_OFF_A), row0 + qt * TT, h * D, n_rows, threadIdx.x, B_EW);
   }
   __syncthreads();
   if (warp == B_MMA && *abort_flag) {  // products already issued finish before TMEM is freed
@@ -573,24 +674,33 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   }
 }
 
+// KEY side: dK, dV of one key tile of one kv head, by a cluster of two CTAs that split the
+// group's query heads (the first ceil(group / 2) heads and the rest).  Each CTA then
+// finishes one of the two tensors: it stages the other tensor's fp32 partial sums in its own
+// shared memory and sends them in one bulk copy into the peer's, and adds the peer's to its
+// own in the order first CTA + second CTA.
 template <int D>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
     k_packed_dkv(const __grid_constant__ BwdParams p) {
-  // swizzle atoms, k-steps and bytes of a K / V / Q / dO tile; dims per column half
   constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM, DH = D / 2;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* base;
+  if (!smem_base(smem_raw, &base, p.err)) return;
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + B_OFF_BAR);
   uint64_t* kv_full = bars;         // K, V
-  uint64_t* qd_full = bars + 1;     // 2 stages (Q, dO, lse, delta of one (head, query tile))
-  uint64_t* qd_empty = bars + 3;    // 2
-  uint64_t* sd_full = bars + 5;     // S^T and dP^T of the item are in TMEM
-  uint64_t* p_half = bars + 6;      // 2: P^T, dS^T chunk hc of the item are in TMEM (one arrival per warp)
-  uint64_t* acc_full = bars + 9;
-  uint64_t* drain = bars + 10;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 11);
+  uint64_t* q_full = bars + 1;      // 3 stages
+  uint64_t* q_empty = bars + 4;     // 3
+  uint64_t* do_full = bars + 7;     // 2 stages (dO, lse, delta of one (head, query tile))
+  uint64_t* do_empty = bars + 9;    // 2
+  uint64_t* s_full = bars + 11;
+  uint64_t* p_full = bars + 12;     // P^T is in TMEM (one arrival per elementwise warp)
+  uint64_t* dp_full = bars + 13;
+  uint64_t* ds_full = bars + 14;    // dS^T is in TMEM (one arrival per elementwise warp)
+  uint64_t* acc_full = bars + 15;
+  uint64_t* drain = bars + 16;
+  uint64_t* peer_full = bars + 17;  // the peer CTA's partial sums of this CTA's tensor have landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint64_t* peer_full = bars + 12;  // the peer CTA's partial sums of this CTA's tensor have landed
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = blockIdx.x >> 1, kvh = item % p.nkv;
@@ -599,20 +709,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
   const int n_keys = min(TT, pt.len - kt * TT);
   const uint32_t crank = cluster_ctarank();
   const int grp = p.nq / p.nkv, n_qt = (pt.len + TT - 1) / TT;
+  const int n_last = pt.len - (n_qt - 1) * TT;  // rows of the sequence's last query tile
   const int hpc = (grp + 1) / 2, h_begin = (int)crank * hpc, h_count = min(grp, h_begin + hpc) - h_begin;
   // (head, query tile) items of this CTA
   const int per_head = n_qt - kt, n_st = h_count * per_head;
-  const int n_last = pt.len - (n_qt - 1) * TT;  // rows of the sequence's last query tile
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&qd_full[i], 1);
-      mbar_init(&qd_empty[i], 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
     }
-    mbar_init(sd_full, 1);
-    mbar_init(&p_half[0], B_EW / 32);
-    mbar_init(&p_half[1], B_EW / 32);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&do_full[i], 1);
+      mbar_init(&do_empty[i], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(p_full, B_EW / 32);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, B_EW / 32);
     mbar_init(acc_full, 1);
     mbar_init(drain, 1);
     mbar_init(peer_full, 1);
@@ -626,7 +741,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;  // S^T [0,128), dP^T [128,256) (P^T, dS^T packed over them), dV, dK
+  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t T_S = 0, T_DP = 128, T_DV = 256, T_DK = 384;  // P^T packed over S^T, dS^T over dP^T
 
   if (warp == B_PROD) {
     if (lane == 0) {
@@ -639,138 +755,177 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
         tma_load_2d(base + B_OFF_A + j * ATOM, &p.tk, kv_full, kvh * D + 64 * j, row0 + kt * TT);
         tma_load_2d(base + B_OFF_A + TILE_BYTES + j * ATOM, &p.tv, kv_full, kvh * D + 64 * j, row0 + kt * TT);
       }
-      int issued = 0;
-      for (int sti = 0; sti < n_st; ++sti) {
-        const int bf = sti & 1;
-        if (sti >= 2 && !mbar_wait(&qd_empty[bf], ((sti >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 31)) break;
-        const int h = kvh * grp + h_begin + sti / per_head, qt = kt + sti % per_head;
-        uint8_t* buf = base + B_OFF_RING + bf * 2 * TILE_BYTES;
-        float* ld = reinterpret_cast<float*>(base + B_OFF_X + bf * 1024);
-        mbar_arrive_expect_tx(&qd_full[bf], 2 * TB + 1024);
-        for (int j = 0; j < NA; ++j) {
-          tma_load_2d(buf + j * ATOM, &p.tq, &qd_full[bf], h * D + 64 * j, row0 + qt * TT);
-          tma_load_2d(buf + TILE_BYTES + j * ATOM, &p.tdo, &qd_full[bf], h * D + 64 * j, row0 + qt * TT);
-        }
-        bulk_load(ld, p.stats + ((size_t)h * p.n_tiles + pt.index - kt + qt) * (2 * TT), 1024, &qd_full[bf]);
-        issued = sti + 1;
+      int issued_q = 0, issued_do = 0;
+      for (int i = 0; i < n_st; ++i) {
+        const int s3 = i % 3, s2 = i & 1;
+        const int h = kvh * grp + h_begin + i / per_head, qt = kt + i % per_head;
+        if (i >= 3 && !mbar_wait(&q_empty[s3], (i / 3 - 1) & 1, abort_flag, p.err, KID_PACKED, 31)) break;
+        mbar_arrive_expect_tx(&q_full[s3], TB);
+        for (int j = 0; j < NA; ++j)
+          tma_load_2d(base + B_OFF_R3 + s3 * TILE_BYTES + j * ATOM, &p.tq, &q_full[s3], h * D + 64 * j, row0 + qt * TT);
+        issued_q = i + 1;
+        if (i >= 2 && !mbar_wait(&do_empty[s2], ((i >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 32)) break;
+        mbar_arrive_expect_tx(&do_full[s2], TB + 1024);
+        for (int j = 0; j < NA; ++j)
+          tma_load_2d(base + B_OFF_R2 + s2 * TILE_BYTES + j * ATOM, &p.tdo, &do_full[s2], h * D + 64 * j, row0 + qt * TT);
+        bulk_load(base + B_OFF_X + s2 * 1024, p.stats + ((size_t)h * p.n_tiles + pt.index - kt + qt) * (2 * TT), 1024,
+                  &do_full[s2]);
+        issued_do = i + 1;
       }
       if (*abort_flag) {  // let the copies already issued land before the CTA exits
         mbar_wait_drain(kv_full, 0);
-        for (int i = (issued > 2 ? issued - 2 : 0); i < issued; ++i) mbar_wait_drain(&qd_full[i & 1], (i >> 1) & 1);
+        for (int i = max(0, issued_q - 3); i < issued_q; ++i) mbar_wait_drain(&q_full[i % 3], (i / 3) & 1);
+        for (int i = max(0, issued_do - 2); i < issued_do; ++i) mbar_wait_drain(&do_full[i & 1], (i >> 1) & 1);
       }
     }
   } else if (warp == B_MMA) {
     constexpr uint32_t idesc_s = idesc_bf16(128, 128, false);  // S^T, dP^T: N = 128 queries
     constexpr uint32_t idesc_a = idesc_bf16(128, D, true);     // dV, dK: dO, Q N-major
     const uint32_t sK = smem_u32(base + B_OFF_A), sV = sK + TILE_BYTES;
-    bool ok = n_st > 0 && __all_sync(0xffffffffu, mbar_wait(kv_full, 0, abort_flag, p.err, KID_PACKED, 32));
-    // dV += P^T dO, dK += dS^T Q, each half as soon as its chunks are in TMEM (chunk hc holds
-    // the k-steps with ks & 2 == 2 hc); then the stage is free
-    auto kv_products = [&](int sti) -> bool {
-      const uint32_t sQ = smem_u32(base + B_OFF_RING + (sti & 1) * 2 * TILE_BYTES), sO = sQ + TILE_BYTES;
-      for (int hc = 0; hc < 2; ++hc) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&p_half[hc], sti & 1, abort_flag, p.err, KID_PACKED, 34))) return false;
-        tc_fence_after();
-        if (lane == 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {  // 16 queries per step
-            const int ks = (i >> 1) * 4 + hc * 2 + (i & 1);
-            const uint32_t acc = (sti | hc | i) ? 1u : 0u;
-            umma_bf16_ta(tmem + 256, tmem + packed_col(0, ks), sdesc_sw128(sO + ks * 2048, ATOM, 1024), idesc_a, acc);
-            umma_bf16_ta(tmem + 384, tmem + packed_col(128, ks), sdesc_sw128(sQ + ks * 2048, ATOM, 1024), idesc_a,
-                         acc);
-          }
-          if (hc == 1) umma_commit(&qd_empty[sti & 1]);
-        }
-        __syncwarp();
-      }
-      return true;
-    };
-    for (int sti = 0; ok && sti < n_st; ++sti) {
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&qd_full[sti & 1], (sti >> 1) & 1, abort_flag, p.err, KID_PACKED,
-                                                   33))))
-        break;
-      // the previous item's P^T and dS^T are read (issue order) before S^T, dP^T overwrite them
-      if (sti >= 1 && !(ok = kv_products(sti - 1))) break;
+    const uint32_t r3 = smem_u32(base + B_OFF_R3), r2 = smem_u32(base + B_OFF_R2);
+    auto wait = [&](uint64_t* bar, int parity, int site) -> bool {
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, abort_flag, p.err, KID_PACKED, site));
       tc_fence_after();
+      return ok;
+    };
+    // block = A B^T over the head dim, both from shared memory
+    auto block = [&](uint32_t t, uint32_t a, uint32_t b, uint64_t* full) {
       if (lane == 0) {
-        const uint32_t sQ = smem_u32(base + B_OFF_RING + (sti & 1) * 2 * TILE_BYTES), sO = sQ + TILE_BYTES;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {  // S^T = K Q^T, dP^T = V dO^T over the head dim
+        for (int ks = 0; ks < KS; ++ks) {
           const uint32_t off = (ks >> 2) * ATOM + (ks & 3) * 32;
-          umma_bf16(tmem, sdesc_sw128(sK + off, 16, 1024), sdesc_sw128(sQ + off, 16, 1024), idesc_s, ks ? 1u : 0u);
-          umma_bf16(tmem + 128, sdesc_sw128(sV + off, 16, 1024), sdesc_sw128(sO + off, 16, 1024), idesc_s,
-                    ks ? 1u : 0u);
+          umma_bf16(tmem + t, sdesc_sw128(a + off, 16, 1024), sdesc_sw128(b + off, 16, 1024), idesc_s, ks ? 1u : 0u);
         }
-        umma_commit(sd_full);
+        umma_commit(full);
       }
       __syncwarp();
+    };
+    // acc += (packed block)^T-side product over the 128 queries, 16 per step
+    auto accumulate = [&](uint32_t t, uint32_t packed, uint32_t b, int i) {
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+        umma_bf16_ta(tmem + t, tmem + packed_col(packed, ks), sdesc_sw128(b + ks * 2048, ATOM, 1024), idesc_a,
+                     (i | ks) ? 1u : 0u);
+    };
+    bool ok = n_st > 0 && wait(kv_full, 0, 33);
+    if (ok && (ok = wait(&q_full[0], 0, 34))) block(T_S, sK, r3, s_full);
+    if (ok && (ok = wait(&do_full[0], 0, 35))) block(T_DP, sV, r2, dp_full);
+    for (int i = 0; ok && i < n_st; ++i) {
+      if (!(ok = wait(p_full, i, 36))) break;
+      if (lane == 0) accumulate(T_DV, T_S, r2 + (i & 1) * TILE_BYTES, i);
+      __syncwarp();
+      if (i + 1 < n_st) {
+        // in issue order: S^T(i+1) overwrites the P^T(i) that dV(i) has read
+        if (!(ok = wait(&q_full[(i + 1) % 3], (i + 1) / 3, 34))) break;
+        block(T_S, sK, r3 + ((i + 1) % 3) * TILE_BYTES, s_full);
+      }
+      if (!(ok = wait(ds_full, i, 37))) break;
+      if (lane == 0) {
+        accumulate(T_DK, T_DP, r3 + (i % 3) * TILE_BYTES, i);
+        umma_commit(&q_empty[i % 3]);
+        umma_commit(&do_empty[i & 1]);  // behind ds_full: the statistics have been read as well
+      }
+      __syncwarp();
+      if (i + 1 < n_st) {
+        if (!(ok = wait(&do_full[(i + 1) & 1], (i + 1) >> 1, 35))) break;
+        block(T_DP, sV, r2 + ((i + 1) & 1) * TILE_BYTES, dp_full);
+      }
     }
-    if (ok) ok = kv_products(n_st - 1);
     if (ok && lane == 0) umma_commit(acc_full);
     __syncwarp();
   } else {
     const int wq = warp & 3, g = warp >> 2;
     const int r = wq * 32 + lane;  // key row = TMEM lane
     const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
-    const float sl = p.scale_log2;
+    const uint64_t sl2 = pack2(p.scale_log2, p.scale_log2);
+    const uint64_t minus = pack2(-1.0f, -1.0f);
     bool ok = true;
-    for (int sti = 0; sti < n_st; ++sti) {
-      const int qt = kt + sti % per_head;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(sd_full, sti & 1, abort_flag, p.err, KID_PACKED, 35)))) break;
+    for (int i = 0; i < n_st; ++i) {
+      const int qt = kt + i % per_head;
+      const bool ragged = qt == n_qt - 1 && n_last < TT, masked = qt == kt || ragged;
+      // statistics of the 64 queries of this warp's columns; queries lo <= c < hi are kept:
+      // those at or behind the key and in front of the sequence's end
+      const float* ld = reinterpret_cast<const float*>(base + B_OFF_X + (i & 1) * 1024) + g * 64;
+      const int lo = qt == kt ? r - g * 64 : 0, hi = ragged ? n_last - g * 64 : 64;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&do_full[i & 1], (i >> 1) & 1, abort_flag, p.err, KID_PACKED, 60))))
+        break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full, i & 1, abort_flag, p.err, KID_PACKED, 61)))) break;
       tc_fence_after();
-      const bool diag = qt == kt, ragged = qt == n_qt - 1 && n_last < TT;
+      uint32_t sv[2][32];
+      tmem_ld32(trow + T_S + g * 64, sv[0]);
+      tmem_ld32(trow + T_S + g * 64 + 32, sv[1]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int hc = 0; hc < 2; ++hc) {
+        uint32_t pp[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(ld + hc * 32 + j);
+          const uint64_t x0 = fma2(pack2(sv[hc][j], sv[hc][j + 1]), sl2, mul2(pack2(l.x, l.y), minus));
+          const uint64_t x1 = fma2(pack2(sv[hc][j + 2], sv[hc][j + 3]), sl2, mul2(pack2(l.z, l.w), minus));
+          float e[4] = {fast_exp2(lo2(x0)), fast_exp2(hi2(x0)), fast_exp2(lo2(x1)), fast_exp2(hi2(x1))};
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) e[k] = hc * 32 + j + k >= lo && hc * 32 + j + k < hi ? e[k] : 0.f;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sv[hc][j + k] = __float_as_uint(e[k]);
+          pp[j / 2] = pack_bf16x2(e[0], e[1]);
+          pp[j / 2 + 1] = pack_bf16x2(e[2], e[3]);
+        }
+        tmem_st16(trow + T_S + g * 64 + hc * 16, pp);  // over scores this warp has read
+      }
       if (ragged) {
-        // rows of Q and dO behind the sequence's end: zeros for the products dS^T Q and P^T dO
-        // (S^T and dP^T are done with them)
-        if (r >= n_last) zero_row<NA>(smem_u32(base + B_OFF_RING + (sti & 1) * 2 * TILE_BYTES + g * TILE_BYTES), r);
+        // rows of Q and dO behind the sequence's end: zeros for the products dS^T Q and P^T dO,
+        // once S^T and dP^T are done with them
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(dp_full, i & 1, abort_flag, p.err, KID_PACKED, 62)))) break;
+        if (r >= n_last)
+          zero_row<NA>(smem_u32(g == 0 ? base + B_OFF_R3 + (i % 3) * TILE_BYTES : base + B_OFF_R2 + (i & 1) * TILE_BYTES), r);
         fence_proxy_async_smem();
       }
-      const float* ld = reinterpret_cast<const float*>(base + B_OFF_X + (sti & 1) * 1024);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(dp_full, i & 1, abort_flag, p.err, KID_PACKED, 62)))) break;
+      tc_fence_after();
+      uint32_t dp[2][32];
+      tmem_ld32(trow + T_DP + g * 64, dp[0]);
+      tmem_ld32(trow + T_DP + g * 64 + 32, dp[1]);
+      tmem_wait_ld();
 #pragma unroll
-      for (int hc = 0; hc < 2; ++hc) {  // queries 64 g + 32 hc .. of the tile
-        uint32_t sv[32], dpv[32], pp[16], dd[16];
-        tmem_ld32(trow + g * 64 + hc * 32, sv);
-        tmem_ld32(trow + 128 + g * 64 + hc * 32, dpv);
-        tmem_wait_ld();
-        const int qi0 = g * 64 + hc * 32;     // query within the tile
-        const int lo = diag ? r - qi0 : 0;             // columns c < lo (queries before the key) are masked,
-        const int hi = ragged ? n_last - qi0 : 32;     // and those from hi on (behind the sequence's end)
+      for (int hc = 0; hc < 2; ++hc) {
+        uint32_t dd[16];
 #pragma unroll
-        for (int j4 = 0; j4 < 8; ++j4) {  // four columns: their lse and delta in one vector load each
-          const float4 l4 = *reinterpret_cast<const float4*>(ld + qi0 + 4 * j4);
-          const float4 d4 = *reinterpret_cast<const float4*>(ld + 128 + qi0 + 4 * j4);
-          const float lv[4] = {l4.x, l4.y, l4.z, l4.w}, dl[4] = {d4.x, d4.y, d4.z, d4.w};
-          float pv[4], ds[4];
+        for (int j = 0; j < 32; j += 4) {
+          const float4 d = *reinterpret_cast<const float4*>(ld + 128 + hc * 32 + j);
+          const uint64_t t0 = fma2(pack2(d.x, d.y), minus, pack2(dp[hc][j], dp[hc][j + 1]));
+          const uint64_t t1 = fma2(pack2(d.z, d.w), minus, pack2(dp[hc][j + 2], dp[hc][j + 3]));
+          const uint64_t y0 = mul2(pack2(sv[hc][j], sv[hc][j + 1]), t0), y1 = mul2(pack2(sv[hc][j + 2], sv[hc][j + 3]), t1);
+          float e[4] = {lo2(y0), hi2(y0), lo2(y1), hi2(y1)};
+          if (masked) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int c = 4 * j4 + e;
-            const bool keep = c >= lo && c < hi;
-            const float pe = fast_exp2(fmaf(__uint_as_float(sv[c]), sl, -lv[e]));
-            pv[e] = keep ? pe : 0.f;
-            ds[e] = keep ? pe * (__uint_as_float(dpv[c]) - dl[e]) : 0.f;
+            for (int k = 0; k < 4; ++k) e[k] = hc * 32 + j + k >= lo && hc * 32 + j + k < hi ? e[k] : 0.f;
           }
-          pp[2 * j4] = pack_bf16x2(pv[0], pv[1]);
-          pp[2 * j4 + 1] = pack_bf16x2(pv[2], pv[3]);
-          dd[2 * j4] = pack_bf16x2(ds[0], ds[1]);
-          dd[2 * j4 + 1] = pack_bf16x2(ds[2], ds[3]);
+          dd[j / 2] = pack_bf16x2(e[0], e[1]);
+          dd[j / 2 + 1] = pack_bf16x2(e[2], e[3]);
         }
-        tmem_st16(trow + g * 64 + hc * 16, pp);  // over scores this warp has read
-        tmem_st16(trow + 128 + g * 64 + hc * 16, dd);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_half[hc]);
+        tmem_st16(trow + T_DP + g * 64 + hc * 16, dd);
       }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
     }
-    const bool have = n_st > 0 && ok && __all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag, p.err, KID_PACKED, 36));
+    const bool have = n_st > 0 && ok && __all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag, p.err, KID_PACKED, 63));
     if (have) tc_fence_after();
     // The partial sums cross over: the first CTA finishes dV and the second dK, so each sends
     // the other tensor (fp32 rows of D floats, 16-byte chunks swizzled by row) from the start
-    // of its freed ring into the back half of the peer's ring.
+    // of its freed rings into the space behind it in the peer's.
     constexpr uint32_t PB = 128u * D * 4u;  // one tensor's partial sums
-    const uint32_t ring = smem_u32(base + B_OFF_RING);
-    const uint32_t t_send = trow + (crank == 0 ? 384u : 256u), t_keep = trow + (crank == 0 ? 256u : 384u);
+    static_assert(2 * PB <= 5u * TILE_BYTES, "the rings hold both sides of the exchange");
+    const uint32_t ring = smem_u32(base + B_OFF_R3);
+    const uint32_t t_send = trow + (crank == 0 ? T_DK : T_DV), t_keep = trow + (crank == 0 ? T_DV : T_DK);
     const uint32_t prow = (uint32_t)r * (D * 4);
 #pragma unroll
     for (int c = 0; c < DH / 32; ++c) {
@@ -797,9 +952,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
       const uint32_t other = crank ^ 1u;
       bulk_copy_to_peer(mapa_shared(ring + PB, other), ring, PB, mapa_shared(smem_u32(peer_full), other));
     }
-    (void)__all_sync(0xffffffffu, mbar_wait(peer_full, 0, abort_flag, p.err, KID_PACKED, 37));
+    (void)__all_sync(0xffffffffu, mbar_wait(peer_full, 0, abort_flag, p.err, KID_PACKED, 64));
     // this CTA's tensor (its sums plus the peer's) through the freed K tile's shared memory
-    // and NA TMA stores; dK takes the softmax scale
+    // and TMA stores; dK takes the softmax scale
     const uint32_t tile = smem_u32(base + B_OFF_A);
     const float sc = crank == 0 ? 1.0f : p.scale;
 #pragma unroll
@@ -845,7 +1000,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
     tmem_dealloc(tmem, 512);
   }
 }
-
 
 template <typename K>
 int allow_smem(K kernel, int bytes, int (&configured)[64]) {
@@ -959,7 +1113,6 @@ extern "C" int nf4ls_packed_attention_fwd(const nf4ls_pack* pack, const nf4ls_pa
 extern "C" int nf4ls_packed_attention_bwd(const nf4ls_pack* pack, const nf4ls_packed_heads* heads,
                                           const nf4ls_packed_attention* t, void* ws_dev, size_t ws_bytes,
                                           nf4ls_stream stream) {
-  static_assert(SMEM_BWD <= 232448, "shared memory of the packed attention backward");
   const char* who = "nf4ls_packed_attention_bwd";
   clear_error();
   NF4_TRY(check_pack(pack, who));
