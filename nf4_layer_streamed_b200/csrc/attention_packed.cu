@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 9);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_number(), lane = threadIdx.x & 31;
   // heads fastest, then the plan's tiles, most key tiles first
   const int h = blockIdx.x % p.nq;
   const PackTile pt = p.tiles[blockIdx.x / p.nq];
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;  // [0, 128) S then P, [128, 256) O
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);  // [0, 128) S then P, [128, 256) O
 
   if (warp == F_PROD) {
     // ------------------------------------------------------------------ TMA producer
@@ -149,35 +149,29 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
     constexpr uint32_t idesc_s = idesc_bf16(128, 128, false);  // Q K^T: both K-major
     constexpr uint32_t idesc_o = idesc_bf16(128, D, true);     // P V: V N-major
     const uint32_t sQ = smem_u32(base + F_OFF_Q), sK = smem_u32(base + F_OFF_K), sV = smem_u32(base + F_OFF_V);
+    const uint32_t el = elect_lane();
     // every wait is agreed on by the whole warp (__all_sync), so that no lane goes on alone
     bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag, p.err, KID_PACKED, 23));
     for (int kt = 0; ok && kt < nk; ++kt) {
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(k_full, kt & 1, abort_flag, p.err, KID_PACKED, 24)))) break;
       tc_fence_after();
-      if (lane == 0) {
-        // tcgen05.mma of one thread run in issue order, so S may overwrite the P that
-        // the previous tile's P V product reads
+      // tcgen05.mma of one thread run in issue order, so S may overwrite the P that the
+      // previous tile's P V product reads
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint32_t off = (ks >> 2) * ATOM + (ks & 3) * 32;
-          umma_bf16(tmem, sdesc_sw128(sQ + off, 16, 1024), sdesc_sw128(sK + off, 16, 1024), idesc_s, ks ? 1u : 0u);
-        }
-        umma_commit(s_full);
-        umma_commit(k_empty);
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint32_t off = (ks >> 2) * ATOM + (ks & 3) * 32;
+        umma_ss(el, tmem, sdesc_sw128(sQ + off, 16, 1024), sdesc_sw128(sK + off, 16, 1024), idesc_s, ks ? 1u : 0u);
       }
-      __syncwarp();
+      commit_by(el, s_full);
+      commit_by(el, k_empty);
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(p_full, kt & 1, abort_flag, p.err, KID_PACKED, 25)))) break;
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(v_full, kt & 1, abort_flag, p.err, KID_PACKED, 26)))) break;
       tc_fence_after();
-      if (lane == 0) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)  // 16 keys per step: P columns 8 ks .., V rows 16 ks ..
-          umma_bf16_ta(tmem + 128, tmem + ks * 8, sdesc_sw128(sV + ks * 2048, ATOM, 1024), idesc_o,
-                       (kt | ks) ? 1u : 0u);
-        umma_commit(v_empty);
-        umma_commit(o_full);
-      }
-      __syncwarp();
+      for (int ks = 0; ks < 8; ++ks)  // 16 keys per step: P columns 8 ks .., V rows 16 ks ..
+        umma_ts(el, tmem + 128, tmem + ks * 8, sdesc_sw128(sV + ks * 2048, ATOM, 1024), idesc_o, (kt | ks) ? 1u : 0u);
+      commit_by(el, v_empty);
+      commit_by(el, o_full);
     }
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
@@ -286,8 +280,7 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
   // On an aborted run the products already issued must finish before TMEM is freed.
   __syncthreads();
   if (warp == F_MMA && *abort_flag) {
-    if (lane == 0) umma_commit(drain);
-    __syncwarp();
+    commit_by(elect_lane(), drain);
     mbar_wait_drain(drain, 0);
   }
   tc_fence_before();
@@ -394,7 +387,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_number(), lane = threadIdx.x & 31;
   const int h = blockIdx.x % p.nq;
   const PackTile pt = p.tiles[blockIdx.x / p.nq];
   const int qt = pt.tile, row0 = pt.row0;
@@ -431,7 +424,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   constexpr uint32_t T_S = 0, T_DP = 128, T_DQ = 256, T_Q = 384, T_DO = 448;  // dS packed over dP
 
   if (warp == B_PROD) {
@@ -476,7 +469,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   } else if (warp == B_MMA) {
     constexpr uint32_t idesc_s = idesc_bf16(128, 128, false);  // S, dP: N = 128 keys
     constexpr uint32_t idesc_a = idesc_bf16(128, D, true);     // dQ += dS K: K N-major
-    const uint32_t s3 = smem_u32(base + B_OFF_R3), s2 = smem_u32(base + B_OFF_R2);
+    const uint32_t s3 = smem_u32(base + B_OFF_R3), s2 = smem_u32(base + B_OFF_R2), el = elect_lane();
     // every wait is agreed on by the whole warp, so that no lane goes on alone
     auto wait = [&](uint64_t* bar, int parity, int site) -> bool {
       const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, abort_flag, p.err, KID_PACKED, site));
@@ -484,27 +477,21 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
       return ok;
     };
     auto scores = [&](int i) {  // S(i): over the head dim, Q in TMEM
-      if (lane == 0) {
-        const uint32_t sK = s3 + (i % 3) * TILE_BYTES;
+      const uint32_t sK = s3 + (i % 3) * TILE_BYTES;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-          umma_bf16_ta(tmem + T_S, tmem + T_Q + ks * 8, sdesc_sw128(sK + (ks >> 2) * ATOM + (ks & 3) * 32, 16, 1024),
-                       idesc_s, ks ? 1u : 0u);
-        umma_commit(s_full);
-      }
-      __syncwarp();
+      for (int ks = 0; ks < KS; ++ks)
+        umma_ts(el, tmem + T_S, tmem + T_Q + ks * 8, sdesc_sw128(sK + (ks >> 2) * ATOM + (ks & 3) * 32, 16, 1024),
+                idesc_s, ks ? 1u : 0u);
+      commit_by(el, s_full);
     };
     auto dprobs = [&](int i) {  // dP(i)
-      if (lane == 0) {
-        const uint32_t sV = s2 + (i & 1) * TILE_BYTES;
+      const uint32_t sV = s2 + (i & 1) * TILE_BYTES;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-          umma_bf16_ta(tmem + T_DP, tmem + T_DO + ks * 8, sdesc_sw128(sV + (ks >> 2) * ATOM + (ks & 3) * 32, 16, 1024),
-                       idesc_s, ks ? 1u : 0u);
-        umma_commit(dp_full);
-        umma_commit(&v_empty[i & 1]);
-      }
-      __syncwarp();
+      for (int ks = 0; ks < KS; ++ks)
+        umma_ts(el, tmem + T_DP, tmem + T_DO + ks * 8, sdesc_sw128(sV + (ks >> 2) * ATOM + (ks & 3) * 32, 16, 1024),
+                idesc_s, ks ? 1u : 0u);
+      commit_by(el, dp_full);
+      commit_by(el, &v_empty[i & 1]);
     };
     bool ok = wait(qa_full, 0, 43) && !*abort_flag;
     if (ok && (ok = wait(&k_full[0], 0, 44))) scores(0);
@@ -516,22 +503,18 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
         scores(i + 1);
       }
       if (!(ok = wait(ds_full, i, 47))) break;
-      if (lane == 0) {
-        const uint32_t sK = s3 + (i % 3) * TILE_BYTES;
+      const uint32_t sK = s3 + (i % 3) * TILE_BYTES;
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)  // 16 keys per step
-          umma_bf16_ta(tmem + T_DQ, tmem + packed_col(T_DP, ks), sdesc_sw128(sK + ks * 2048, ATOM, 1024), idesc_a,
-                       (i | ks) ? 1u : 0u);
-        umma_commit(&k_empty[i % 3]);
-      }
-      __syncwarp();
+      for (int ks = 0; ks < 8; ++ks)  // 16 keys per step
+        umma_ts(el, tmem + T_DQ, tmem + packed_col(T_DP, ks), sdesc_sw128(sK + ks * 2048, ATOM, 1024), idesc_a,
+                (i | ks) ? 1u : 0u);
+      commit_by(el, &k_empty[i % 3]);
       if (i + 1 < n_kt) {
         if (!(ok = wait(&v_full[(i + 1) & 1], (i + 1) >> 1, 45))) break;
         dprobs(i + 1);
       }
     }
-    if (ok && lane == 0) umma_commit(acc_full);
-    __syncwarp();
+    if (ok) commit_by(el, acc_full);
   } else {
     // ------------------------------------------------------------------ elementwise + epilogue
     const int wq = warp & 3, g = warp >> 2;
@@ -662,8 +645,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   }
   __syncthreads();
   if (warp == B_MMA && *abort_flag) {  // products already issued finish before TMEM is freed
-    if (lane == 0) umma_commit(drain);
-    __syncwarp();
+    commit_by(elect_lane(), drain);
     mbar_wait_drain(drain, 0);
   }
   tc_fence_before();
@@ -702,7 +684,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_number(), lane = threadIdx.x & 31;
   const int item = blockIdx.x >> 1, kvh = item % p.nkv;
   const PackTile pt = p.tiles[item / p.nkv];
   const int kt = pt.tile, row0 = pt.row0;
@@ -741,7 +723,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   constexpr uint32_t T_S = 0, T_DP = 128, T_DV = 256, T_DK = 384;  // P^T packed over S^T, dS^T over dP^T
 
   if (warp == B_PROD) {
@@ -788,51 +770,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
       tc_fence_after();
       return ok;
     };
+    const uint32_t el = elect_lane();
     // block = A B^T over the head dim, both from shared memory
     auto block = [&](uint32_t t, uint32_t a, uint32_t b, uint64_t* full) {
-      if (lane == 0) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint32_t off = (ks >> 2) * ATOM + (ks & 3) * 32;
-          umma_bf16(tmem + t, sdesc_sw128(a + off, 16, 1024), sdesc_sw128(b + off, 16, 1024), idesc_s, ks ? 1u : 0u);
-        }
-        umma_commit(full);
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint32_t off = (ks >> 2) * ATOM + (ks & 3) * 32;
+        umma_ss(el, tmem + t, sdesc_sw128(a + off, 16, 1024), sdesc_sw128(b + off, 16, 1024), idesc_s, ks ? 1u : 0u);
       }
-      __syncwarp();
+      commit_by(el, full);
     };
     // acc += (packed block)^T-side product over the 128 queries, 16 per step
     auto accumulate = [&](uint32_t t, uint32_t packed, uint32_t b, int i) {
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)
-        umma_bf16_ta(tmem + t, tmem + packed_col(packed, ks), sdesc_sw128(b + ks * 2048, ATOM, 1024), idesc_a,
-                     (i | ks) ? 1u : 0u);
+        umma_ts(el, tmem + t, tmem + packed_col(packed, ks), sdesc_sw128(b + ks * 2048, ATOM, 1024), idesc_a,
+                (i | ks) ? 1u : 0u);
     };
     bool ok = n_st > 0 && wait(kv_full, 0, 33);
     if (ok && (ok = wait(&q_full[0], 0, 34))) block(T_S, sK, r3, s_full);
     if (ok && (ok = wait(&do_full[0], 0, 35))) block(T_DP, sV, r2, dp_full);
     for (int i = 0; ok && i < n_st; ++i) {
       if (!(ok = wait(p_full, i, 36))) break;
-      if (lane == 0) accumulate(T_DV, T_S, r2 + (i & 1) * TILE_BYTES, i);
-      __syncwarp();
+      accumulate(T_DV, T_S, r2 + (i & 1) * TILE_BYTES, i);
       if (i + 1 < n_st) {
         // in issue order: S^T(i+1) overwrites the P^T(i) that dV(i) has read
         if (!(ok = wait(&q_full[(i + 1) % 3], (i + 1) / 3, 34))) break;
         block(T_S, sK, r3 + ((i + 1) % 3) * TILE_BYTES, s_full);
       }
       if (!(ok = wait(ds_full, i, 37))) break;
-      if (lane == 0) {
-        accumulate(T_DK, T_DP, r3 + (i % 3) * TILE_BYTES, i);
-        umma_commit(&q_empty[i % 3]);
-        umma_commit(&do_empty[i & 1]);  // behind ds_full: the statistics have been read as well
-      }
-      __syncwarp();
+      accumulate(T_DK, T_DP, r3 + (i % 3) * TILE_BYTES, i);
+      commit_by(el, &q_empty[i % 3]);
+      commit_by(el, &do_empty[i & 1]);  // behind ds_full: the statistics have been read as well
       if (i + 1 < n_st) {
         if (!(ok = wait(&do_full[(i + 1) & 1], (i + 1) >> 1, 35))) break;
         block(T_DP, sV, r2 + ((i + 1) & 1) * TILE_BYTES, dp_full);
       }
     }
-    if (ok && lane == 0) umma_commit(acc_full);
-    __syncwarp();
+    if (ok) commit_by(el, acc_full);
   } else {
     const int wq = warp & 3, g = warp >> 2;
     const int r = wq * 32 + lane;  // key row = TMEM lane
@@ -989,8 +964,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
   }
   __syncthreads();
   if (warp == B_MMA && *abort_flag) {  // products already issued finish before TMEM is freed
-    if (lane == 0) umma_commit(drain);
-    __syncwarp();
+    commit_by(elect_lane(), drain);
     mbar_wait_drain(drain, 0);
   }
   tc_fence_before();
