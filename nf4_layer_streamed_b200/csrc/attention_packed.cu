@@ -1,6 +1,7 @@
 // Causal grouped-query attention over a packed batch (forward and gradients) on the
 // 5th-generation tensor cores: the sequences lie one behind the other and have any length.
 #include <cstring>
+#include <type_traits>
 
 #include "attention_tile.cuh"
 #include "common.cuh"
@@ -25,7 +26,7 @@ struct BwdParams {
   CUtensorMap tdq, tdk, tdv;        // the gradients, same boxes (TMA stores)
   const PackTile* tiles;            // query tiles or key tiles, most work first
   const float* lse;
-  float* stats;  // [nq, n_tiles, 2, 128]: lse log2(e) and delta, by the query side for the key side
+  float* stats;  // [nq, n_tiles, 2, 128]: -lse log2(e) and -delta, by the query side for the key side
   __nv_bfloat16 *dq, *dk, *dv;
   int ld_dq, ld_dk, ld_dv, total, n_tiles, nq, nkv;
   float scale, scale_log2;
@@ -39,6 +40,63 @@ __device__ __forceinline__ void zero_row(uint32_t tile, int r) {
   for (int j = 0; j < NA; ++j)
 #pragma unroll
     for (int c = 0; c < 8; ++c) st_shared_v4(tile + j * ATOM + r * 128 + c * 16, 0u, 0u, 0u, 0u);
+}
+
+constexpr uint32_t kCubicPairs = 0xA4;  // three of eight
+
+// Two 32-bit values to an instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  return (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32);
+}
+__device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) { return (uint64_t)a | ((uint64_t)b << 32); }
+
+// 2^x of both values by arithmetic: x = n + r with n whole and |r| <= 1/2, 2^r by a cubic of
+// least largest relative error on that range (7.5e-5, its mean removed; a probability is
+// rounded to bf16 next, 2^-8), n added to the exponent.  x below -126 gives 2^-126; NaN
+// stays non-finite.  The exponential unit takes 8 cycles per warp and value, this 6 of the
+// multiplier's and 4 of the integer pipe's; together they take what neither does alone.
+__device__ __forceinline__ void exp2_by_cubic(uint64_t x, float& e0, float& e1) {
+  constexpr float magic = 12582912.0f;  // 1.5 2^23: adding it leaves round(x) in the low bits
+  float a, b;
+  asm("max.NaN.f32 %0, %1, 0fC2FC0000;" : "=f"(a) : "f"(lo2(x)));
+  asm("max.NaN.f32 %0, %1, 0fC2FC0000;" : "=f"(b) : "f"(hi2(x)));
+  const uint64_t t = pack2(a, b), y = add2(t, pack2(magic, magic));
+  const uint64_t r = fma2(add2(y, pack2(-magic, -magic)), pack2(-1.0f, -1.0f), t);
+  uint64_t q = fma2(pack2(0.05517138f, 0.05517138f), r, pack2(0.24260989f, 0.24260989f));
+  q = fma2(q, r, pack2(0.69325742f, 0.69325742f));
+  q = fma2(q, r, pack2(0.99992294f, 0.99992294f));
+  e0 = __uint_as_float((uint32_t)q + ((uint32_t)y << 23));
+  e1 = __uint_as_float((uint32_t)(q >> 32) + ((uint32_t)(y >> 32) << 23));
+}
+__device__ __forceinline__ void exp2_by_unit(uint64_t x, float& e0, float& e1) {
+  e0 = fast_exp2(lo2(x));
+  e1 = fast_exp2(hi2(x));
+}
+// Which of eight neighbouring pairs take the cubic.
+__device__ constexpr bool cubic_pair(int j) { return ((kCubicPairs >> (j & 7)) & 1) != 0; }
+template <typename F>
+__device__ __forceinline__ void either(bool c, F&& f) {  // two straight-line forms of f, not one with a select per value
+  if (c)
+    f(std::true_type{});
+  else
+    f(std::false_type{});
 }
 
 // The staged tile at `tile` to rows row .. row + n_rows - 1 and columns col .. col + D - 1 of
@@ -62,7 +120,7 @@ __device__ __forceinline__ void store_tile(const CUtensorMap* map, __nv_bfloat16
 }
 
 // warps 0-3: softmax and epilogue (warp w owns TMEM lanes 32 w .. 32 w + 31, one query
-// row per thread); warp 4: TMA producer; warp 5: MMA issuer
+// row per thread, its 128 scores in registers); warp 4: TMA producer; warp 5: MMA issuer
 constexpr int F_THREADS = 192, F_PROD = 4, F_MMA = 5;
 constexpr int F_OFF_Q = 0, F_OFF_K = TILE_BYTES, F_OFF_V = 2 * TILE_BYTES, F_OFF_BAR = 3 * TILE_BYTES;
 constexpr int SMEM_TC = 1024 + F_OFF_BAR + 128;
@@ -80,10 +138,10 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
   uint64_t* v_full = bars + 3;
   uint64_t* v_empty = bars + 4;
   uint64_t* s_full = bars + 5;
-  uint64_t* p_full = bars + 6;
-  uint64_t* o_full = bars + 7;   // one phase per key tile: the P V product of that tile is done
-  uint64_t* drain = bars + 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 9);
+  uint64_t* p_half = bars + 6;   // 2: P of keys 64 h .. 64 h + 63 is in TMEM (one arrival per softmax warp)
+  uint64_t* o_full = bars + 8;   // one phase per key tile: the P V product of that tile is done
+  uint64_t* drain = bars + 9;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 10);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = warp_number(), lane = threadIdx.x & 31;
@@ -102,7 +160,8 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
     mbar_init(v_full, 1);
     mbar_init(v_empty, 1);
     mbar_init(s_full, 1);
-    mbar_init(p_full, 4);
+    mbar_init(&p_half[0], 4);
+    mbar_init(&p_half[1], 4);
     mbar_init(o_full, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -164,12 +223,16 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
       }
       commit_by(el, s_full);
       commit_by(el, k_empty);
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(p_full, kt & 1, abort_flag, p.err, KID_PACKED, 25)))) break;
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(v_full, kt & 1, abort_flag, p.err, KID_PACKED, 26)))) break;
-      tc_fence_after();
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks)  // 16 keys per step: P columns 8 ks .., V rows 16 ks ..
-        umma_ts(el, tmem + 128, tmem + ks * 8, sdesc_sw128(sV + ks * 2048, ATOM, 1024), idesc_o, (kt | ks) ? 1u : 0u);
+      for (int hf = 0; hf < 2; ++hf) {  // the first half runs under the second half's exponentials
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&p_half[hf], kt & 1, abort_flag, p.err, KID_PACKED, 25)))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)  // 16 keys per step: P columns 8 ks .., V rows 16 ks ..
+          umma_ts(el, tmem + 128, tmem + ks * 8, sdesc_sw128(sV + ks * 2048, ATOM, 1024), idesc_o, (kt | ks) ? 1u : 0u);
+      }
+      if (!ok) break;
       commit_by(el, v_empty);
       commit_by(el, o_full);
     }
@@ -196,14 +259,14 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[c][i] = c * 32 + i <= r ? v[c][i] : 0xFF800000u;
       }
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // independent chains
+      float m4[4];  // independent chains
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int e = 0; e < 4; ++e) m4[e] = fmaxf(__uint_as_float(v[0][e]), __uint_as_float(v[0][4 + e]));
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
+      for (int i = 8; i < 128; i += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(v[c][i + e]), __uint_as_float(v[c][i + 4 + e])));
+        for (int e = 0; e < 4; ++e)
+          m4[e] = fmaxf(fmaxf(m4[e], __uint_as_float(v[i / 32][i % 32 + e])), __uint_as_float(v[i / 32][i % 32 + 4 + e]));
       float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       mx *= sl;
       const float m_new = (kt == 0 || mx > m_run + kRescaleLog2) ? fmaxf(mx, m_run) : m_run;
@@ -226,20 +289,6 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
         l_run *= alpha;
       }
       m_run = m_new;
-      float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float p0 = fast_exp2(fmaf(__uint_as_float(v[c][2 * j]), sl, -m_run));
-          const float p1 = fast_exp2(fmaf(__uint_as_float(v[c][2 * j + 1]), sl, -m_run));
-          s4[2 * (j & 1)] += p0;
-          s4[2 * (j & 1) + 1] += p1;
-          pk[j] = pack_bf16x2(p0, p1);
-        }
-        tmem_st16(trow + c * 16, pk);
-      }
       if (diag && n_rows < TT) {
         // rows of V behind the sequence's end belong to others: zeros, so that a
         // non-finite value there times a probability of 0 stays out of O
@@ -247,11 +296,35 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
         if (r >= n_rows) zero_row<NA>(smem_u32(base + F_OFF_V), r);
         fence_proxy_async_smem();
       }
-      tmem_wait_st();
-      l_run += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+      const uint64_t sl2 = pack2(sl, sl), nm2 = pack2(-m_run, -m_run);
+      uint64_t acc[2] = {0, 0};
+      either(diag, [&](auto exact) {  // the diagonal tile's probabilities of 0 are exactly that
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+          for (int c = 2 * hf; c < 2 * hf + 2; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const uint64_t x = fma2(pack2(v[c][2 * j], v[c][2 * j + 1]), sl2, nm2);
+              float e0, e1;
+              if (!exact && cubic_pair(j))
+                exp2_by_cubic(x, e0, e1);
+              else
+                exp2_by_unit(x, e0, e1);
+              acc[j & 1] = add2(acc[j & 1], pack2(e0, e1));
+              pk[j] = pack_bf16x2(e0, e1);
+            }
+            tmem_st16(trow + c * 16, pk);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_half[hf]);
+        }
+      });
+      acc[0] = add2(acc[0], acc[1]);
+      l_run += lo2(acc[0]) + hi2(acc[0]);
     }
     // O / sum through the freed Q tile's shared memory and two TMA stores (coalesced rows);
     // all four warps reach the barrier, the store is issued only when no wait failed
@@ -334,29 +407,6 @@ __device__ __forceinline__ bool smem_base(uint8_t* raw, uint8_t** base, int* err
   if (threadIdx.x == 0) record_error(err, 2, KID_PACKED, 1);
   return false;
 }
-
-// (a0, a1) * (b0, b1) + (c0, c1) and its parts, two to an instruction.
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  return (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32);
-}
-__device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) { return (uint64_t)a | ((uint64_t)b << 32); }
 
 // QUERY side: dQ of one query tile of one head.  The Q and dO tiles are copied into TMEM
 // (bf16 pairs, one query row per lane), so that S and dP read only K and V from shared
@@ -570,8 +620,8 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     const float dl = ok ? red[r] + red[128 + r] : 0.f;
     if (ok && g == 0) {
       float* st = p.stats + ((size_t)h * p.n_tiles + pt.index) * (2 * TT);
-      st[r] = lse2;
-      st[TT + r] = dl;
+      st[r] = -lse2;
+      st[TT + r] = -dl;
     }
     const uint64_t sl2 = pack2(p.scale_log2, p.scale_log2), nlse2 = pack2(-lse2, -lse2), ndl2 = pack2(-dl, -dl);
     for (int kt = 0; ok && kt < n_kt; ++kt) {
@@ -595,8 +645,13 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
           const uint64_t x = fma2(pack2(sv[hc][j], sv[hc][j + 1]), sl2, nlse2);
-          sv[hc][j] = __float_as_uint(fast_exp2(lo2(x)));
-          sv[hc][j + 1] = __float_as_uint(fast_exp2(hi2(x)));
+          float e0, e1;
+          if (cubic_pair(j / 2))
+            exp2_by_cubic(x, e0, e1);
+          else
+            exp2_by_unit(x, e0, e1);
+          sv[hc][j] = __float_as_uint(e0);
+          sv[hc][j + 1] = __float_as_uint(e1);
         }
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(dp_full, kt & 1, abort_flag, p.err, KID_PACKED, 53)))) break;
       tc_fence_after();
@@ -604,23 +659,25 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
       tmem_ld32(trow + T_DP + g * 64, dp[0]);
       tmem_ld32(trow + T_DP + g * 64 + 32, dp[1]);
       tmem_wait_ld();
+      either(diag, [&](auto masked) {
 #pragma unroll
-      for (int hc = 0; hc < 2; ++hc) {  // keys 64 g + 32 hc .. of the tile
-        uint32_t dd[16];
+        for (int hc = 0; hc < 2; ++hc) {  // keys 64 g + 32 hc .. of the tile
+          uint32_t dd[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const uint64_t ds = mul2(pack2(sv[hc][2 * j], sv[hc][2 * j + 1]),
-                                   add2(pack2(dp[hc][2 * j], dp[hc][2 * j + 1]), ndl2));
-          float d0 = lo2(ds), d1 = hi2(ds);
-          if (diag) {
-            const int c = g * 64 + hc * 32 + 2 * j;
-            d0 = c <= r ? d0 : 0.f;
-            d1 = c + 1 <= r ? d1 : 0.f;
+          for (int j = 0; j < 16; ++j) {
+            const uint64_t ds = mul2(pack2(sv[hc][2 * j], sv[hc][2 * j + 1]),
+                                     add2(pack2(dp[hc][2 * j], dp[hc][2 * j + 1]), ndl2));
+            float d0 = lo2(ds), d1 = hi2(ds);
+            if (masked) {
+              const int c = g * 64 + hc * 32 + 2 * j;
+              d0 = c <= r ? d0 : 0.f;
+              d1 = c + 1 <= r ? d1 : 0.f;
+            }
+            dd[j] = pack_bf16x2(d0, d1);
           }
-          dd[j] = pack_bf16x2(d0, d1);
+          tmem_st16(trow + T_DP + g * 64 + hc * 16, dd);  // over dP values this warp has read
         }
-        tmem_st16(trow + T_DP + g * 64 + hc * 16, dd);  // over dP values this warp has read
-      }
+      });
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -813,7 +870,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
     const int r = wq * 32 + lane;  // key row = TMEM lane
     const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
     const uint64_t sl2 = pack2(p.scale_log2, p.scale_log2);
-    const uint64_t minus = pack2(-1.0f, -1.0f);
     bool ok = true;
     for (int i = 0; i < n_st; ++i) {
       const int qt = kt + i % per_head;
@@ -830,26 +886,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
       tmem_ld32(trow + T_S + g * 64, sv[0]);
       tmem_ld32(trow + T_S + g * 64 + 32, sv[1]);
       tmem_wait_ld();
+      either(masked, [&](auto mask) {
 #pragma unroll
-      for (int hc = 0; hc < 2; ++hc) {
-        uint32_t pp[16];
+        for (int hc = 0; hc < 2; ++hc) {
+          uint32_t pp[16];
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(ld + hc * 32 + j);
-          const uint64_t x0 = fma2(pack2(sv[hc][j], sv[hc][j + 1]), sl2, mul2(pack2(l.x, l.y), minus));
-          const uint64_t x1 = fma2(pack2(sv[hc][j + 2], sv[hc][j + 3]), sl2, mul2(pack2(l.z, l.w), minus));
-          float e[4] = {fast_exp2(lo2(x0)), fast_exp2(hi2(x0)), fast_exp2(lo2(x1)), fast_exp2(hi2(x1))};
-          if (masked) {
+          for (int j = 0; j < 32; j += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(ld + hc * 32 + j);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) e[k] = hc * 32 + j + k >= lo && hc * 32 + j + k < hi ? e[k] : 0.f;
+            for (int k = 0; k < 4; k += 2) {
+              const uint64_t x = fma2(pack2(sv[hc][j + k], sv[hc][j + k + 1]), sl2, k ? pack2(l.z, l.w) : pack2(l.x, l.y));
+              float e0, e1;
+              if (cubic_pair((j + k) / 2))
+                exp2_by_cubic(x, e0, e1);
+              else
+                exp2_by_unit(x, e0, e1);
+              if (mask) {
+                const int c = hc * 32 + j + k;
+                e0 = c >= lo && c < hi ? e0 : 0.f;
+                e1 = c + 1 >= lo && c + 1 < hi ? e1 : 0.f;
+              }
+              sv[hc][j + k] = __float_as_uint(e0);
+              sv[hc][j + k + 1] = __float_as_uint(e1);
+              pp[(j + k) / 2] = pack_bf16x2(e0, e1);
+            }
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) sv[hc][j + k] = __float_as_uint(e[k]);
-          pp[j / 2] = pack_bf16x2(e[0], e[1]);
-          pp[j / 2 + 1] = pack_bf16x2(e[2], e[3]);
+          tmem_st16(trow + T_S + g * 64 + hc * 16, pp);  // over scores this warp has read
         }
-        tmem_st16(trow + T_S + g * 64 + hc * 16, pp);  // over scores this warp has read
-      }
+      });
       if (ragged) {
         // rows of Q and dO behind the sequence's end: zeros for the products dS^T Q and P^T dO,
         // once S^T and dP^T are done with them
@@ -868,25 +932,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
       tmem_ld32(trow + T_DP + g * 64, dp[0]);
       tmem_ld32(trow + T_DP + g * 64 + 32, dp[1]);
       tmem_wait_ld();
+      either(masked, [&](auto mask) {
 #pragma unroll
-      for (int hc = 0; hc < 2; ++hc) {
-        uint32_t dd[16];
+        for (int hc = 0; hc < 2; ++hc) {
+          uint32_t dd[16];
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 d = *reinterpret_cast<const float4*>(ld + 128 + hc * 32 + j);
-          const uint64_t t0 = fma2(pack2(d.x, d.y), minus, pack2(dp[hc][j], dp[hc][j + 1]));
-          const uint64_t t1 = fma2(pack2(d.z, d.w), minus, pack2(dp[hc][j + 2], dp[hc][j + 3]));
-          const uint64_t y0 = mul2(pack2(sv[hc][j], sv[hc][j + 1]), t0), y1 = mul2(pack2(sv[hc][j + 2], sv[hc][j + 3]), t1);
-          float e[4] = {lo2(y0), hi2(y0), lo2(y1), hi2(y1)};
-          if (masked) {
+          for (int j = 0; j < 32; j += 4) {
+            const float4 d = *reinterpret_cast<const float4*>(ld + 128 + hc * 32 + j);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) e[k] = hc * 32 + j + k >= lo && hc * 32 + j + k < hi ? e[k] : 0.f;
+            for (int k = 0; k < 4; k += 2) {
+              const uint64_t y = mul2(pack2(sv[hc][j + k], sv[hc][j + k + 1]),
+                                      add2(pack2(dp[hc][j + k], dp[hc][j + k + 1]), k ? pack2(d.z, d.w) : pack2(d.x, d.y)));
+              float e0 = lo2(y), e1 = hi2(y);
+              if (mask) {  // not by the zero of p alone: dP of a masked place may be anything
+                const int c = hc * 32 + j + k;
+                e0 = c >= lo && c < hi ? e0 : 0.f;
+                e1 = c + 1 >= lo && c + 1 < hi ? e1 : 0.f;
+              }
+              dd[(j + k) / 2] = pack_bf16x2(e0, e1);
+            }
           }
-          dd[j / 2] = pack_bf16x2(e[0], e[1]);
-          dd[j / 2 + 1] = pack_bf16x2(e[2], e[3]);
+          tmem_st16(trow + T_DP + g * 64 + hc * 16, dd);
         }
-        tmem_st16(trow + T_DP + g * 64 + hc * 16, dd);
-      }
+      });
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
