@@ -186,12 +186,12 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
       for (int j = 0; j < NA; ++j) tma_load_2d(base + F_OFF_Q + j * ATOM, &p.tq, q_full, h * D + 64 * j, row0 + qt * TT);
       int issued_k = 0, issued_v = 0;
       for (int kt = 0; kt < nk; ++kt) {
-        if (kt > 0 && !mbar_wait(k_empty, (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 21)) break;
+        if (kt > 0 && !mbar_sleep(k_empty, (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 21)) break;
         mbar_arrive_expect_tx(k_full, TB);
         for (int j = 0; j < NA; ++j)
           tma_load_2d(base + F_OFF_K + j * ATOM, &p.tk, k_full, kvh * D + 64 * j, row0 + kt * TT);
         issued_k = kt + 1;
-        if (kt > 0 && !mbar_wait(v_empty, (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 22)) break;
+        if (kt > 0 && !mbar_sleep(v_empty, (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 22)) break;
         mbar_arrive_expect_tx(v_full, TB);
         for (int j = 0; j < NA; ++j)
           tma_load_2d(base + F_OFF_V + j * ATOM, &p.tv, v_full, kvh * D + 64 * j, row0 + kt * TT);
@@ -210,9 +210,9 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
     const uint32_t sQ = smem_u32(base + F_OFF_Q), sK = smem_u32(base + F_OFF_K), sV = smem_u32(base + F_OFF_V);
     const uint32_t el = elect_lane();
     // every wait is agreed on by the whole warp (__all_sync), so that no lane goes on alone
-    bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag, p.err, KID_PACKED, 23));
+    bool ok = __all_sync(0xffffffffu, mbar_sleep(q_full, 0, abort_flag, p.err, KID_PACKED, 23));
     for (int kt = 0; ok && kt < nk; ++kt) {
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(k_full, kt & 1, abort_flag, p.err, KID_PACKED, 24)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_sleep(k_full, kt & 1, abort_flag, p.err, KID_PACKED, 24)))) break;
       tc_fence_after();
       // tcgen05.mma of one thread run in issue order, so S may overwrite the P that the
       // previous tile's P V product reads
@@ -223,10 +223,10 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
       }
       commit_by(el, s_full);
       commit_by(el, k_empty);
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(v_full, kt & 1, abort_flag, p.err, KID_PACKED, 26)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_sleep(v_full, kt & 1, abort_flag, p.err, KID_PACKED, 26)))) break;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {  // the first half runs under the second half's exponentials
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&p_half[hf], kt & 1, abort_flag, p.err, KID_PACKED, 25)))) break;
+        if (!(ok = __all_sync(0xffffffffu, mbar_sleep(&p_half[hf], kt & 1, abort_flag, p.err, KID_PACKED, 25)))) break;
         tc_fence_after();
 #pragma unroll
         for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)  // 16 keys per step: P columns 8 ks .., V rows 16 ks ..
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int kt = 0; kt < nk; ++kt) {
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full, kt & 1, abort_flag, p.err, KID_PACKED, 27)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_sleep(s_full, kt & 1, abort_flag, p.err, KID_PACKED, 27)))) break;
       tc_fence_after();
       const bool diag = kt == qt;
       // the row of scores, held in registers; masked ones (on the diagonal tile, which is
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
       const bool resc = kt > 0 && m_new != m_run;
       if (__any_sync(0xffffffffu, resc)) {
         // the previous tile's P V product must be in O before O is scaled
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(o_full, (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 28)))) break;
+        if (!(ok = __all_sync(0xffffffffu, mbar_sleep(o_full, (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 28)))) break;
         tc_fence_after();
         const float alpha = resc ? fast_exp2(m_run - m_new) : 1.0f;
 #pragma unroll
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
       if (diag && n_rows < TT) {
         // rows of V behind the sequence's end belong to others: zeros, so that a
         // non-finite value there times a probability of 0 stays out of O
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(v_full, kt & 1, abort_flag, p.err, KID_PACKED, 30)))) break;
+        if (!(ok = __all_sync(0xffffffffu, mbar_sleep(v_full, kt & 1, abort_flag, p.err, KID_PACKED, 30)))) break;
         if (r >= n_rows) zero_row<NA>(smem_u32(base + F_OFF_V), r);
         fence_proxy_async_smem();
       }
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
     }
     // O / sum through the freed Q tile's shared memory and two TMA stores (coalesced rows);
     // all four warps reach the barrier, the store is issued only when no wait failed
-    if (ok && __all_sync(0xffffffffu, mbar_wait(o_full, (nk - 1) & 1, abort_flag, p.err, KID_PACKED, 29))) {
+    if (ok && __all_sync(0xffffffffu, mbar_sleep(o_full, (nk - 1) & 1, abort_flag, p.err, KID_PACKED, 29))) {
       tc_fence_after();
       const float inv = 1.0f / l_run;
       const uint32_t tile = smem_u32(base + F_OFF_Q);
@@ -385,17 +385,22 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
 // tiles in order; key side: query heads of the group, then query tiles), so results are
 // bit-reproducible.
 
-// warps 0-7: elementwise and epilogue (warp w: TMEM lane quarter w % 4, columns 64 (w / 4) ..
-// of a block); warp 8: TMA producer; warp 9: MMA issuer
-constexpr int B_THREADS = 320, B_PROD = 8, B_MMA = 9, B_EW = 256;
+// warps 0-15: elementwise and epilogue (warp w: TMEM lane quarter w % 4, columns
+// 32 (w / 4) .. of a block; four on each scheduler hide one another's waits where two did
+// not); warp 16: TMA producer; warp 17: MMA issuer
+constexpr int B_THREADS = 576, B_PROD = 16, B_MMA = 17, B_EW = 512;
 constexpr int B_OFF_A = 0;                              // Q, dO (query side) or K, V (key side)
 constexpr int B_OFF_R3 = 2 * TILE_BYTES;                // 3 stages: K (query side) or Q (key side)
 constexpr int B_OFF_R2 = B_OFF_R3 + 3 * TILE_BYTES;     // 2 stages: V (query side) or dO (key side)
-constexpr int B_OFF_X = B_OFF_R2 + 2 * TILE_BYTES;      // query side: delta halves [2][128]; key side: 2 stages
+constexpr int B_OFF_X = B_OFF_R2 + 2 * TILE_BYTES;      // query side: delta quarters [4][128]; key side: 2 stages
                                                         // x (128 lse + 128 delta floats)
 constexpr int B_OFF_BAR = B_OFF_X + 2048;
 constexpr int SMEM_BWD = 232448;  // all of it: what lies behind the barriers is slack for the alignment
 static_assert(B_OFF_BAR + 256 + 512 <= SMEM_BWD, "shared memory of the packed attention backward");
+
+// TMEM column of the A operand of 16-row step ks (0-7) of a block whose first column is c0:
+// column group g packed its 32 rows' values to columns c0 + 32 g .. c0 + 32 g + 15.
+__device__ __forceinline__ uint32_t packed32(uint32_t c0, int ks) { return c0 + (ks >> 1) * 32 + (ks & 1) * 8; }
 
 __device__ __forceinline__ void bar_ew() { asm volatile("bar.sync 1, %0;" ::"n"(B_EW) : "memory"); }
 
@@ -414,8 +419,7 @@ __device__ __forceinline__ bool smem_base(uint8_t* raw, uint8_t** base, int* err
 // delivers, while the next tiles land in it).
 template <int D>
 __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constant__ BwdParams p) {
-  // swizzle atoms, k-steps and bytes of a tile; dims per column half
-  constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM, DH = D / 2;
+  constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM;  // swizzle atoms, k-steps and bytes of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base;
   if (!smem_base(smem_raw, &base, p.err)) return;
@@ -492,13 +496,13 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
       int issued_k = 0, issued_v = 0;
       for (int kt = 0; kt < n_kt; ++kt) {
         const int sk = kt % 3, sv = kt & 1;
-        if (kt == 2 && !mbar_wait(o_read, 0, abort_flag, p.err, KID_PACKED, 40)) break;
-        if (kt >= 3 && !mbar_wait(&k_empty[sk], (kt / 3 - 1) & 1, abort_flag, p.err, KID_PACKED, 41)) break;
+        if (kt == 2 && !mbar_sleep(o_read, 0, abort_flag, p.err, KID_PACKED, 40)) break;
+        if (kt >= 3 && !mbar_sleep(&k_empty[sk], (kt / 3 - 1) & 1, abort_flag, p.err, KID_PACKED, 41)) break;
         mbar_arrive_expect_tx(&k_full[sk], TB);
         for (int j = 0; j < NA; ++j)
           tma_load_2d(base + B_OFF_R3 + sk * TILE_BYTES + j * ATOM, &p.tk, &k_full[sk], kvh * D + 64 * j, row0 + kt * TT);
         issued_k = kt + 1;
-        if (kt >= 2 && !mbar_wait(&v_empty[sv], ((kt >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 42)) break;
+        if (kt >= 2 && !mbar_sleep(&v_empty[sv], ((kt >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 42)) break;
         mbar_arrive_expect_tx(&v_full[sv], TB);
         for (int j = 0; j < NA; ++j)
           tma_load_2d(base + B_OFF_R2 + sv * TILE_BYTES + j * ATOM, &p.tv, &v_full[sv], kvh * D + 64 * j, row0 + kt * TT);
@@ -522,7 +526,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     const uint32_t s3 = smem_u32(base + B_OFF_R3), s2 = smem_u32(base + B_OFF_R2), el = elect_lane();
     // every wait is agreed on by the whole warp, so that no lane goes on alone
     auto wait = [&](uint64_t* bar, int parity, int site) -> bool {
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, abort_flag, p.err, KID_PACKED, site));
+      const bool ok = __all_sync(0xffffffffu, mbar_sleep(bar, parity & 1, abort_flag, p.err, KID_PACKED, site));
       tc_fence_after();
       return ok;
     };
@@ -556,7 +560,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
       const uint32_t sK = s3 + (i % 3) * TILE_BYTES;
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)  // 16 keys per step
-        umma_ts(el, tmem + T_DQ, tmem + packed_col(T_DP, ks), sdesc_sw128(sK + ks * 2048, ATOM, 1024), idesc_a,
+        umma_ts(el, tmem + T_DQ, tmem + packed32(T_DP, ks), sdesc_sw128(sK + ks * 2048, ATOM, 1024), idesc_a,
                 (i | ks) ? 1u : 0u);
       commit_by(el, &k_empty[i % 3]);
       if (i + 1 < n_kt) {
@@ -570,41 +574,41 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     const int wq = warp & 3, g = warp >> 2;
     const int r = wq * 32 + lane;  // query row = TMEM lane
     const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
-    // First Q and dO into TMEM (the MMA warp starts on them), then delta = rowsum(dO * O)
-    // over this thread's DH dims (dims g DH .. of its row: 16-byte chunks c0 + c of swizzle
-    // atom g DH / 64 of the dO and O tiles), the two halves added through smem.  TMEM
-    // column g DH / 2 + 4 c + i holds the pair i of chunk c.
+    // First Q and dO into TMEM (the MMA warp starts on them), then delta = rowsum(dO * O);
+    // group g < D / 32 takes dims 32 g .. of its row: 16-byte chunks c0 .. c0 + 3 of swizzle
+    // atom g / 2 of the tiles, TMEM columns 16 g ..; the parts of delta are added through smem
     float* red = reinterpret_cast<float*>(base + B_OFF_X);
-    const int atom = (g * DH) / 64, c0 = ((g * DH) % 64) / 8;
+    const bool has_dims = g < D / 32;
+    const int atom = g >> 1, c0 = (g & 1) * 4;
     const uint8_t* q_row = base + B_OFF_A + atom * ATOM + r * 128;
     const uint8_t* dO_row = base + B_OFF_A + TILE_BYTES + atom * ATOM + r * 128;
     const uint8_t* o_row = base + B_OFF_R3 + 2 * TILE_BYTES + atom * ATOM + r * 128;
     // rows behind the sequence's end: no lse to read; their lanes compute values that
     // nothing stores
     const float lse2 = r < n_rows ? p.lse[(size_t)h * p.total + row0 + qt * TT + r] * 1.4426950408889634f : 0.f;
-    bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag, p.err, KID_PACKED, 50));
-    if (ok) {
-      uint32_t qv[DH / 2], dv[DH / 2];
+    bool ok = __all_sync(0xffffffffu, mbar_sleep(q_full, 0, abort_flag, p.err, KID_PACKED, 50));
+    if (ok && has_dims) {
+      uint32_t qv[16], dv[16];
 #pragma unroll
-      for (int c = 0; c < DH / 8; ++c) {
+      for (int c = 0; c < 4; ++c) {
         const uint32_t off = (uint32_t)(((c0 + c) ^ (r & 7)) << 4);
         const uint4 d = *reinterpret_cast<const uint4*>(dO_row + off);
         const uint4 q = *reinterpret_cast<const uint4*>(q_row + off);
         qv[4 * c] = q.x, qv[4 * c + 1] = q.y, qv[4 * c + 2] = q.z, qv[4 * c + 3] = q.w;
         dv[4 * c] = d.x, dv[4 * c + 1] = d.y, dv[4 * c + 2] = d.z, dv[4 * c + 3] = d.w;
       }
-      tmem_st_cols(trow + T_Q + g * (DH / 2), qv);
-      tmem_st_cols(trow + T_DO + g * (DH / 2), dv);
+      tmem_st16(trow + T_Q + g * 16, qv);
+      tmem_st16(trow + T_DO + g * 16, dv);
       tmem_wait_st();
     }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(qa_full);  // also on failure: the MMA warp then sees the abort
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_full, 0, abort_flag, p.err, KID_PACKED, 51));
-    if (ok) {
+    if (ok) ok = __all_sync(0xffffffffu, mbar_sleep(o_full, 0, abort_flag, p.err, KID_PACKED, 51));
+    if (ok && has_dims) {
       float s = 0.f;
 #pragma unroll
-      for (int c = 0; c < DH / 8; ++c) {
+      for (int c = 0; c < 4; ++c) {
         const uint32_t off = (uint32_t)(((c0 + c) ^ (r & 7)) << 4);
         const uint4 a = *reinterpret_cast<const uint4*>(o_row + off);
         const uint4 d = *reinterpret_cast<const uint4*>(dO_row + off);
@@ -617,7 +621,9 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     __syncwarp();
     if (lane == 0) mbar_arrive(o_read);
     bar_ew();
-    const float dl = ok ? red[r] + red[128 + r] : 0.f;
+    float dl = 0.f;
+    if (ok)
+      for (int i = 0; i < D / 32; ++i) dl += red[i * 128 + r];
     if (ok && g == 0) {
       float* st = p.stats + ((size_t)h * p.n_tiles + pt.index) * (2 * TT);
       st[r] = -lse2;
@@ -626,11 +632,10 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     const uint64_t sl2 = pack2(p.scale_log2, p.scale_log2), nlse2 = pack2(-lse2, -lse2), ndl2 = pack2(-dl, -dl);
     for (int kt = 0; ok && kt < n_kt; ++kt) {
       const bool diag = kt == qt;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full, kt & 1, abort_flag, p.err, KID_PACKED, 52)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_sleep(s_full, kt & 1, abort_flag, p.err, KID_PACKED, 52)))) break;
       tc_fence_after();
-      uint32_t sv[2][32];
-      tmem_ld32(trow + T_S + g * 64, sv[0]);
-      tmem_ld32(trow + T_S + g * 64 + 32, sv[1]);
+      uint32_t sv[32];
+      tmem_ld32(trow + T_S + g * 32, sv);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
@@ -641,42 +646,35 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
         fence_proxy_async_smem();
       }
 #pragma unroll
-      for (int hc = 0; hc < 2; ++hc)
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const uint64_t x = fma2(pack2(sv[hc][j], sv[hc][j + 1]), sl2, nlse2);
-          float e0, e1;
-          if (cubic_pair(j / 2))
-            exp2_by_cubic(x, e0, e1);
-          else
-            exp2_by_unit(x, e0, e1);
-          sv[hc][j] = __float_as_uint(e0);
-          sv[hc][j + 1] = __float_as_uint(e1);
-        }
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(dp_full, kt & 1, abort_flag, p.err, KID_PACKED, 53)))) break;
+      for (int j = 0; j < 32; j += 2) {
+        const uint64_t x = fma2(pack2(sv[j], sv[j + 1]), sl2, nlse2);
+        float e0, e1;
+        if (cubic_pair(j / 2))
+          exp2_by_cubic(x, e0, e1);
+        else
+          exp2_by_unit(x, e0, e1);
+        sv[j] = __float_as_uint(e0);
+        sv[j + 1] = __float_as_uint(e1);
+      }
+      if (!(ok = __all_sync(0xffffffffu, mbar_sleep(dp_full, kt & 1, abort_flag, p.err, KID_PACKED, 53)))) break;
       tc_fence_after();
-      uint32_t dp[2][32];
-      tmem_ld32(trow + T_DP + g * 64, dp[0]);
-      tmem_ld32(trow + T_DP + g * 64 + 32, dp[1]);
+      uint32_t dp[32];
+      tmem_ld32(trow + T_DP + g * 32, dp);
       tmem_wait_ld();
-      either(diag, [&](auto masked) {
+      either(diag, [&](auto masked) {  // keys 32 g .. of the tile
+        uint32_t dd[16];
 #pragma unroll
-        for (int hc = 0; hc < 2; ++hc) {  // keys 64 g + 32 hc .. of the tile
-          uint32_t dd[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint64_t ds = mul2(pack2(sv[hc][2 * j], sv[hc][2 * j + 1]),
-                                     add2(pack2(dp[hc][2 * j], dp[hc][2 * j + 1]), ndl2));
-            float d0 = lo2(ds), d1 = hi2(ds);
-            if (masked) {
-              const int c = g * 64 + hc * 32 + 2 * j;
-              d0 = c <= r ? d0 : 0.f;
-              d1 = c + 1 <= r ? d1 : 0.f;
-            }
-            dd[j] = pack_bf16x2(d0, d1);
+        for (int j = 0; j < 16; ++j) {
+          const uint64_t ds = mul2(pack2(sv[2 * j], sv[2 * j + 1]), add2(pack2(dp[2 * j], dp[2 * j + 1]), ndl2));
+          float d0 = lo2(ds), d1 = hi2(ds);
+          if (masked) {
+            const int c = g * 32 + 2 * j;
+            d0 = c <= r ? d0 : 0.f;
+            d1 = c + 1 <= r ? d1 : 0.f;
           }
-          tmem_st16(trow + T_DP + g * 64 + hc * 16, dd);  // over dP values this warp has read
+          dd[j] = pack_bf16x2(d0, d1);
         }
+        tmem_st16(trow + T_DP + g * 32, dd);  // over dP values this warp has read
       });
       tmem_wait_st();
       tc_fence_before();
@@ -685,15 +683,14 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     }
     // dQ through the Q tile's shared memory (Q is in TMEM) and TMA stores; every elementwise
     // warp reaches the barrier, the store is issued only when no wait failed
-    if (ok && __all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag, p.err, KID_PACKED, 54))) {
+    if (ok && __all_sync(0xffffffffu, mbar_sleep(acc_full, 0, abort_flag, p.err, KID_PACKED, 54))) {
       tc_fence_after();
-      uint32_t v[DH / 32][32];
-#pragma unroll
-      for (int i = 0; i < DH / 32; ++i) tmem_ld32(trow + T_DQ + g * DH + 32 * i, v[i]);
-      tmem_wait_ld();
-      const uint32_t tile = smem_u32(base + B_OFF_A);
-#pragma unroll
-      for (int i = 0; i < DH / 32; ++i) stage_row32(tile, r, g * (DH / 32) + i, v[i], p.scale);
+      if (has_dims) {
+        uint32_t v[32];
+        tmem_ld32(trow + T_DQ + g * 32, v);
+        tmem_wait_ld();
+        stage_row32(smem_u32(base + B_OFF_A), r, g, v, p.scale);
+      }
     }
     fence_proxy_async_smem();
     bar_ew();
@@ -721,7 +718,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
 template <int D>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
     k_packed_dkv(const __grid_constant__ BwdParams p) {
-  constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM, DH = D / 2;
+  constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base;
   if (!smem_base(smem_raw, &base, p.err)) return;
@@ -798,12 +795,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
       for (int i = 0; i < n_st; ++i) {
         const int s3 = i % 3, s2 = i & 1;
         const int h = kvh * grp + h_begin + i / per_head, qt = kt + i % per_head;
-        if (i >= 3 && !mbar_wait(&q_empty[s3], (i / 3 - 1) & 1, abort_flag, p.err, KID_PACKED, 31)) break;
+        if (i >= 3 && !mbar_sleep(&q_empty[s3], (i / 3 - 1) & 1, abort_flag, p.err, KID_PACKED, 31)) break;
         mbar_arrive_expect_tx(&q_full[s3], TB);
         for (int j = 0; j < NA; ++j)
           tma_load_2d(base + B_OFF_R3 + s3 * TILE_BYTES + j * ATOM, &p.tq, &q_full[s3], h * D + 64 * j, row0 + qt * TT);
         issued_q = i + 1;
-        if (i >= 2 && !mbar_wait(&do_empty[s2], ((i >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 32)) break;
+        if (i >= 2 && !mbar_sleep(&do_empty[s2], ((i >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 32)) break;
         mbar_arrive_expect_tx(&do_full[s2], TB + 1024);
         for (int j = 0; j < NA; ++j)
           tma_load_2d(base + B_OFF_R2 + s2 * TILE_BYTES + j * ATOM, &p.tdo, &do_full[s2], h * D + 64 * j, row0 + qt * TT);
@@ -823,7 +820,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
     const uint32_t sK = smem_u32(base + B_OFF_A), sV = sK + TILE_BYTES;
     const uint32_t r3 = smem_u32(base + B_OFF_R3), r2 = smem_u32(base + B_OFF_R2);
     auto wait = [&](uint64_t* bar, int parity, int site) -> bool {
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, abort_flag, p.err, KID_PACKED, site));
+      const bool ok = __all_sync(0xffffffffu, mbar_sleep(bar, parity & 1, abort_flag, p.err, KID_PACKED, site));
       tc_fence_after();
       return ok;
     };
@@ -841,7 +838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
     auto accumulate = [&](uint32_t t, uint32_t packed, uint32_t b, int i) {
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)
-        umma_ts(el, tmem + t, tmem + packed_col(packed, ks), sdesc_sw128(b + ks * 2048, ATOM, 1024), idesc_a,
+        umma_ts(el, tmem + t, tmem + packed32(packed, ks), sdesc_sw128(b + ks * 2048, ATOM, 1024), idesc_a,
                 (i | ks) ? 1u : 0u);
     };
     bool ok = n_st > 0 && wait(kv_full, 0, 33);
@@ -870,55 +867,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
     const int r = wq * 32 + lane;  // key row = TMEM lane
     const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
     const uint64_t sl2 = pack2(p.scale_log2, p.scale_log2);
+    const int row_f = wq * 32 + (lane >> 2), col0 = g * 32 + 2 * (lane & 3);  // of the first fragment value
     bool ok = true;
     for (int i = 0; i < n_st; ++i) {
       const int qt = kt + i % per_head;
       const bool ragged = qt == n_qt - 1 && n_last < TT, masked = qt == kt || ragged;
-      // statistics of the 64 queries of this warp's columns; queries lo <= c < hi are kept:
-      // those at or behind the key and in front of the sequence's end
-      const float* ld = reinterpret_cast<const float*>(base + B_OFF_X + (i & 1) * 1024) + g * 64;
-      const int lo = qt == kt ? r - g * 64 : 0, hi = ragged ? n_last - g * 64 : 64;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&do_full[i & 1], (i >> 1) & 1, abort_flag, p.err, KID_PACKED, 60))))
+      // The block in fragments, for the sake of the statistics, which belong to its columns:
+      // a lane sees 8 of the warp's 32 columns, so a warp's loads of them take a quarter of
+      // the shared-memory cycles that whole rows per lane take (those, beside the products'
+      // own operands, held this pass up to 1850 cycles; it takes about half of that now).
+      // Row l / 4 + 8 of lane half hl and column 8 j + 2 (l % 4) of the warp's 32 x 32 part;
+      // queries lo <= c < hi are kept: those at or behind the key, in front of the end.
+      const float* ld = reinterpret_cast<const float*>(base + B_OFF_X + (i & 1) * 1024) + col0;
+      const int diag_row = qt == kt ? row_f - col0 : -TT, hi = ragged ? n_last - col0 : TT;
+      if (!(ok = __all_sync(0xffffffffu, mbar_sleep(&do_full[i & 1], (i >> 1) & 1, abort_flag, p.err, KID_PACKED, 60))))
         break;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full, i & 1, abort_flag, p.err, KID_PACKED, 61)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_sleep(s_full, i & 1, abort_flag, p.err, KID_PACKED, 61)))) break;
       tc_fence_after();
-      uint32_t sv[2][32];
-      tmem_ld32(trow + T_S + g * 64, sv[0]);
-      tmem_ld32(trow + T_S + g * 64 + 32, sv[1]);
+      uint32_t sv[2][16];
+#pragma unroll
+      for (int hl = 0; hl < 2; ++hl) tmem_ld_frag(trow + (uint32_t)(hl << 20) + T_S + g * 32, sv[hl]);
       tmem_wait_ld();
       either(masked, [&](auto mask) {
+        uint32_t pp[2][8];
 #pragma unroll
-        for (int hc = 0; hc < 2; ++hc) {
-          uint32_t pp[16];
+        for (int j = 0; j < 4; ++j) {
+          const float2 l = *reinterpret_cast<const float2*>(ld + 8 * j);
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(ld + hc * 32 + j);
-#pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-              const uint64_t x = fma2(pack2(sv[hc][j + k], sv[hc][j + k + 1]), sl2, k ? pack2(l.z, l.w) : pack2(l.x, l.y));
-              float e0, e1;
-              if (cubic_pair((j + k) / 2))
-                exp2_by_cubic(x, e0, e1);
-              else
-                exp2_by_unit(x, e0, e1);
-              if (mask) {
-                const int c = hc * 32 + j + k;
-                e0 = c >= lo && c < hi ? e0 : 0.f;
-                e1 = c + 1 >= lo && c + 1 < hi ? e1 : 0.f;
-              }
-              sv[hc][j + k] = __float_as_uint(e0);
-              sv[hc][j + k + 1] = __float_as_uint(e1);
-              pp[(j + k) / 2] = pack_bf16x2(e0, e1);
+          for (int k = 0; k < 4; ++k) {  // the four pairs of these two columns
+            const int hl = k >> 1, e = 4 * j + 2 * (k & 1);
+            const uint64_t x = fma2(pack2(sv[hl][e], sv[hl][e + 1]), sl2, pack2(l.x, l.y));
+            float e0, e1;
+            if (cubic_pair(4 * j + k))
+              exp2_by_cubic(x, e0, e1);
+            else
+              exp2_by_unit(x, e0, e1);
+            if (mask) {
+              const int lo = diag_row + 16 * hl + 8 * (k & 1);
+              e0 = 8 * j >= lo && 8 * j < hi ? e0 : 0.f;
+              e1 = 8 * j + 1 >= lo && 8 * j + 1 < hi ? e1 : 0.f;
             }
+            sv[hl][e] = __float_as_uint(e0);
+            sv[hl][e + 1] = __float_as_uint(e1);
+            pp[hl][e / 2] = pack_bf16x2(e0, e1);
           }
-          tmem_st16(trow + T_S + g * 64 + hc * 16, pp);  // over scores this warp has read
         }
+#pragma unroll
+        for (int hl = 0; hl < 2; ++hl)  // over scores this warp has read
+          tmem_st_frag(trow + (uint32_t)(hl << 20) + T_S + g * 32, pp[hl]);
       });
       if (ragged) {
         // rows of Q and dO behind the sequence's end: zeros for the products dS^T Q and P^T dO,
         // once S^T and dP^T are done with them
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(dp_full, i & 1, abort_flag, p.err, KID_PACKED, 62)))) break;
-        if (r >= n_last)
+        if (!(ok = __all_sync(0xffffffffu, mbar_sleep(dp_full, i & 1, abort_flag, p.err, KID_PACKED, 62)))) break;
+        if (r >= n_last && g < 2)
           zero_row<NA>(smem_u32(g == 0 ? base + B_OFF_R3 + (i % 3) * TILE_BYTES : base + B_OFF_R2 + (i & 1) * TILE_BYTES), r);
         fence_proxy_async_smem();
       }
@@ -926,41 +928,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(dp_full, i & 1, abort_flag, p.err, KID_PACKED, 62)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_sleep(dp_full, i & 1, abort_flag, p.err, KID_PACKED, 62)))) break;
       tc_fence_after();
-      uint32_t dp[2][32];
-      tmem_ld32(trow + T_DP + g * 64, dp[0]);
-      tmem_ld32(trow + T_DP + g * 64 + 32, dp[1]);
+      uint32_t dp[2][16];
+#pragma unroll
+      for (int hl = 0; hl < 2; ++hl) tmem_ld_frag(trow + (uint32_t)(hl << 20) + T_DP + g * 32, dp[hl]);
       tmem_wait_ld();
       either(masked, [&](auto mask) {
+        uint32_t dd[2][8];
 #pragma unroll
-        for (int hc = 0; hc < 2; ++hc) {
-          uint32_t dd[16];
+        for (int j = 0; j < 4; ++j) {
+          const float2 d = *reinterpret_cast<const float2*>(ld + 128 + 8 * j);
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 d = *reinterpret_cast<const float4*>(ld + 128 + hc * 32 + j);
-#pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-              const uint64_t y = mul2(pack2(sv[hc][j + k], sv[hc][j + k + 1]),
-                                      add2(pack2(dp[hc][j + k], dp[hc][j + k + 1]), k ? pack2(d.z, d.w) : pack2(d.x, d.y)));
-              float e0 = lo2(y), e1 = hi2(y);
-              if (mask) {  // not by the zero of p alone: dP of a masked place may be anything
-                const int c = hc * 32 + j + k;
-                e0 = c >= lo && c < hi ? e0 : 0.f;
-                e1 = c + 1 >= lo && c + 1 < hi ? e1 : 0.f;
-              }
-              dd[(j + k) / 2] = pack_bf16x2(e0, e1);
+          for (int k = 0; k < 4; ++k) {
+            const int hl = k >> 1, e = 4 * j + 2 * (k & 1);
+            const uint64_t y = mul2(pack2(sv[hl][e], sv[hl][e + 1]), add2(pack2(dp[hl][e], dp[hl][e + 1]), pack2(d.x, d.y)));
+            float e0 = lo2(y), e1 = hi2(y);
+            if (mask) {  // not by the zero of p alone: dP of a masked place may be anything
+              const int lo = diag_row + 16 * hl + 8 * (k & 1);
+              e0 = 8 * j >= lo && 8 * j < hi ? e0 : 0.f;
+              e1 = 8 * j + 1 >= lo && 8 * j + 1 < hi ? e1 : 0.f;
             }
+            dd[hl][e / 2] = pack_bf16x2(e0, e1);
           }
-          tmem_st16(trow + T_DP + g * 64 + hc * 16, dd);
         }
+#pragma unroll
+        for (int hl = 0; hl < 2; ++hl) tmem_st_frag(trow + (uint32_t)(hl << 20) + T_DP + g * 32, dd[hl]);
       });
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_full);
     }
-    const bool have = n_st > 0 && ok && __all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag, p.err, KID_PACKED, 63));
+    const bool have = n_st > 0 && ok && __all_sync(0xffffffffu, mbar_sleep(acc_full, 0, abort_flag, p.err, KID_PACKED, 63));
     if (have) tc_fence_after();
     // The partial sums cross over: the first CTA finishes dV and the second dK, so each sends
     // the other tensor (fp32 rows of D floats, 16-byte chunks swizzled by row) from the start
@@ -970,16 +970,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
     const uint32_t ring = smem_u32(base + B_OFF_R3);
     const uint32_t t_send = trow + (crank == 0 ? T_DK : T_DV), t_keep = trow + (crank == 0 ? T_DV : T_DK);
     const uint32_t prow = (uint32_t)r * (D * 4);
-#pragma unroll
-    for (int c = 0; c < DH / 32; ++c) {
+    const bool has_dims = g < D / 32;  // dims 32 g ..
+    if (has_dims) {
       uint32_t v[32];
       if (have) {
-        tmem_ld32(t_send + g * DH + c * 32, v);
+        tmem_ld32(t_send + g * 32, v);
         tmem_wait_ld();
       }
 #pragma unroll
       for (int q4 = 0; q4 < 8; ++q4) {
-        const uint32_t o = ring + prow + ((uint32_t)(((g * DH + c * 32) / 4 + q4) ^ (r & 7)) << 4);
+        const uint32_t o = ring + prow + ((uint32_t)((g * 8 + q4) ^ (r & 7)) << 4);
         if (have)
           st_shared_v4(o, v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
         else
@@ -995,27 +995,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
       const uint32_t other = crank ^ 1u;
       bulk_copy_to_peer(mapa_shared(ring + PB, other), ring, PB, mapa_shared(smem_u32(peer_full), other));
     }
-    (void)__all_sync(0xffffffffu, mbar_wait(peer_full, 0, abort_flag, p.err, KID_PACKED, 64));
+    (void)__all_sync(0xffffffffu, mbar_sleep(peer_full, 0, abort_flag, p.err, KID_PACKED, 64));
     // this CTA's tensor (its sums plus the peer's) through the freed K tile's shared memory
     // and TMA stores; dK takes the softmax scale
     const uint32_t tile = smem_u32(base + B_OFF_A);
     const float sc = crank == 0 ? 1.0f : p.scale;
-#pragma unroll
-    for (int c = 0; c < DH / 32; ++c) {
+    if (has_dims) {
       float v[32];
       uint32_t vr[32];
       if (have) {
-        tmem_ld32(t_keep + g * DH + c * 32, vr);
+        tmem_ld32(t_keep + g * 32, vr);
         tmem_wait_ld();
       }
 #pragma unroll
       for (int q4 = 0; q4 < 8; ++q4) {
-        const uint4 in = ld_shared_v4(ring + PB + prow + ((uint32_t)(((g * DH + c * 32) / 4 + q4) ^ (r & 7)) << 4));
+        const uint4 in = ld_shared_v4(ring + PB + prow + ((uint32_t)((g * 8 + q4) ^ (r & 7)) << 4));
         const float iv[4] = {__uint_as_float(in.x), __uint_as_float(in.y), __uint_as_float(in.z), __uint_as_float(in.w)};
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[4 * q4 + e] = ((have ? __uint_as_float(vr[4 * q4 + e]) : 0.f) + iv[e]) * sc;
       }
-      stage_row32(tile, r, g * (DH / 32) + c, v);
+      stage_row32(tile, r, g, v);
     }
     fence_proxy_async_smem();
     bar_ew();
