@@ -136,29 +136,34 @@ __device__ __forceinline__ void commit_by(uint32_t el, uint64_t* bar) {
 // The warp's number and a value of shared memory as the same in every lane.
 __device__ __forceinline__ int warp_number() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
 
-// mbar_wait (common.cuh) with the thread suspended for up to 20 us per try, so that waiting
-// warps leave the issue slots to those that compute.
-__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int kid,
-                                           int site) {
-  const uint32_t a = smem_u32(bar);
+// mbar_wait (common.cuh) of a whole converged warp: its first lane asks the barrier, under a
+// predicate, and every decision is voted, so that no lane ever runs apart from the others.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int kid,
+                                          int site) {
+  const uint32_t a = smem_u32(bar), first = (threadIdx.x & 31) == 0 ? 1u : 0u;
   unsigned long long t0 = 0;
-  while (true) {
+  for (int i = 0;; ++i) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 e, %3, 0;\n\t"
+        "setp.ne.b32 p, %3, %3;\n\t"
+        "@e mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(a), "r"(parity), "r"(20000u)
+        : "r"(a), "r"(parity), "r"(first)
         : "memory");
-    if (ok) return true;
-    if (*abort_flag) return false;
-    const unsigned long long t = global_ns();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > kWaitLimitNs) {
-      *abort_flag = 1;
-      record_error(err, 1, kid, site);
-      return false;
+    if (__any_sync(0xffffffffu, ok)) return true;
+    if ((i & 15) == 15) {
+      const unsigned long long t = global_ns();
+      if (t0 == 0) t0 = t;
+      const bool late = __any_sync(0xffffffffu, t - t0 > kWaitLimitNs);
+      if (late && first) {
+        *abort_flag = 1;
+        record_error(err, 1, kid, site);
+      }
+      __syncwarp();
+      if (__any_sync(0xffffffffu, late || *abort_flag != 0)) return false;
     }
   }
 }
