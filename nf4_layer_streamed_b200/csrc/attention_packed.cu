@@ -42,8 +42,6 @@ __device__ __forceinline__ void zero_row(uint32_t tile, int r) {
     for (int c = 0; c < 8; ++c) st_shared_v4(tile + j * ATOM + r * 128 + c * 16, 0u, 0u, 0u, 0u);
 }
 
-constexpr uint32_t kCubicPairs = 0xA4;  // three of eight
-
 // Two 32-bit values to an instruction.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   return (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32);
@@ -67,30 +65,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) { return (uint64_t)a | ((uint64_t)b << 32); }
 
-// 2^x of both values by arithmetic: x = n + r with n whole and |r| <= 1/2, 2^r by a cubic of
-// least largest relative error on that range (7.5e-5, its mean removed; a probability is
-// rounded to bf16 next, 2^-8), n added to the exponent.  x below -126 gives 2^-126; NaN
-// stays non-finite.  The exponential unit takes 8 cycles per warp and value, this 6 of the
-// multiplier's and 4 of the integer pipe's; together they take what neither does alone.
-__device__ __forceinline__ void exp2_by_cubic(uint64_t x, float& e0, float& e1) {
-  constexpr float magic = 12582912.0f;  // 1.5 2^23: adding it leaves round(x) in the low bits
-  float a, b;
-  asm("max.NaN.f32 %0, %1, 0fC2FC0000;" : "=f"(a) : "f"(lo2(x)));
-  asm("max.NaN.f32 %0, %1, 0fC2FC0000;" : "=f"(b) : "f"(hi2(x)));
-  const uint64_t t = pack2(a, b), y = add2(t, pack2(magic, magic));
-  const uint64_t r = fma2(add2(y, pack2(-magic, -magic)), pack2(-1.0f, -1.0f), t);
-  uint64_t q = fma2(pack2(0.05517138f, 0.05517138f), r, pack2(0.24260989f, 0.24260989f));
-  q = fma2(q, r, pack2(0.69325742f, 0.69325742f));
-  q = fma2(q, r, pack2(0.99992294f, 0.99992294f));
-  e0 = __uint_as_float((uint32_t)q + ((uint32_t)y << 23));
-  e1 = __uint_as_float((uint32_t)(q >> 32) + ((uint32_t)(y >> 32) << 23));
-}
-__device__ __forceinline__ void exp2_by_unit(uint64_t x, float& e0, float& e1) {
-  e0 = fast_exp2(lo2(x));
-  e1 = fast_exp2(hi2(x));
-}
-// Which of eight neighbouring pairs take the cubic.
-__device__ constexpr bool cubic_pair(int j) { return ((kCubicPairs >> (j & 7)) & 1) != 0; }
 template <typename F>
 __device__ __forceinline__ void either(bool c, F&& f) {  // two straight-line forms of f, not one with a select per value
   if (c)
@@ -261,6 +235,7 @@ __global__ void __launch_bounds__(F_THREADS, 1) k_packed_fwd(const __grid_consta
       for (int x = 0; ok && x < n_both; ++x) {
         const int n = x == 0 ? nk_a : nk;
         if (kt >= n) continue;
+        if (kt + 1 < n && !(ok = wait(&k_full[(kt + 1) & 1], (kt + 1) >> 1, 24))) break;  // long there: not on P's way
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {  // the first half runs under the second half's exponentials
           if (!(ok = wait(&p_half[2 * x + hf], kt, 25))) break;
@@ -275,10 +250,7 @@ __global__ void __launch_bounds__(F_THREADS, 1) k_packed_fwd(const __grid_consta
         commit_by(el, &o_full[x]);
         // tcgen05.mma of one thread run in issue order, so S may overwrite the P that this
         // tile's P V product reads
-        if (kt + 1 < n) {
-          if (!(ok = wait(&k_full[(kt + 1) & 1], (kt + 1) >> 1, 24))) break;
-          scores(x, kt + 1);
-        }
+        if (kt + 1 < n) scores(x, kt + 1);
       }
       if (!ok) break;
       if (kt + 1 < nk) commit_by(el, &k_empty[(kt + 1) & 1]);
@@ -358,28 +330,23 @@ __global__ void __launch_bounds__(F_THREADS, 1) k_packed_fwd(const __grid_consta
       }
       const uint64_t sl2 = pack2(sl, sl), nm2 = pack2(-m_run, -m_run);
       uint64_t acc[2] = {0, 0};
-      either(diag, [&](auto exact) {  // the diagonal tile's probabilities of 0 are exactly that
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t pk[16];
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t pk[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint64_t x = fma2(pack2(v[hf][2 * j], v[hf][2 * j + 1]), sl2, nm2);
-            float e0, e1;
-            if (!exact && cubic_pair(j))
-              exp2_by_cubic(x, e0, e1);
-            else
-              exp2_by_unit(x, e0, e1);
-            acc[j & 1] = add2(acc[j & 1], pack2(e0, e1));
-            pk[j] = pack_bf16x2(e0, e1);
-          }
-          tmem_st16(trow + g * 32 + hf * 16, pk);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_half[2 * t + hf]);
+        for (int j = 0; j < 16; ++j) {
+          const uint64_t y = fma2(pack2(v[hf][2 * j], v[hf][2 * j + 1]), sl2, nm2);
+          const float e0 = fast_exp2(lo2(y)), e1 = fast_exp2(hi2(y));
+          acc[j & 1] = add2(acc[j & 1], pack2(e0, e1));
+          pk[j] = pack_bf16x2(e0, e1);
         }
-      });
+        tmem_st16(trow + g * 32 + hf * 16, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_half[2 * t + hf]);
+        __syncwarp();
+      }
       acc[0] = add2(acc[0], acc[1]);
       l_run += lo2(acc[0]) + hi2(acc[0]);
       if (*abort_flag) ok = false;
@@ -439,7 +406,10 @@ __global__ void __launch_bounds__(F_THREADS, 1) k_packed_fwd(const __grid_consta
 // one that is there:
 //   query side:  S(i+1) | dQ(i) | dP(i+1)          key side:  dV(i) | S(i+1) | dK(i) | dP(i+1)
 // The exponentials of item i + 1 need only S(i+1) and run under the two products behind
-// it, and dS(i), which needs dP(i), under the product behind that.  The tiles come
+// it, and dS(i), which needs dP(i), under the product behind that.  (With columns of its
+// own for dS and dO left in shared memory, dP(i+1) need not wait for dQ(i), but dP then
+// reads both operands from shared memory: 2% slower.)  The key side hands P and dS over in
+// halves, so that the product of the first half runs under the making of the second.  The tiles come
 // through two rings: those that the first and the last product of an item read (K; Q)
 // live longest and have three stages, the others (V; dO) two.
 // The query side also forms delta = rowsum(dO * O) and writes it beside lse log2e for the
@@ -714,13 +684,8 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
 #pragma unroll
       for (int j = 0; j < 32; j += 2) {
         const uint64_t x = fma2(pack2(sv[j], sv[j + 1]), sl2, nlse2);
-        float e0, e1;
-        if (cubic_pair(j / 2))
-          exp2_by_cubic(x, e0, e1);
-        else
-          exp2_by_unit(x, e0, e1);
-        sv[j] = __float_as_uint(e0);
-        sv[j + 1] = __float_as_uint(e1);
+        sv[j] = __float_as_uint(fast_exp2(lo2(x)));
+        sv[j + 1] = __float_as_uint(fast_exp2(hi2(x)));
       }
       if (!(ok = warp_wait(dp_full, kt & 1, abort_flag, p.err, KID_PACKED, 53))) break;
       tc_fence_after();
@@ -795,13 +760,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
   uint64_t* do_full = bars + 7;     // 2 stages (dO, lse, delta of one (head, query tile))
   uint64_t* do_empty = bars + 9;    // 2
   uint64_t* s_full = bars + 11;
-  uint64_t* p_full = bars + 12;     // P^T is in TMEM (one arrival per elementwise warp)
-  uint64_t* dp_full = bars + 13;
-  uint64_t* ds_full = bars + 14;    // dS^T is in TMEM (one arrival per elementwise warp)
-  uint64_t* acc_full = bars + 15;
-  uint64_t* drain = bars + 16;
-  uint64_t* peer_full = bars + 17;  // the peer CTA's partial sums of this CTA's tensor have landed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
+  uint64_t* dp_full = bars + 12;
+  uint64_t* p_half = bars + 13;     // 2: P^T of queries 16 h .. of each 32 is in TMEM (one arrival per elementwise warp)
+  uint64_t* ds_half = bars + 15;    // 2: dS^T likewise
+  uint64_t* acc_full = bars + 17;
+  uint64_t* drain = bars + 18;
+  uint64_t* peer_full = bars + 19;  // the peer CTA's partial sums of this CTA's tensor have landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = warp_number(), lane = threadIdx.x & 31;
@@ -829,9 +794,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
       mbar_init(&do_empty[i], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(p_full, B_EW / 32);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, B_EW / 32);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&p_half[i], B_EW / 32);
+      mbar_init(&ds_half[i], B_EW / 32);
+    }
     mbar_init(acc_full, 1);
     mbar_init(drain, 1);
     mbar_init(peer_full, 1);
@@ -903,32 +870,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
       }
       commit_by(el, full);
     };
-    // acc += (packed block)^T-side product over the 128 queries, 16 per step
-    auto accumulate = [&](uint32_t t, uint32_t packed, uint32_t b, int i) {
+    // acc += (packed block)^T-side product over the 128 queries, 16 per step, each half of the
+    // steps as soon as its part of the block is there
+    auto accumulate = [&](uint32_t t, uint32_t packed, uint32_t b, int i, uint64_t* half, int site) -> bool {
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-        umma_ts(el, tmem + t, tmem + packed32(packed, ks), sdesc_sw128(b + ks * 2048, ATOM, 1024), idesc_a,
-                (i | ks) ? 1u : 0u);
+      for (int hf = 0; hf < 2; ++hf) {
+        if (!wait(&half[hf], i, site)) return false;
+#pragma unroll
+        for (int ks = hf; ks < 8; ks += 2)
+          umma_ts(el, tmem + t, tmem + packed32(packed, ks), sdesc_sw128(b + ks * 2048, ATOM, 1024), idesc_a,
+                  (i | ks) ? 1u : 0u);
+      }
+      return true;
     };
     bool ok = n_st > 0 && wait(kv_full, 0, 33);
     if (ok && (ok = wait(&q_full[0], 0, 34))) block(T_S, sK, r3, s_full);
     if (ok && (ok = wait(&do_full[0], 0, 35))) block(T_DP, sV, r2, dp_full);
     for (int i = 0; ok && i < n_st; ++i) {
-      if (!(ok = wait(p_full, i, 36))) break;
-      accumulate(T_DV, T_S, r2 + (i & 1) * TILE_BYTES, i);
-      if (i + 1 < n_st) {
-        // in issue order: S^T(i+1) overwrites the P^T(i) that dV(i) has read
-        if (!(ok = wait(&q_full[(i + 1) % 3], (i + 1) / 3, 34))) break;
-        block(T_S, sK, r3 + ((i + 1) % 3) * TILE_BYTES, s_full);
-      }
-      if (!(ok = wait(ds_full, i, 37))) break;
-      accumulate(T_DK, T_DP, r3 + (i % 3) * TILE_BYTES, i);
+      const bool more = i + 1 < n_st;
+      if (more && !(ok = wait(&q_full[(i + 1) % 3], (i + 1) / 3, 34))) break;
+      if (!(ok = accumulate(T_DV, T_S, r2 + (i & 1) * TILE_BYTES, i, p_half, 36))) break;
+      // in issue order: S^T(i+1) overwrites the P^T(i) that dV(i) has read
+      if (more) block(T_S, sK, r3 + ((i + 1) % 3) * TILE_BYTES, s_full);
+      if (more && !(ok = wait(&do_full[(i + 1) & 1], (i + 1) >> 1, 35))) break;
+      if (!(ok = accumulate(T_DK, T_DP, r3 + (i % 3) * TILE_BYTES, i, ds_half, 37))) break;
       commit_by(el, &q_empty[i % 3]);
-      commit_by(el, &do_empty[i & 1]);  // behind ds_full: the statistics have been read as well
-      if (i + 1 < n_st) {
-        if (!(ok = wait(&do_full[(i + 1) & 1], (i + 1) >> 1, 35))) break;
-        block(T_DP, sV, r2 + ((i + 1) & 1) * TILE_BYTES, dp_full);
-      }
+      commit_by(el, &do_empty[i & 1]);  // behind ds_half: the statistics have been read as well
+      if (more) block(T_DP, sV, r2 + ((i + 1) & 1) * TILE_BYTES, dp_full);
     }
     if (ok) commit_by(el, acc_full);
   } else if (warp >= B_FIRST) {
@@ -958,34 +926,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
 #pragma unroll
       for (int hl = 0; hl < 2; ++hl) tmem_ld_frag(trow + (uint32_t)(hl << 20) + T_S + g * 32, sv[hl]);
       tmem_wait_ld();
-      either(masked, [&](auto mask) {
-        uint32_t pp[2][8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 l = *reinterpret_cast<const float2*>(ld + 8 * j);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // the four pairs of these two columns
-            const int hl = k >> 1, e = 4 * j + 2 * (k & 1);
-            const uint64_t x = fma2(pack2(sv[hl][e], sv[hl][e + 1]), sl2, pack2(l.x, l.y));
-            float e0, e1;
-            if (cubic_pair(4 * j + k))
-              exp2_by_cubic(x, e0, e1);
-            else
-              exp2_by_unit(x, e0, e1);
-            if (mask) {
-              const int lo = diag_row + 16 * hl + 8 * (k & 1);
-              e0 = 8 * j >= lo && 8 * j < hi ? e0 : 0.f;
-              e1 = 8 * j + 1 >= lo && 8 * j + 1 < hi ? e1 : 0.f;
-            }
-            sv[hl][e] = __float_as_uint(e0);
-            sv[hl][e + 1] = __float_as_uint(e1);
-            pp[hl][e / 2] = pack_bf16x2(e0, e1);
-          }
-        }
-#pragma unroll
-        for (int hl = 0; hl < 2; ++hl)  // over scores this warp has read
-          tmem_st_frag(trow + (uint32_t)(hl << 20) + T_S + g * 32, pp[hl]);
-      });
       if (ragged) {
         // rows of Q and dO behind the sequence's end: zeros for the products dS^T Q and P^T dO,
         // once S^T and dP^T are done with them
@@ -994,10 +934,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
           zero_row<NA>(smem_u32(g == 0 ? base + B_OFF_R3 + (i % 3) * TILE_BYTES : base + B_OFF_R2 + (i & 1) * TILE_BYTES), r);
         fence_proxy_async_smem();
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+      // columns 16 hf .. of this warp's 32 as bf16 pairs over the block (which this warp has
+      // read), then on to the product
+      auto hand_over = [&](uint32_t t, int hf, const uint32_t (&w)[2][4], uint64_t* half) {
+#pragma unroll
+        for (int hl = 0; hl < 2; ++hl) tmem_st_frag(trow + (uint32_t)(hl << 20) + t + g * 32 + hf * 8, w[hl]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&half[hf]);
+        __syncwarp();
+      };
+      either(masked, [&](auto mask) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t pp[2][4];
+#pragma unroll
+          for (int j = 2 * hf; j < 2 * hf + 2; ++j) {
+            const float2 l = *reinterpret_cast<const float2*>(ld + 8 * j);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // the four pairs of these two columns
+              const int hl = k >> 1, e = 4 * j + 2 * (k & 1);
+              const uint64_t x = fma2(pack2(sv[hl][e], sv[hl][e + 1]), sl2, pack2(l.x, l.y));
+              float e0 = fast_exp2(lo2(x)), e1 = fast_exp2(hi2(x));
+              if (mask) {
+                const int lo = diag_row + 16 * hl + 8 * (k & 1);
+                e0 = 8 * j >= lo && 8 * j < hi ? e0 : 0.f;
+                e1 = 8 * j + 1 >= lo && 8 * j + 1 < hi ? e1 : 0.f;
+              }
+              sv[hl][e] = __float_as_uint(e0);
+              sv[hl][e + 1] = __float_as_uint(e1);
+              pp[hl][(e / 2) & 3] = pack_bf16x2(e0, e1);
+            }
+          }
+          hand_over(T_S, hf, pp, p_half);
+        }
+      });
       if (!(ok = warp_wait(dp_full, i & 1, abort_flag, p.err, KID_PACKED, 62))) break;
       tc_fence_after();
       uint32_t dp[2][16];
@@ -1005,30 +977,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
       for (int hl = 0; hl < 2; ++hl) tmem_ld_frag(trow + (uint32_t)(hl << 20) + T_DP + g * 32, dp[hl]);
       tmem_wait_ld();
       either(masked, [&](auto mask) {
-        uint32_t dd[2][8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 d = *reinterpret_cast<const float2*>(ld + 128 + 8 * j);
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t dd[2][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int hl = k >> 1, e = 4 * j + 2 * (k & 1);
-            const uint64_t y = mul2(pack2(sv[hl][e], sv[hl][e + 1]), add2(pack2(dp[hl][e], dp[hl][e + 1]), pack2(d.x, d.y)));
-            float e0 = lo2(y), e1 = hi2(y);
-            if (mask) {  // not by the zero of p alone: dP of a masked place may be anything
-              const int lo = diag_row + 16 * hl + 8 * (k & 1);
-              e0 = 8 * j >= lo && 8 * j < hi ? e0 : 0.f;
-              e1 = 8 * j + 1 >= lo && 8 * j + 1 < hi ? e1 : 0.f;
+          for (int j = 2 * hf; j < 2 * hf + 2; ++j) {
+            const float2 d = *reinterpret_cast<const float2*>(ld + 128 + 8 * j);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int hl = k >> 1, e = 4 * j + 2 * (k & 1);
+              const uint64_t y = mul2(pack2(sv[hl][e], sv[hl][e + 1]), add2(pack2(dp[hl][e], dp[hl][e + 1]), pack2(d.x, d.y)));
+              float e0 = lo2(y), e1 = hi2(y);
+              if (mask) {  // not by the zero of p alone: dP of a masked place may be anything
+                const int lo = diag_row + 16 * hl + 8 * (k & 1);
+                e0 = 8 * j >= lo && 8 * j < hi ? e0 : 0.f;
+                e1 = 8 * j + 1 >= lo && 8 * j + 1 < hi ? e1 : 0.f;
+              }
+              dd[hl][(e / 2) & 3] = pack_bf16x2(e0, e1);
             }
-            dd[hl][e / 2] = pack_bf16x2(e0, e1);
           }
+          hand_over(T_DP, hf, dd, ds_half);
         }
-#pragma unroll
-        for (int hl = 0; hl < 2; ++hl) tmem_st_frag(trow + (uint32_t)(hl << 20) + T_DP + g * 32, dd[hl]);
       });
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
     }
     const bool have = n_st > 0 && ok && warp_wait(acc_full, 0, abort_flag, p.err, KID_PACKED, 63);
     if (have) tc_fence_after();
