@@ -8,7 +8,9 @@ stream_prefetch and the pool, model and building-block calls.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -394,12 +396,15 @@ def _rows2d(t, name: str, rows: int, width: int) -> int:
     stride in elements (a multiple of 8, as 16-byte rows need)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[0] < rows or t.shape[1] != width:
-        raise ValueError(f"{name}: expected bf16 [>= {rows}, {width}], got {t.dtype} {tuple(t.shape)}")
-    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
-    if (width > 1 and t.stride(1) != 1) or ld < width or ld % 8 or ld >= 1 << 31:
+    shape = t.shape
+    if t.dtype is not torch.bfloat16 or len(shape) != 2 or shape[0] < rows or shape[1] != width:
+        raise ValueError(f"{name}: expected bf16 [>= {rows}, {width}], got {t.dtype} {tuple(shape)}")
+    ld, col = t.stride()
+    if shape[0] <= 1 and ld < width:
+        ld = width
+    if col != 1 or ld < width or ld & 7 or ld >= 1 << 31:
         raise ValueError(f"{name}: strides {t.stride()} (unit column stride; row stride a multiple of 8, at least the width)")
-    if t.data_ptr() % 16:
+    if t.data_ptr() & 15:
         raise ValueError(f"{name}: must be 16-byte aligned")
     return ld
 
@@ -421,31 +426,39 @@ def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
     return True
 
 
-class _On:
-    """The device of a call's tensors made current, and its stream: `stream`, or the
-    device's current one.  Everything the call allocates belongs to that stream."""
+# The packed calls of a short batch take a few microseconds on the GPU, less than their own
+# way through Python: what follows keeps that way short (argument structs by struct.pack,
+# the raw current stream, the head configurations remembered by value).
+_ATTENTION = struct.Struct("9P8i")       # nf4ls_packed_attention
+_ROPE_ROWS = struct.Struct("6P8if4x")    # nf4ls_rope_rows
+_LOGITS = struct.Struct("Pqi4xP")        # nf4ls_logits
+_PREF_OUT = struct.Struct("6P")          # nf4ls_preference_out
+_POLICY_CFG = struct.Struct("4f")        # nf4ls_policy_cfg
+_POLICY_ROWS = struct.Struct("4P")       # nf4ls_policy_rows
+_PREF_CFG = struct.Struct("i2f")         # nf4ls_preference_cfg
 
-    def __init__(self, device, stream, **tensors):
-        for name, t in tensors.items():
-            if t is not None and t.device != device:
-                raise ValueError(f"{name}: on {t.device}, the call is on {device}")
-        if device.type != "cuda":
-            raise ValueError(f"{next(iter(tensors))}: must be a CUDA tensor")
-        if stream is not None and stream.device != device:
+
+def _elsewhere(device, stream, *tensors):
+    """Checks that the call's tensors are on `device`, a CUDA device, and returns the context
+    to make the call in when that is not the current device, or a stream is given (what the
+    call allocates then belongs to that stream), else None."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors on {device}: must be CUDA tensors")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"a tensor on {t.device}, the call is on {device}")
+    if stream is not None:
+        if stream.device != device:
             raise ValueError(f"stream: on {stream.device}, the call is on {device}")
-        self.ctx = torch.cuda.stream(stream) if stream is not None else \
-            torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
-
-    def __enter__(self) -> ctypes.c_void_p:
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *exc) -> None:
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        return torch.cuda.stream(stream)
+    return None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
+def _current(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+@functools.lru_cache(maxsize=64)
 def _heads(n_q: int, n_kv: int, head_dim: int, scale) -> B.PackedHeads:
     if head_dim not in (64, 128):
         raise ValueError(f"head_dim {head_dim}: 64 or 128")
@@ -470,14 +483,18 @@ def packed_attention_fwd(pack: PackedRows, q, k, v, n_q: int, n_kv: int, head_di
         ld_o = _rows2d(out, "out", rows, qd)
         if any(_overlap(out, t) for t in (q, k, v)):
             raise ValueError("out: overlaps an input")
-    with _On(pack.device, stream, q=q, k=k, v=v, out=out) as s:
-        if out is None:
-            out, ld_o = torch.empty(rows, qd, dtype=torch.bfloat16, device=pack.device), qd
-        lse = torch.empty(n_q, rows, dtype=torch.float32, device=pack.device)
-        if rows:
-            t = B.PackedAttention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), None, None,
-                                  None, None, ld_q, ld_k, ld_v, ld_o, 0, 0, 0, 0)
-            B.call("nf4ls_packed_attention_fwd", pack._ref, ctypes.byref(heads), ctypes.byref(t), s)
+    dev = pack.device
+    ctx = _elsewhere(dev, stream, q, k, v, out)
+    if ctx is not None:
+        with ctx:
+            return packed_attention_fwd(pack, q, k, v, n_q, n_kv, head_dim, scale, out)
+    if out is None:
+        out, ld_o = torch.empty((rows, qd), dtype=torch.bfloat16, device=dev), qd
+    lse = torch.empty((n_q, rows), dtype=torch.float32, device=dev)
+    if rows:
+        B.call("nf4ls_packed_attention_fwd", pack._ref, heads,
+               _ATTENTION.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), 0, 0, 0, 0,
+                               ld_q, ld_k, ld_v, ld_o, 0, 0, 0, 0), _current(dev))
     return out, lse
 
 
@@ -498,17 +515,22 @@ def packed_attention_bwd(pack: PackedRows, q, k, v, o, do, lse, n_q: int, n_kv: 
         if any(_overlap(a, b) for a in out for b in (q, k, v, o, do)) or _overlap(dq, dk) or _overlap(dq, dv) or \
                 _overlap(dk, dv):
             raise ValueError("out: overlaps an input or another output")
-    with _On(pack.device, stream, q=q, k=k, v=v, o=o, do=do, lse=lse, dq=dq, dk=dk, dv=dv) as s:
-        if out is None:
-            dq, dk, dv = (torch.empty(rows, w, dtype=torch.bfloat16, device=pack.device) for w in (qd, kvd, kvd))
-            ld_dq, ld_dk, ld_dv = qd, kvd, kvd
-        if rows:
-            nb = B.lib().nf4ls_packed_attention_ws_bytes(pack._ref, ctypes.byref(heads))
-            ws = _buffer(nb, pack.device)
-            t = B.PackedAttention(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                  do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ld_q, ld_k, ld_v, ld_o,
-                                  ld_do, ld_dq, ld_dk, ld_dv)
-            B.call("nf4ls_packed_attention_bwd", pack._ref, ctypes.byref(heads), ctypes.byref(t), _p(ws), nb, s)
+    dev = pack.device
+    ctx = _elsewhere(dev, stream, q, k, v, o, do, lse, dq, dk, dv)
+    if ctx is not None:
+        with ctx:
+            return packed_attention_bwd(pack, q, k, v, o, do, lse, n_q, n_kv, head_dim, scale, out)
+    if out is None:
+        dq, ld_dq = torch.empty((rows, qd), dtype=torch.bfloat16, device=dev), qd
+        dk, ld_dk = torch.empty((rows, kvd), dtype=torch.bfloat16, device=dev), kvd
+        dv, ld_dv = torch.empty((rows, kvd), dtype=torch.bfloat16, device=dev), kvd
+    if rows:
+        nb = B.lib().nf4ls_packed_attention_ws_bytes(pack._ref, heads)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        B.call("nf4ls_packed_attention_bwd", pack._ref, heads,
+               _ATTENTION.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(),
+                               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ld_q, ld_k, ld_v, ld_o, ld_do, ld_dq,
+                               ld_dk, ld_dv), ws.data_ptr(), nb, _current(dev))
     return dq, dk, dv
 
 
@@ -546,6 +568,8 @@ class Rope:
         self.turns_host = turns
         self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
         self.device = self.turns.device
+        self._turns = self.turns.data_ptr()
+        self._ref = ctypes.byref(self.cfg)
 
 
 def rope_apply(rope: Rope, positions: torch.Tensor, q, k, n_q: int, n_kv: int, inverse: bool = False, out=None,
@@ -568,15 +592,19 @@ def rope_apply(rope: Rope, positions: torch.Tensor, q, k, n_q: int, n_kv: int, i
             return _overlap(a, b) and not (a.data_ptr() == b.data_ptr() and a.stride() == b.stride())
         if clash(qo, q) or clash(ko, k) or _overlap(qo, k) or _overlap(ko, q) or _overlap(qo, ko):
             raise ValueError("out: overlaps an input or another output")
-    with _On(rope.device, stream, positions=positions, q=q, k=k, out_q=qo, out_k=ko) as s:
-        if out is None:
-            qo = torch.empty(rows, n_q * d, dtype=torch.bfloat16, device=q.device)
-            ko = torch.empty(rows, n_kv * d, dtype=torch.bfloat16, device=q.device)
-            ld_qo, ld_ko = n_q * d, n_kv * d
-        if rows:
-            t = B.RopeRows(rope.turns.data_ptr(), positions.data_ptr(), q.data_ptr(), k.data_ptr(), qo.data_ptr(),
-                           ko.data_ptr(), rows, n_q, n_kv, ld_q, ld_k, ld_qo, ld_ko, int(bool(inverse)), rope.mscale)
-            B.call("nf4ls_rope_apply", ctypes.byref(rope.cfg), ctypes.byref(t), s)
+    dev = rope.device
+    ctx = _elsewhere(dev, stream, positions, q, k, qo, ko)
+    if ctx is not None:
+        with ctx:
+            return rope_apply(rope, positions, q, k, n_q, n_kv, inverse, out)
+    if out is None:
+        qo, ld_qo = torch.empty((rows, n_q * d), dtype=torch.bfloat16, device=dev), n_q * d
+        ko, ld_ko = torch.empty((rows, n_kv * d), dtype=torch.bfloat16, device=dev), n_kv * d
+    if rows:
+        B.call("nf4ls_rope_apply", rope._ref,
+               _ROPE_ROWS.pack(rope._turns, positions.data_ptr(), q.data_ptr(), k.data_ptr(), qo.data_ptr(),
+                               ko.data_ptr(), rows, n_q, n_kv, ld_q, ld_k, ld_qo, ld_ko, 1 if inverse else 0,
+                               rope.mscale), _current(dev))
     return qo, ko
 
 
@@ -600,10 +628,13 @@ class PreferenceForward:
 def _logits2d(t, name: str, rows: int) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[0] < rows or t.shape[1] < 1:
-        raise ValueError(f"{name}: expected bf16 [>= {rows}, vocab], got {t.dtype} {tuple(t.shape)}")
-    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-    if (t.shape[1] > 1 and t.stride(1) != 1) or ld < t.shape[1]:
+    shape = t.shape
+    if t.dtype is not torch.bfloat16 or len(shape) != 2 or shape[0] < rows or shape[1] < 1:
+        raise ValueError(f"{name}: expected bf16 [>= {rows}, vocab], got {t.dtype} {tuple(shape)}")
+    ld, col = t.stride()
+    if shape[0] <= 1 and ld < shape[1]:
+        ld = shape[1]
+    if (col != 1 and shape[1] > 1) or ld < shape[1]:
         raise ValueError(f"{name}: strides {t.stride()} (unit column stride; row stride at least the vocab)")
     return ld
 
@@ -632,16 +663,20 @@ def preference_loss_fwd(pack: PackedRows, logits: torch.Tensor, targets: torch.T
     ld = _logits2d(logits, "logits", n)
     _need(targets, "targets", torch.int32, n)
     _need(ref_logp, "ref_logp", torch.float32, pack.n_seqs)
-    cfg = B.PreferenceCfg(PREFERENCE_KINDS[kind], beta, label_smoothing)
-    with _On(pack.device, stream, logits=logits, targets=targets, ref_logp=ref_logp) as s:
-        # row_stats first: 16-byte rows
-        m = pack.n_seqs
-        buf = torch.empty(5 * n + 2 * m + m // 2 + 1, dtype=torch.float32, device=pack.device)
-        stats, logp, seq_logp, coef, margin, loss = buf.split((4 * n, n, m, m, m // 2, 1))
-        o = B.PreferenceOut(loss.data_ptr(), seq_logp.data_ptr(), margin.data_ptr(), coef.data_ptr(), logp.data_ptr(),
-                            stats.data_ptr())
-        t = B.Logits(logits.data_ptr(), ld, logits.shape[1], targets.data_ptr())
-        B.call("nf4ls_preference_fwd", pack._ref, ctypes.byref(cfg), ctypes.byref(t), _p(ref_logp), ctypes.byref(o), s)
+    dev = pack.device
+    ctx = _elsewhere(dev, stream, logits, targets, ref_logp)
+    if ctx is not None:
+        with ctx:
+            return preference_loss_fwd(pack, logits, targets, ref_logp, beta, kind, label_smoothing)
+    m = pack.n_seqs
+    # row_stats first: 16-byte rows
+    buf = torch.empty(5 * n + 2 * m + m // 2 + 1, dtype=torch.float32, device=dev)
+    stats, logp, seq_logp, coef, margin, loss = torch.split_with_sizes(buf, (4 * n, n, m, m, m // 2, 1))
+    at = buf.data_ptr()
+    B.call("nf4ls_preference_fwd", pack._ref, _PREF_CFG.pack(PREFERENCE_KINDS[kind], beta, label_smoothing),
+           _LOGITS.pack(logits.data_ptr(), ld, logits.shape[1], targets.data_ptr()), ref_logp.data_ptr(),
+           _PREF_OUT.pack(at + 4 * (5 * n + 2 * m + m // 2), at + 20 * n, at + 4 * (5 * n + 2 * m),
+                          at + 4 * (5 * n + m), at + 16 * n, at), _current(dev))
     return PreferenceForward(loss, seq_logp, margin, logp, coef, stats)
 
 
@@ -658,14 +693,18 @@ def preference_loss_bwd(pack: PackedRows, logits: torch.Tensor, targets: torch.T
     _need(fwd.row_stats, "row_stats", torch.float32, 4 * n)
     _need(fwd.coef, "coef", torch.float32, pack.n_seqs)
     ld_d = _grad_rows(out, logits, n) if out is not None else logits.shape[1]
-    with _On(pack.device, stream, logits=logits, targets=targets, row_stats=fwd.row_stats, coef=fwd.coef,
-             out=out) as s:
-        if out is None:
-            out = torch.empty(n, ld_d, dtype=torch.bfloat16, device=pack.device)
-        if n:
-            o = B.PreferenceOut(None, None, None, fwd.coef.data_ptr(), None, fwd.row_stats.data_ptr())
-            t = B.Logits(logits.data_ptr(), ld, logits.shape[1], targets.data_ptr())
-            B.call("nf4ls_preference_bwd", pack._ref, ctypes.byref(t), ctypes.byref(o), grad_scale, _p(out), ld_d, s)
+    dev = pack.device
+    ctx = _elsewhere(dev, stream, logits, targets, fwd.row_stats, fwd.coef, out)
+    if ctx is not None:
+        with ctx:
+            return preference_loss_bwd(pack, logits, targets, fwd, grad_scale, out)
+    if out is None:
+        out = torch.empty((n, ld_d), dtype=torch.bfloat16, device=dev)
+    if n:
+        B.call("nf4ls_preference_bwd", pack._ref,
+               _LOGITS.pack(logits.data_ptr(), ld, logits.shape[1], targets.data_ptr()),
+               _PREF_OUT.pack(0, 0, 0, fwd.coef.data_ptr(), 0, fwd.row_stats.data_ptr()), grad_scale, out.data_ptr(),
+               ld_d, _current(dev))
     return out
 
 
@@ -689,17 +728,22 @@ def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Ten
     if out is not None and not grad:
         raise ValueError("out: without grad there is no gradient to write")
     ld_d = _grad_rows(out, logits, n) if out is not None else logits.shape[1]
-    cfg = B.PolicyCfg(clip_low, clip_high, kl_coef, grad_scale)
-    with _On(logits.device, stream, logits=logits, targets=targets, out=out, **rows) as s:
-        buf = torch.empty(2 * n + 1, dtype=torch.float32, device=logits.device)
-        logp, row_loss, loss = buf.split((n, n, 1))
-        if grad and out is None:
-            out = torch.empty(n, ld_d, dtype=torch.bfloat16, device=logits.device)
-        t = B.Logits(logits.data_ptr(), ld, logits.shape[1], targets.data_ptr())
-        r = B.PolicyRows(old_logp.data_ptr(), 0 if ref_logp is None else ref_logp.data_ptr(), advantages.data_ptr(),
-                         weights.data_ptr())
-        B.call("nf4ls_policy_loss", ctypes.byref(cfg), n, ctypes.byref(t), ctypes.byref(r), loss.data_ptr(),
-               logp.data_ptr(), row_loss.data_ptr(), _p(out), ld_d, s)
+    dev = logits.device
+    ctx = _elsewhere(dev, stream, targets, old_logp, ref_logp, advantages, weights, out)
+    if ctx is not None:
+        with ctx:
+            return policy_loss(logits, targets, old_logp, ref_logp, advantages, weights, clip_low, clip_high, kl_coef,
+                               grad, grad_scale, out)
+    buf = torch.empty(2 * n + 1, dtype=torch.float32, device=dev)
+    logp, _, loss = torch.split_with_sizes(buf, (n, n, 1))
+    if grad and out is None:
+        out = torch.empty((n, ld_d), dtype=torch.bfloat16, device=dev)
+    at = buf.data_ptr()
+    B.call("nf4ls_policy_loss", _POLICY_CFG.pack(clip_low, clip_high, kl_coef, grad_scale), n,
+           _LOGITS.pack(logits.data_ptr(), ld, logits.shape[1], targets.data_ptr()),
+           _POLICY_ROWS.pack(old_logp.data_ptr(), 0 if ref_logp is None else ref_logp.data_ptr(),
+                             advantages.data_ptr(), weights.data_ptr()),
+           at + 8 * n, at, at + 4 * n, 0 if out is None else out.data_ptr(), ld_d, _current(dev))
     return loss, logp, out
 
 

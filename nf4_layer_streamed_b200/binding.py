@@ -204,18 +204,14 @@ SIGNATURES = {
     "nf4ls_pack_layout": (ctypes.c_int, [P, I32, ctypes.POINTER(Pack)]),
     "nf4ls_pack_fill": (ctypes.c_int, [P, ctypes.POINTER(Pack), P, SZ]),
     "nf4ls_packed_attention_ws_bytes": (SZ, [ctypes.POINTER(Pack), ctypes.POINTER(PackedHeads)]),
-    "nf4ls_packed_attention_fwd": (ctypes.c_int, [ctypes.POINTER(Pack), ctypes.POINTER(PackedHeads),
-                                                  ctypes.POINTER(PackedAttention), P]),
-    "nf4ls_packed_attention_bwd": (ctypes.c_int, [ctypes.POINTER(Pack), ctypes.POINTER(PackedHeads),
-                                                  ctypes.POINTER(PackedAttention), P, SZ, P]),
+    # structs of per-call pointers as P: the callers pass bytes laid out like them
+    "nf4ls_packed_attention_fwd": (ctypes.c_int, [ctypes.POINTER(Pack), ctypes.POINTER(PackedHeads), P, P]),
+    "nf4ls_packed_attention_bwd": (ctypes.c_int, [ctypes.POINTER(Pack), ctypes.POINTER(PackedHeads), P, P, SZ, P]),
     "nf4ls_rope_table": (ctypes.c_int, [ctypes.POINTER(RopeCfg), P, ctypes.POINTER(ctypes.c_float)]),
-    "nf4ls_rope_apply": (ctypes.c_int, [ctypes.POINTER(RopeCfg), ctypes.POINTER(RopeRows), P]),
-    "nf4ls_preference_fwd": (ctypes.c_int, [ctypes.POINTER(Pack), ctypes.POINTER(PreferenceCfg),
-                                            ctypes.POINTER(Logits), P, ctypes.POINTER(PreferenceOut), P]),
-    "nf4ls_preference_bwd": (ctypes.c_int, [ctypes.POINTER(Pack), ctypes.POINTER(Logits),
-                                            ctypes.POINTER(PreferenceOut), ctypes.c_float, P, ctypes.c_int64, P]),
-    "nf4ls_policy_loss": (ctypes.c_int, [ctypes.POINTER(PolicyCfg), I32, ctypes.POINTER(Logits),
-                                         ctypes.POINTER(PolicyRows), P, P, P, P, ctypes.c_int64, P]),
+    "nf4ls_rope_apply": (ctypes.c_int, [ctypes.POINTER(RopeCfg), P, P]),
+    "nf4ls_preference_fwd": (ctypes.c_int, [ctypes.POINTER(Pack), P, P, P, P, P]),
+    "nf4ls_preference_bwd": (ctypes.c_int, [ctypes.POINTER(Pack), P, P, ctypes.c_float, P, ctypes.c_int64, P]),
+    "nf4ls_policy_loss": (ctypes.c_int, [P, I32, P, P, P, P, P, P, ctypes.c_int64, P]),
 }
 
 _LIB = None

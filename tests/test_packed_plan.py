@@ -140,3 +140,14 @@ def test_attention_c_calls_check_their_arguments_on_the_host():
     pack.n_tiles = 13                                           # not what the layout gave
     assert fwd() == -1
     assert B.call_status("nf4ls_packed_attention_fwd", None, ctypes.byref(heads), ctypes.byref(t), None) == -1
+
+
+def test_argument_structs_are_laid_out_like_the_bindings():
+    for packed, struct in ((api._ATTENTION, B.PackedAttention), (api._ROPE_ROWS, B.RopeRows),
+                           (api._LOGITS, B.Logits), (api._PREF_OUT, B.PreferenceOut), (api._POLICY_CFG, B.PolicyCfg),
+                           (api._POLICY_ROWS, B.PolicyRows), (api._PREF_CFG, B.PreferenceCfg)):
+        assert packed.size == ctypes.sizeof(struct)
+        n = len(struct._fields_)
+        values = [float(i + 1) if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(struct._fields_)]
+        got = struct.from_buffer_copy(packed.pack(*values))
+        assert [getattr(got, name) for name, _ in struct._fields_] == values and n == len(values)
