@@ -454,6 +454,11 @@ def _elsewhere(device, stream, *tensors):
     return None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
+def _rows_like(t: torch.Tensor, rows: int) -> torch.Tensor:
+    """A new matrix of `rows` contiguous rows of t's width and type."""
+    return torch.empty_like(t) if t.shape[0] == rows else t.new_empty((rows, t.shape[1]))
+
+
 def _current(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
@@ -489,8 +494,8 @@ def packed_attention_fwd(pack: PackedRows, q, k, v, n_q: int, n_kv: int, head_di
         with ctx:
             return packed_attention_fwd(pack, q, k, v, n_q, n_kv, head_dim, scale, out)
     if out is None:
-        out, ld_o = torch.empty((rows, qd), dtype=torch.bfloat16, device=dev), qd
-    lse = torch.empty((n_q, rows), dtype=torch.float32, device=dev)
+        out, ld_o = _rows_like(q, rows), qd
+    lse = q.new_empty((n_q, rows), dtype=torch.float32)
     if rows:
         B.call("nf4ls_packed_attention_fwd", pack._ref, heads,
                _ATTENTION.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), 0, 0, 0, 0,
@@ -521,9 +526,9 @@ def packed_attention_bwd(pack: PackedRows, q, k, v, o, do, lse, n_q: int, n_kv: 
         with ctx:
             return packed_attention_bwd(pack, q, k, v, o, do, lse, n_q, n_kv, head_dim, scale, out)
     if out is None:
-        dq, ld_dq = torch.empty((rows, qd), dtype=torch.bfloat16, device=dev), qd
-        dk, ld_dk = torch.empty((rows, kvd), dtype=torch.bfloat16, device=dev), kvd
-        dv, ld_dv = torch.empty((rows, kvd), dtype=torch.bfloat16, device=dev), kvd
+        dq, ld_dq = _rows_like(q, rows), qd
+        dk, ld_dk = _rows_like(k, rows), kvd
+        dv, ld_dv = _rows_like(v, rows), kvd
     if rows:
         nb = B.lib().nf4ls_packed_attention_ws_bytes(pack._ref, heads)
         ws = torch.empty(nb, dtype=torch.uint8, device=dev)
@@ -598,8 +603,8 @@ def rope_apply(rope: Rope, positions: torch.Tensor, q, k, n_q: int, n_kv: int, i
         with ctx:
             return rope_apply(rope, positions, q, k, n_q, n_kv, inverse, out)
     if out is None:
-        qo, ld_qo = torch.empty((rows, n_q * d), dtype=torch.bfloat16, device=dev), n_q * d
-        ko, ld_ko = torch.empty((rows, n_kv * d), dtype=torch.bfloat16, device=dev), n_kv * d
+        qo, ld_qo = _rows_like(q, rows), n_q * d
+        ko, ld_ko = _rows_like(k, rows), n_kv * d
     if rows:
         B.call("nf4ls_rope_apply", rope._ref,
                _ROPE_ROWS.pack(rope._turns, positions.data_ptr(), q.data_ptr(), k.data_ptr(), qo.data_ptr(),
@@ -699,7 +704,7 @@ def preference_loss_bwd(pack: PackedRows, logits: torch.Tensor, targets: torch.T
         with ctx:
             return preference_loss_bwd(pack, logits, targets, fwd, grad_scale, out)
     if out is None:
-        out = torch.empty((n, ld_d), dtype=torch.bfloat16, device=dev)
+        out = _rows_like(logits, n)
     if n:
         B.call("nf4ls_preference_bwd", pack._ref,
                _LOGITS.pack(logits.data_ptr(), ld, logits.shape[1], targets.data_ptr()),
@@ -737,7 +742,7 @@ def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Ten
     buf = torch.empty(2 * n + 1, dtype=torch.float32, device=dev)
     logp, _, loss = torch.split_with_sizes(buf, (n, n, 1))
     if grad and out is None:
-        out = torch.empty((n, ld_d), dtype=torch.bfloat16, device=dev)
+        out = _rows_like(logits, n)
     at = buf.data_ptr()
     B.call("nf4ls_policy_loss", _POLICY_CFG.pack(clip_low, clip_high, kl_coef, grad_scale), n,
            _LOGITS.pack(logits.data_ptr(), ld, logits.shape[1], targets.data_ptr()),

@@ -58,7 +58,7 @@ def check_grad(got, x, t, has, c, dc):
     assert off <= 1.0
 
 
-VOCABS = [1, 7, 64, 1000, 49152, 50257, 128256]
+VOCABS = [1, 7, 64, 1000, 49152, 50257, 128256, 262147]
 
 
 @pytest.mark.parametrize("kind,eps", [("sigmoid", 0.0), ("sigmoid", 0.1), ("hinge", 0.0), ("squared", 0.0)])
