@@ -8,9 +8,6 @@
 //     that reads them again and writes the gradient;
 //   policy: the coefficient follows from the row alone: statistics and gradient in one launch.
 // What bounds them is memory: rows of up to 128 k logits are read and written once per pass.
-// A cluster of blocks holds a row in its registers (up to 64 values a thread), so the
-// policy gradient does not read the row a second time: 1999 rows of 128 k logits read 344
-// instead of 690 MB from DRAM.
 #include <algorithm>
 #include <cmath>
 
@@ -135,15 +132,16 @@ __device__ __forceinline__ void block_grad(const __nv_bfloat16* in, __nv_bfloat1
     for (int e = 0; e < 4; ++e) r[e] = pack_bf16x2(g(bf16_lo(w[e]), i0 + 2 * e), g(bf16_hi(w[e]), i0 + 2 * e + 1));
     o[j] = make_uint4(r[0], r[1], r[2], r[3]);
   };
-  int j = t;
-  for (; j + 3 * LT < sp.n16; j += 4 * LT) {
-    const uint4 a = v[j], b = v[j + LT], c = v[j + 2 * LT], d = v[j + 3 * LT];
+  // last pieces first: the statistics pass over the same row has left them in L2
+  int j = t + (sp.n16 - 1 - t) / LT * LT;  // this thread's last piece (below t: none)
+  for (; j >= t + 3 * LT; j -= 4 * LT) {
+    const uint4 a = v[j], b = v[j - LT], c = v[j - 2 * LT], d = v[j - 3 * LT];
     piece(a, j);
-    piece(b, j + LT);
-    piece(c, j + 2 * LT);
-    piece(d, j + 3 * LT);
+    piece(b, j - LT);
+    piece(c, j - 2 * LT);
+    piece(d, j - 3 * LT);
   }
-  for (; j < sp.n16; j += LT) piece(v[j], j);
+  for (; j >= t && j < sp.n16; j -= LT) piece(v[j], j);
   const int i = sp.tail0 + t;
   if (i < V) out[i] = __float2bfloat16_rn(g(__bfloat162float(in[i]), i));
 }
@@ -153,7 +151,7 @@ __device__ __forceinline__ void block_zero(__nv_bfloat16* out, int V) {
   const int t = threadIdx.x;
   if (t < sp.head) out[t] = __float2bfloat16_rn(0.f);
   uint4* o = reinterpret_cast<uint4*>(out + sp.head);
-  for (int j = t; j < sp.n16; j += LT) o[j] = make_uint4(0u, 0u, 0u, 0u);
+  for (int j = t; j < sp.n16; j += blockDim.x) o[j] = make_uint4(0u, 0u, 0u, 0u);
   if (sp.tail0 + t < V) out[sp.tail0 + t] = __float2bfloat16_rn(0.f);
 }
 
@@ -167,111 +165,11 @@ __device__ __forceinline__ double target_logp(float xt, Stat st) {
 __device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-constexpr int NV = 8;             // 16-byte pieces of a row in a thread's registers
-constexpr int MAX_CLUSTER = 8;    // blocks that share a row
-constexpr int CLUSTER_ROW = LT * NV * 8;  // values that one block holds
-
-// One row's part in registers: rank's share of the row's whole pieces; the values in front
-// of the first and behind the last 16-byte boundary go to rank 0's first threads.
-struct RowPart {
-  RowSplit sp;
-  int first, count;  // pieces of this rank
-  uint4 v[NV];
-  float edge0, edge1;
-  __device__ RowPart(const __nv_bfloat16* row, int V, int rank, int ranks) : sp(row, V) {
-    const int per = (sp.n16 + ranks - 1) / ranks;
-    first = min(rank * per, sp.n16);
-    count = min(per, sp.n16 - first);
-    const uint4* p = reinterpret_cast<const uint4*>(row + sp.head) + first;
-    const int t = threadIdx.x;
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (t + k * LT < count) v[k] = p[t + k * LT];
-    edge0 = rank == 0 && t < sp.head ? __bfloat162float(row[t]) : -INFINITY;
-    edge1 = rank == 0 && sp.tail0 + t < V ? __bfloat162float(row[sp.tail0 + t]) : -INFINITY;
-  }
-};
-
-// The row's statistics from all ranks' parts, in a fixed order.  Every block of the cluster
-// has arrived once before (cluster_begin): its shared memory may be written to.
-__device__ __forceinline__ void cluster_begin(int ranks) {
-  if (ranks > 1) cluster_arrive_relaxed();
-}
-__device__ __forceinline__ Stat cluster_stats(const RowPart& p, int rank, int ranks) {
-  __shared__ Stat red[LT / 32];
-  __shared__ Stat all[MAX_CLUSTER];
-  const int t = threadIdx.x;
-  Stat st = {-INFINITY, 0.0f};
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-    if (t + k * LT < p.count) add8(st, p.v[k]);
-  if (rank == 0) {
-    add1(st, p.edge0);
-    add1(st, p.edge1);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    st = merge(st, {__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o)});
-  if ((t & 31) == 0) red[t >> 5] = st;
-  if (ranks > 1) cluster_wait();
-  __syncthreads();
-  if (t < 32) {
-    st = t < LT / 32 ? red[t] : Stat{-INFINITY, 0.0f};
-#pragma unroll
-    for (int o = LT / 64; o > 0; o >>= 1)
-      st = merge(st, {__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o)});
-    st.m = __shfl_sync(0xffffffffu, st.m, 0);
-    st.s = __shfl_sync(0xffffffffu, st.s, 0);
-    if (ranks == 1) {
-      if (t == 0) all[0] = st;
-    } else if (t < ranks) {  // to every block of the cluster, this one among them
-      const uint32_t a = mapa_shared(smem_u32(&all[rank]), t);
-      st_cluster_f32(a, st.m);
-      st_cluster_f32(a + 4, st.s);
-    }
-  }
-  if (ranks == 1) {
-    __syncthreads();
-  } else {
-    cluster_sync_all();
-  }
-  st = all[0];
-  for (int i = 1; i < ranks; ++i) st = merge(st, all[i]);
-  return st;
-}
-
-// Grid: rows x cluster ranks.
-__global__ void __launch_bounds__(LT, 2) k_token_logp(const __nv_bfloat16* __restrict__ logits, int64_t ld, int V,
-                                                      const int32_t* __restrict__ targets, float4* __restrict__ stats,
-                                                      float* __restrict__ logp, int ranks) {
-  next_may_start();
-  const int row = blockIdx.x / ranks, rank = blockIdx.x - row * ranks;
-  const int target = targets[row];
-  if (target < 0 || target >= V) {  // every block of the cluster
-    if (rank == 0 && threadIdx.x == 0) {
-      stats[row] = make_float4(0.f, 1.f, 0.f, 0.f);
-      logp[row] = 0.f;
-    }
-    return;
-  }
-  cluster_begin(ranks);
-  const __nv_bfloat16* x = logits + (size_t)row * ld;
-  const float xt = __bfloat162float(x[target]);
-  const RowPart part(x, V, rank, ranks);
-  const Stat st = cluster_stats(part, rank, ranks);
-  if (rank == 0 && threadIdx.x == 0) {
-    const double lp = target_logp(xt, st);
-    const float hi = (float)lp;
-    // what the rounding of logp leaves out, for the sums over a sequence
-    stats[row] = make_float4(st.m, st.s, isfinite(hi) ? (float)(lp - (double)hi) : 0.f, 0.f);
-    logp[row] = hi;
-  }
-}
-
-// The same for rows that no cluster holds.
-__global__ void __launch_bounds__(LT) k_token_logp_long(const __nv_bfloat16* __restrict__ logits, int64_t ld, int V,
-                                                        const int32_t* __restrict__ targets,
-                                                        float4* __restrict__ stats, float* __restrict__ logp) {
+// A block per row.  (Clusters that share a row measured 140 us for 2048 rows of 128 k logits,
+// this 73: small independent blocks, four to an SM, hide the reductions' waits best.)
+__global__ void __launch_bounds__(LT) k_token_logp(const __nv_bfloat16* __restrict__ logits, int64_t ld, int V,
+                                                   const int32_t* __restrict__ targets, float4* __restrict__ stats,
+                                                   float* __restrict__ logp) {
   next_may_start();
   const int row = blockIdx.x;
   const int target = targets[row];
@@ -354,7 +252,7 @@ __global__ void __launch_bounds__(PT) k_preference(const int32_t* __restrict__ c
   }
 }
 
-__global__ void __launch_bounds__(LT) k_logits_grad(const __nv_bfloat16* logits, int64_t ld, int V,
+__global__ void __launch_bounds__(LT, 4) k_logits_grad(const __nv_bfloat16* logits, int64_t ld, int V,
                                                     const int32_t* __restrict__ targets,
                                                     const float4* __restrict__ stats, const int32_t* __restrict__ seq,
                                                     const float* __restrict__ coef, float scale, __nv_bfloat16* dlogits,
@@ -384,8 +282,8 @@ struct PolicyParams {
   float *logp, *row_loss;
 };
 
-// By one thread: the row's loss and the coefficient of its gradient; write: into memory too.
-__device__ __forceinline__ float policy_row(const PolicyParams& p, int row, float xt, Stat st, bool write) {
+// By one thread: the row's loss, into memory, and the coefficient of its gradient.
+__device__ __forceinline__ float policy_row(const PolicyParams& p, int row, float xt, Stat st) {
   const double lp = target_logp(xt, st);
   const float a = p.adv[row], w = p.weights[row];
   const float r = expf((float)(lp - (double)p.old_logp[row]));
@@ -394,94 +292,30 @@ __device__ __forceinline__ float policy_row(const PolicyParams& p, int row, floa
   const bool passes = free_s <= held;  // the gradient flows through the unclipped term
   // no KL term where its coefficient is 0 (ref_logp may then be null)
   const float gap = p.kl > 0.0f ? (float)((double)p.ref_logp[row] - lp) : 0.0f, e1 = expm1f(gap);
-  if (write) {
-    const float surrogate = isnan(r) ? r : (passes ? free_s : held);
-    p.logp[row] = (float)lp;
-    p.row_loss[row] = w * (p.kl * (e1 - gap) - surrogate);
-  }
+  const float surrogate = isnan(r) ? r : (passes ? free_s : held);
+  p.logp[row] = (float)lp;
+  p.row_loss[row] = w * (p.kl * (e1 - gap) - surrogate);
   return w * (-p.kl * e1 - (passes ? free_s : 0.0f)) * p.scale;
 }
 
-// A row without a target; the ranks share the zeros.
-__device__ __forceinline__ void policy_no_row(const PolicyParams& p, int row, __nv_bfloat16* out, int rank, int ranks) {
-  if (rank == 0 && threadIdx.x == 0) {
-    p.logp[row] = 0.f;
-    p.row_loss[row] = 0.f;
-  }
-  if (!out) return;
-  const int per = ((p.V + ranks - 1) / ranks + 7) & ~7, a = min(rank * per, p.V);
-  block_zero(out + a, min(per, p.V - a));
-}
-
-// Grid: rows x cluster ranks; the row stays in the cluster's registers from the statistics
-// to the gradient.
-__global__ void __launch_bounds__(LT, 2) k_policy(const PolicyParams p, int ranks) {
-  __shared__ float c_sh;
-  next_may_start();
-  const int row = blockIdx.x / ranks, rank = blockIdx.x - row * ranks;
-  const int t = threadIdx.x, target = p.targets[row];
-  __nv_bfloat16* out = p.dlogits ? p.dlogits + (size_t)row * p.ld_d : nullptr;
-  if (target < 0 || target >= p.V) {  // every block of the cluster
-    policy_no_row(p, row, out, rank, ranks);
-    return;
-  }
-  cluster_begin(ranks);
-  const __nv_bfloat16* x = p.logits + (size_t)row * p.ld;
-  // before the cluster's barrier: behind it the gradient may overwrite the row in place
-  const float xt = __bfloat162float(x[target]);
-  const RowPart part(x, p.V, rank, ranks);
-  const Stat st = cluster_stats(part, rank, ranks);
-  if (t == 0) c_sh = policy_row(p, row, xt, st, rank == 0);
-  if (!out) return;
-  __syncthreads();
-  const float coef = c_sh;
-  // out = coef (onehot(target) - exp(x - m) / s); a coefficient of 0 makes zeros of any row
-  const float ref = safe_ref(st.m), k = -coef / st.s;
-  auto g = [&](float v, int i) {
-    const float e = coef == 0.0f ? 0.0f : exp2_fast((v - ref) * kLog2e) * k;
-    return i == target ? e + coef : e;
-  };
-  const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-#pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const int j = part.first + t + n * LT, i0 = part.sp.head + j * 8;
-    if (t + n * LT >= part.count) continue;
-    const uint32_t w[4] = {part.v[n].x, part.v[n].y, part.v[n].z, part.v[n].w};
-    uint32_t r[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = pack_bf16x2(g(bf16_lo(w[e]), i0 + 2 * e), g(bf16_hi(w[e]), i0 + 2 * e + 1));
-    if (same) {
-      *reinterpret_cast<uint4*>(out + i0) = make_uint4(r[0], r[1], r[2], r[3]);
-    } else {  // rows that start at different places within 16 bytes
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        out[i0 + 2 * e] = __ushort_as_bfloat16((unsigned short)r[e]);
-        out[i0 + 2 * e + 1] = __ushort_as_bfloat16((unsigned short)(r[e] >> 16));
-      }
-    }
-  }
-  if (rank == 0) {
-    if (t < part.sp.head) out[t] = __float2bfloat16_rn(g(part.edge0, t));
-    const int i = part.sp.tail0 + t;
-    if (i < p.V) out[i] = __float2bfloat16_rn(g(part.edge1, i));
-  }
-}
-
-// The same for rows that no cluster holds.
-__global__ void __launch_bounds__(LT) k_policy_long(const PolicyParams p) {
+__global__ void __launch_bounds__(LT, 4) k_policy(const PolicyParams p) {
   __shared__ float c_sh;
   next_may_start();
   const int row = blockIdx.x;
   const int target = p.targets[row];
   __nv_bfloat16* out = p.dlogits ? p.dlogits + (size_t)row * p.ld_d : nullptr;
   if (target < 0 || target >= p.V) {
-    policy_no_row(p, row, out, 0, 1);
+    if (threadIdx.x == 0) {
+      p.logp[row] = 0.f;
+      p.row_loss[row] = 0.f;
+    }
+    if (out) block_zero(out, p.V);
     return;
   }
   const __nv_bfloat16* x = p.logits + (size_t)row * p.ld;
   const float xt = __bfloat162float(x[target]);
   const Stat st = block_stats(x, p.V);
-  if (threadIdx.x == 0) c_sh = policy_row(p, row, xt, st, true);
+  if (threadIdx.x == 0) c_sh = policy_row(p, row, xt, st);
   if (!out) return;
   __syncthreads();
   const float c = c_sh;
@@ -507,23 +341,10 @@ __global__ void __launch_bounds__(PT) k_sum_rows(const float* __restrict__ v, in
   }
 }
 
-// Blocks that share a row: as many as hold it in registers, and more, up to the largest
-// portable cluster, while the rows alone leave SMs idle (96 rows of 48 k logits: 12.2 us
-// with one block a row, which also reads the row twice; see the table of the design notes
-// for what it takes now).  0: no cluster holds the row.
-int row_ranks(int rows, int V) {
-  int c = 1;
-  while (c < MAX_CLUSTER && (int64_t)c * CLUSTER_ROW < V) c *= 2;
-  if ((int64_t)c * CLUSTER_ROW < V) return 0;
-  while (c < MAX_CLUSTER && (int64_t)rows * c < 296 && c * LT * 8 < V) c *= 2;
-  return c;
-}
-
-// A launch that may begin while the one before it still runs (its kernel waits itself), on
-// clusters of `cluster` blocks.
+// A launch; early: it may begin while the one before it still runs (its kernel waits itself).
 template <typename... P, typename... A>
-int launch(void (*k)(P...), int64_t blocks, int threads, int cluster, bool early, cudaStream_t s, A... args) {
-  cudaLaunchAttribute at[2];
+int launch(void (*k)(P...), int64_t blocks, int threads, bool early, cudaStream_t s, A... args) {
+  cudaLaunchAttribute at[1];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3((unsigned)threads);
@@ -532,12 +353,6 @@ int launch(void (*k)(P...), int64_t blocks, int threads, int cluster, bool early
   if (early) {
     at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (cluster > 1) {
-    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    at[cfg.numAttrs].val.clusterDim.x = (unsigned)cluster;
-    at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
-    ++cfg.numAttrs;
   }
   NF4_CUDA_TRY(cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...));
   note_launch();
@@ -588,17 +403,10 @@ extern "C" int nf4ls_preference_fwd(const nf4ls_pack* pack, const nf4ls_preferen
   auto* stats = reinterpret_cast<float4*>(out->row_stats);
   if (pack->total > 0) {
     const auto* x = static_cast<const __nv_bfloat16*>(t->logits_dev);
-    const int ranks = row_ranks(pack->total, t->vocab);
-    if ((int64_t)pack->total * ranks > 0x7FFFFFFF) return fail(NF4LS_SHAPE, "%s: too many rows for one launch", who);
-    if (ranks)
-      NF4_TRY(launch(k_token_logp, (int64_t)pack->total * ranks, LT, ranks, false, s, x, t->ld, t->vocab, t->targets_dev,
-                     stats, out->logp, ranks));
-    else
-      NF4_TRY(launch(k_token_logp_long, pack->total, LT, 1, false, s, x, t->ld, t->vocab, t->targets_dev, stats,
-                     out->logp));
+    NF4_TRY(launch(k_token_logp, pack->total, LT, false, s, x, t->ld, t->vocab, t->targets_dev, stats, out->logp));
   }
   const int32_t* cu = reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(pack->plan_dev) + pack->off_cu);
-  NF4_TRY(launch(k_preference, 1, PT, 1, true, s, cu, pack->n_seqs, out->logp, stats, ref_logp_dev, c->beta,
+  NF4_TRY(launch(k_preference, 1, PT, true, s, cu, pack->n_seqs, out->logp, stats, ref_logp_dev, c->beta,
                  c->label_smoothing, c->kind, out->seq_logp, out->margin, out->coef, out->loss));
   return NF4LS_OK;
 }
@@ -614,7 +422,7 @@ extern "C" int nf4ls_preference_bwd(const nf4ls_pack* pack, const nf4ls_logits* 
   if (!aligned(saved->row_stats, 16)) return fail(NF4LS_ALIGN, "%s: row_stats must be 16-byte aligned", who);
   NF4_TRY(check_grad(t, dlogits_dev, ld_d, who));
   const int32_t* seq = reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(pack->plan_dev) + pack->off_seq);
-  NF4_TRY(launch(k_logits_grad, pack->total, LT, 1, true, static_cast<cudaStream_t>(stream),
+  NF4_TRY(launch(k_logits_grad, pack->total, LT, true, static_cast<cudaStream_t>(stream),
                  static_cast<const __nv_bfloat16*>(t->logits_dev), t->ld, t->vocab, t->targets_dev,
                  reinterpret_cast<const float4*>(saved->row_stats), seq, saved->coef, grad_scale,
                  static_cast<__nv_bfloat16*>(dlogits_dev), ld_d));
@@ -655,13 +463,8 @@ extern "C" int nf4ls_policy_loss(const nf4ls_policy_cfg* c, int32_t rows, const 
     p.scale = c->grad_scale;
     p.logp = logp_dev;
     p.row_loss = row_loss_dev;
-    const int ranks = row_ranks(rows, t->vocab);
-    if ((int64_t)rows * ranks > 0x7FFFFFFF) return fail(NF4LS_SHAPE, "%s: too many rows for one launch", who);
-    if (ranks)
-      NF4_TRY(launch(k_policy, (int64_t)rows * ranks, LT, ranks, false, s, p, ranks));
-    else
-      NF4_TRY(launch(k_policy_long, rows, LT, 1, false, s, p));
+    NF4_TRY(launch(k_policy, rows, LT, false, s, p));
   }
-  NF4_TRY(launch(k_sum_rows, 1, PT, 1, true, s, row_loss_dev, rows, loss_dev));
+  NF4_TRY(launch(k_sum_rows, 1, PT, true, s, row_loss_dev, rows, loss_dev));
   return NF4LS_OK;
 }
