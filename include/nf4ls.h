@@ -583,15 +583,14 @@ int nf4ls_attention_bwd(const nf4ls_layer_cfg* cfg, const void* q_dev, const voi
  * copies it into a 256-byte aligned device buffer and sets plan_dev.  The plan serves
  * every packed call of the batch, on any stream, and is only read.  Both are host-only.
  * In the plan: cu int32 [n_seqs + 1] (first row of each sequence, then total), positions
- * int32 [total] (row - cu of its sequence), seq int32 [total] (its sequence), and three
- * lists of 128-row tiles (query tiles, key tiles, pairs of query tiles), each sorted with
- * the most work first. */
+ * int32 [total] (row - cu of its sequence), seq int32 [total] (its sequence), and two
+ * lists of 128-row tiles (query tiles, key tiles), each sorted with the most work first. */
 #define NF4LS_PACK_MAX_SEQS (1 << 20)
 #define NF4LS_PACK_MAX_ROWS (1 << 28)
 
 typedef struct {
-    int32_t n_seqs, total, n_tiles, n_pairs, max_len, pad;
-    uint64_t off_cu, off_positions, off_seq, off_query_tiles, off_key_tiles, off_query_pairs, plan_bytes;
+    int32_t n_seqs, total, n_tiles, max_len;
+    uint64_t off_cu, off_positions, off_seq, off_query_tiles, off_key_tiles, plan_bytes;
     const void* plan_dev;
 } nf4ls_pack;
 

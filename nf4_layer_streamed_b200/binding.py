@@ -76,10 +76,11 @@ class DiskInfo(ctypes.Structure):
 
 class Pack(ctypes.Structure):
     _fields_ = [("n_seqs", ctypes.c_int32), ("total", ctypes.c_int32), ("n_tiles", ctypes.c_int32),
-                ("n_pairs", ctypes.c_int32), ("max_len", ctypes.c_int32), ("pad", ctypes.c_int32),
+                ("max_len", ctypes.c_int32),
                 ("off_cu", ctypes.c_uint64), ("off_positions", ctypes.c_uint64),
                 ("off_seq", ctypes.c_uint64), ("off_query_tiles", ctypes.c_uint64),
-                ("off_key_tiles", ctypes.c_uint64), ("off_query_pairs", ctypes.c_uint64), ("plan_bytes", ctypes.c_uint64), ("plan_dev", ctypes.c_void_p)]
+                ("off_key_tiles", ctypes.c_uint64), ("plan_bytes", ctypes.c_uint64),
+                ("plan_dev", ctypes.c_void_p)]
 
 
 class PackedHeads(ctypes.Structure):

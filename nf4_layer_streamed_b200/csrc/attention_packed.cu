@@ -94,80 +94,81 @@ __device__ __forceinline__ void store_tile(const CUtensorMap* map, __nv_bfloat16
 }
 
 // ------------------------------------------------------------------------------ forward
-// One block per pair of neighbouring 128-query tiles A, B of one head and sequence (B may be
-// missing), online softmax over the key tiles up to each one's diagonal:
+// One block per 128-query tile of one head and sequence, two blocks on an SM, online
+// softmax over the key tiles up to the diagonal:
 //   S = Q K^T; p = 2^(S scale log2e - m), the reference maximum m of a row moving only when a
 //   tile's maximum exceeds it by more than 2^8; O += P V, P as bf16 over the scores it came
 //   from; o = O / sum p.
-// Within a tile these depend on one another, so the tensor core would stand still during
-// the exponentials: the two tiles take turns, the products of one, P V(A) then S(A) of the
-// next key tile, under the exponentials of the other.  (Two blocks of one tile each on an
-// SM fall into step instead: both compute exponentials, then both want the tensor core;
-// they took 3600 cycles for a pair's step.)  K and V tiles serve both.
-// warp 0: MMA issuer, warp 1: TMA producer (the scheduler prefers its oldest warp: as the
-// last warps of the block they waited up to 600 cycles for an issue slot between busy
-// softmax warps); warps 4-11: softmax and epilogue of A, 12-19: of B (TMEM lanes
-// 32 (w % 4) .., one query row per thread, keys 64 (w / 4 % 2) .. of a tile in registers)
-constexpr int F_THREADS = 640, F_MMA = 0, F_PROD = 1, F_FIRST = 4, F_SM = 256;
-constexpr int F_OFF_Q = 0, F_OFF_K = 2 * TILE_BYTES, F_OFF_V = 4 * TILE_BYTES;  // two Q, two stages of K and of V
-constexpr int F_OFF_X = 6 * TILE_BYTES;  // row maxima (then sums): [tile A, B][2 steps][2 key halves][128]
-constexpr int F_OFF_BAR = F_OFF_X + 4096;
-constexpr int SMEM_TC = 1024 + F_OFF_BAR + 256;
+// Within a tile these depend on one another; the second block's products run meanwhile, and
+// the first half of P V under the second half's exponentials.  16.4k rows of 8B heads, the
+// tensor core's work 444 us: 740 us; 2048 rows: 25.8 us.  What bounds it is the hand-over
+// (scores to registers, P back, a wait each way), about 700 cycles of a tile's 1400, which
+// two blocks do not always fill.  Built and measured beside it (long, short): two tiles of
+// one block taking turns under one issuer, 751 and 31 us; blocks that go through a list of
+// tiles, 801 and 25.6 us (the list's state spills the scores); a row shared by two warps,
+// 854 and 28 us; three of eight exponentials by a cubic on the multiplier instead of the
+// exponential unit, 3% slower (13 issue slots for 8 cycles of the unit).  Every lane
+// waits on a barrier by itself here: one lane for its warp took 770 us, on the gradients'
+// kernels it is the faster form.
+// warps 0-3: softmax and epilogue (warp w owns TMEM lanes 32 w .. 32 w + 31, one query
+// row per thread, its 128 scores in registers); warp 4: TMA producer; warp 5: MMA issuer
+constexpr int F_THREADS = 192, F_PROD = 4, F_MMA = 5;
+constexpr int F_OFF_Q = 0, F_OFF_K = TILE_BYTES, F_OFF_V = 2 * TILE_BYTES, F_OFF_BAR = 3 * TILE_BYTES;
+constexpr int SMEM_TC = 1024 + F_OFF_BAR + 128;
 constexpr float kRescaleLog2 = 8.0f;  // the reference maximum may trail the true one by this much
 
 template <int D>
-__global__ void __launch_bounds__(F_THREADS, 1) k_packed_fwd(const __grid_constant__ FwdParams p) {
+__global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_constant__ FwdParams p) {
   constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM;  // swizzle atoms, k-steps and bytes of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + F_OFF_BAR);
-  uint64_t* q_full = bars;        // 2: A, B
-  uint64_t* k_full = bars + 2;    // 2 stages
-  uint64_t* k_empty = bars + 4;   // 2
-  uint64_t* v_full = bars + 6;    // 2
-  uint64_t* v_empty = bars + 8;   // 2
-  uint64_t* s_full = bars + 10;   // 2: A, B
-  uint64_t* p_half = bars + 12;   // [A, B][2]: P of keys 32 h .. of both key halves is in TMEM (one arrival per warp)
-  uint64_t* o_full = bars + 16;   // 2: A, B; one phase per key tile: its P V product is done
-  uint64_t* drain = bars + 18;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = bars + 1;
+  uint64_t* k_empty = bars + 2;
+  uint64_t* v_full = bars + 3;
+  uint64_t* v_empty = bars + 4;
+  uint64_t* s_full = bars + 5;
+  uint64_t* p_half = bars + 6;   // 2: P of keys 64 h .. 64 h + 63 is in TMEM (one arrival per softmax warp)
+  uint64_t* o_full = bars + 8;   // one phase per key tile: the P V product of that tile is done
+  uint64_t* drain = bars + 9;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 10);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = warp_number(), lane = threadIdx.x & 31;
-  // heads fastest, then the plan's pairs, most work first
+  // heads fastest, then the plan's tiles, most key tiles first
   const int h = blockIdx.x % p.nq;
   const PackTile pt = p.tiles[blockIdx.x / p.nq];
-  const int row0 = pt.row0, kvh = h / (p.nq / p.nkv);
-  const int n_both = pt.len > (pt.tile + 1) * TT ? 2 : 1;  // tiles of this block
-  const int nk_a = pt.tile + 1, nk = pt.tile + n_both;     // key tiles of A, and of the last tile
+  const int qt = pt.tile, row0 = pt.row0;
+  const int n_rows = min(TT, pt.len - qt * TT);  // rows of this tile (keys of the diagonal tile)
+  const int kvh = h / (p.nq / p.nkv);
+  const int nk = qt + 1;  // key tiles at or before the diagonal
 
   // by the producer: the MMA warp goes straight to the allocation, which takes a whole,
   // converged warp (beside a branch of its own first lane it faulted)
   if (warp == F_PROD && lane == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 1);
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_half[2 * i], F_SM / 32);
-      mbar_init(&p_half[2 * i + 1], F_SM / 32);
-      mbar_init(&o_full[i], 1);
-    }
+    mbar_init(q_full, 1);
+    mbar_init(k_full, 1);
+    mbar_init(k_empty, 1);
+    mbar_init(v_full, 1);
+    mbar_init(v_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(&p_half[0], 4);
+    mbar_init(&p_half[1], 4);
+    mbar_init(o_full, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == F_MMA) {
     __syncwarp();
-    tmem_alloc(tmem_slot, 512);
+    tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);  // of A: [0, 128) S then P, [128, 256) O; B behind
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);  // [0, 128) S then P, [128, 256) O
 
   if (warp == F_PROD) {
     // ------------------------------------------------------------------ TMA producer
@@ -175,34 +176,25 @@ __global__ void __launch_bounds__(F_THREADS, 1) k_packed_fwd(const __grid_consta
       tma_prefetch_desc(&p.tq);
       tma_prefetch_desc(&p.tk);
       tma_prefetch_desc(&p.tv);
-      int issued = 0;
+      mbar_arrive_expect_tx(q_full, TB);
+      for (int j = 0; j < NA; ++j) tma_load_2d(base + F_OFF_Q + j * ATOM, &p.tq, q_full, h * D + 64 * j, row0 + qt * TT);
+      int issued_k = 0, issued_v = 0;
       for (int kt = 0; kt < nk; ++kt) {
-        const int st = kt & 1;
-        if (kt < n_both) {  // Q of A before the first K tile, Q of B before the second
-          mbar_arrive_expect_tx(&q_full[kt], TB);
-          for (int j = 0; j < NA; ++j)
-            tma_load_2d(base + F_OFF_Q + kt * TILE_BYTES + j * ATOM, &p.tq, &q_full[kt], h * D + 64 * j,
-                        row0 + (pt.tile + kt) * TT);
-        }
-        if (kt >= 2 && !mbar_wait(&k_empty[st], ((kt >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 21)) break;
-        mbar_arrive_expect_tx(&k_full[st], TB);
+        if (kt > 0 && !mbar_wait(k_empty, (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 21)) break;
+        mbar_arrive_expect_tx(k_full, TB);
         for (int j = 0; j < NA; ++j)
-          tma_load_2d(base + F_OFF_K + st * TILE_BYTES + j * ATOM, &p.tk, &k_full[st], kvh * D + 64 * j, row0 + kt * TT);
-        if (kt >= 2 && !mbar_wait(&v_empty[st], ((kt >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 22)) {
-          mbar_wait_drain(&k_full[st], (kt >> 1) & 1);
-          break;
-        }
-        mbar_arrive_expect_tx(&v_full[st], TB);
+          tma_load_2d(base + F_OFF_K + j * ATOM, &p.tk, k_full, kvh * D + 64 * j, row0 + kt * TT);
+        issued_k = kt + 1;
+        if (kt > 0 && !mbar_wait(v_empty, (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 22)) break;
+        mbar_arrive_expect_tx(v_full, TB);
         for (int j = 0; j < NA; ++j)
-          tma_load_2d(base + F_OFF_V + st * TILE_BYTES + j * ATOM, &p.tv, &v_full[st], kvh * D + 64 * j, row0 + kt * TT);
-        issued = kt + 1;
+          tma_load_2d(base + F_OFF_V + j * ATOM, &p.tv, v_full, kvh * D + 64 * j, row0 + kt * TT);
+        issued_v = kt + 1;
       }
       if (*abort_flag) {  // let the copies already issued land before the CTA exits
-        for (int i = 0; i < min(n_both, issued); ++i) mbar_wait_drain(&q_full[i], 0);
-        for (int i = max(0, issued - 2); i < issued; ++i) {
-          mbar_wait_drain(&k_full[i & 1], (i >> 1) & 1);
-          mbar_wait_drain(&v_full[i & 1], (i >> 1) & 1);
-        }
+        mbar_wait_drain(q_full, 0);
+        if (issued_k > 0) mbar_wait_drain(k_full, (issued_k - 1) & 1);
+        if (issued_v > 0) mbar_wait_drain(v_full, (issued_v - 1) & 1);
       }
     }
   } else if (warp == F_MMA) {
@@ -211,111 +203,81 @@ __global__ void __launch_bounds__(F_THREADS, 1) k_packed_fwd(const __grid_consta
     constexpr uint32_t idesc_o = idesc_bf16(128, D, true);     // P V: V N-major
     const uint32_t sQ = smem_u32(base + F_OFF_Q), sK = smem_u32(base + F_OFF_K), sV = smem_u32(base + F_OFF_V);
     const uint32_t el = elect_lane();
-    // every wait is agreed on by the whole warp, so that no lane goes on alone
-    auto wait = [&](uint64_t* bar, int parity, int site) -> bool {
-      const bool ok = warp_wait(bar, parity & 1, abort_flag, p.err, KID_PACKED, site);
+    // every wait is agreed on by the whole warp , so that no lane goes on alone
+    bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag, p.err, KID_PACKED, 23));
+    for (int kt = 0; ok && kt < nk; ++kt) {
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(k_full, kt & 1, abort_flag, p.err, KID_PACKED, 24)))) break;
       tc_fence_after();
-      return ok;
-    };
-    auto scores = [&](int x, int kt) {
-      const uint32_t a = sQ + x * TILE_BYTES, b = sK + (kt & 1) * TILE_BYTES;
+      // tcgen05.mma of one thread run in issue order, so S may overwrite the P that the
+      // previous tile's P V product reads
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         const uint32_t off = (ks >> 2) * ATOM + (ks & 3) * 32;
-        umma_ss(el, tmem + x * 256, sdesc_sw128(a + off, 16, 1024), sdesc_sw128(b + off, 16, 1024), idesc_s, ks ? 1u : 0u);
+        umma_ss(el, tmem, sdesc_sw128(sQ + off, 16, 1024), sdesc_sw128(sK + off, 16, 1024), idesc_s, ks ? 1u : 0u);
       }
-      commit_by(el, &s_full[x]);
-    };
-    bool ok = wait(&q_full[0], 0, 23) && wait(&k_full[0], 0, 24);
-    if (ok) scores(0, 0);
-    if (ok && n_both == 2 && (ok = wait(&q_full[1], 0, 23))) scores(1, 0);
-    if (ok) commit_by(el, &k_empty[0]);
-    for (int kt = 0; ok && kt < nk; ++kt) {
-      if (!(ok = wait(&v_full[kt & 1], kt >> 1, 26))) break;
-      for (int x = 0; ok && x < n_both; ++x) {
-        const int n = x == 0 ? nk_a : nk;
-        if (kt >= n) continue;
-        if (kt + 1 < n && !(ok = wait(&k_full[(kt + 1) & 1], (kt + 1) >> 1, 24))) break;  // long there: not on P's way
+      commit_by(el, s_full);
+      commit_by(el, k_empty);
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(v_full, kt & 1, abort_flag, p.err, KID_PACKED, 26)))) break;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {  // the first half runs under the second half's exponentials
-          if (!(ok = wait(&p_half[2 * x + hf], kt, 25))) break;
+      for (int hf = 0; hf < 2; ++hf) {  // the first half runs under the second half's exponentials
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&p_half[hf], kt & 1, abort_flag, p.err, KID_PACKED, 25)))) break;
+        tc_fence_after();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // 16 keys per step: P columns 8 ks .., V rows 16 ks ..
-            const int ks = 4 * (j >> 1) + 2 * hf + (j & 1);
-            umma_ts(el, tmem + x * 256 + 128, tmem + x * 256 + ks * 8,
-                    sdesc_sw128(sV + (kt & 1) * TILE_BYTES + ks * 2048, ATOM, 1024), idesc_o, (kt | hf | j) ? 1u : 0u);
-          }
-        }
-        if (!ok) break;
-        commit_by(el, &o_full[x]);
-        // tcgen05.mma of one thread run in issue order, so S may overwrite the P that this
-        // tile's P V product reads
-        if (kt + 1 < n) scores(x, kt + 1);
+        for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)  // 16 keys per step: P columns 8 ks .., V rows 16 ks ..
+          umma_ts(el, tmem + 128, tmem + ks * 8, sdesc_sw128(sV + ks * 2048, ATOM, 1024), idesc_o, (kt | ks) ? 1u : 0u);
       }
       if (!ok) break;
-      if (kt + 1 < nk) commit_by(el, &k_empty[(kt + 1) & 1]);
-      commit_by(el, &v_empty[kt & 1]);
+      commit_by(el, v_empty);
+      commit_by(el, o_full);
     }
-  } else if (warp >= F_FIRST && warp < F_FIRST + 8 * n_both) {
+  } else {
     // ------------------------------------------------------------------ softmax + epilogue
-    const int w = warp - F_FIRST, t = w >> 3, wq = w & 3, g = (w >> 2) & 1;  // tile, lane quarter, key half
-    const int r = wq * 32 + lane;  // query row in the tile = TMEM lane
-    const int qt = pt.tile + t;
-    const int n_rows = min(TT, pt.len - qt * TT);
-    const uint32_t trow = tmem + t * 256 + ((uint32_t)(wq * 32) << 16);
+    const int r = warp * 32 + lane;  // query row in the tile = TMEM lane
+    const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
     const float sl = p.scale_log2;
-    float* xch = reinterpret_cast<float*>(base + F_OFF_X) + t * 512;
-    // the two warps of the same rows meet here, each having loaded its scores
-    auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(2 + t * 4 + wq) : "memory"); };
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
-    for (int kt = 0; kt <= qt; ++kt) {
-      // a failed wait does not leave the loop here: the other warp of the pair would wait at
-      // the meeting for good
-      ok = warp_wait(&s_full[t], kt & 1, abort_flag, p.err, KID_PACKED, 27) && ok;
+    for (int kt = 0; kt < nk; ++kt) {
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full, kt & 1, abort_flag, p.err, KID_PACKED, 27)))) break;
       tc_fence_after();
       const bool diag = kt == qt;
-      // this half of the row of scores; masked ones (on the diagonal tile, which is also the
-      // only one that the sequence may end in) become -inf whatever they were
-      uint32_t v[2][32];
-      tmem_ld32(trow + g * 64, v[0]);
-      tmem_ld32(trow + g * 64 + 32, v[1]);
+      // the row of scores, held in registers; masked ones (on the diagonal tile, which is
+      // also the only one that the sequence may end in) become -inf whatever they were
+      uint32_t v[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(trow + c * 32, v[c]);
       tmem_wait_ld();
       if (diag) {
-        const int last = r - g * 64;
 #pragma unroll
-        for (int c = 0; c < 64; ++c) v[c / 32][c % 32] = c <= last ? v[c / 32][c % 32] : 0xFF800000u;
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[c][i] = c * 32 + i <= r ? v[c][i] : 0xFF800000u;
       }
       float m4[4];  // independent chains
 #pragma unroll
       for (int e = 0; e < 4; ++e) m4[e] = fmaxf(__uint_as_float(v[0][e]), __uint_as_float(v[0][4 + e]));
 #pragma unroll
-      for (int i = 8; i < 64; i += 8)
+      for (int i = 8; i < 128; i += 8)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           m4[e] = fmaxf(fmaxf(m4[e], __uint_as_float(v[i / 32][i % 32 + e])), __uint_as_float(v[i / 32][i % 32 + 4 + e]));
       float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      float* x = xch + (kt & 1) * 256;
-      x[g * 128 + r] = mx;
-      tc_fence_before();
-      meet();
-      tc_fence_after();
-      mx = fmaxf(mx, x[(g ^ 1) * 128 + r]) * sl;
+      mx *= sl;
       const float m_new = (kt == 0 || mx > m_run + kRescaleLog2) ? fmaxf(mx, m_run) : m_run;
       const bool resc = kt > 0 && m_new != m_run;
       if (__any_sync(0xffffffffu, resc)) {
         // the previous tile's P V product must be in O before O is scaled
-        ok = warp_wait(&o_full[t], (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 28) && ok;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(o_full, (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 28)))) break;
         tc_fence_after();
         const float alpha = resc ? fast_exp2(m_run - m_new) : 1.0f;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {  // this warp's half of the dims, 16 at a time
+        for (int c = 0; c < D / 16; ++c) {  // 16 columns at a time: the scores hold the registers
           uint32_t o[16];
-          tmem_ld16(trow + 128 + g * (D / 2) + c * 16, o);
+          tmem_ld16(trow + 128 + c * 16, o);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          tmem_st16(trow + 128 + g * (D / 2) + c * 16, o);
+          tmem_st16(trow + 128 + c * 16, o);
         }
         tmem_wait_st();
         l_run *= alpha;
@@ -324,59 +286,57 @@ __global__ void __launch_bounds__(F_THREADS, 1) k_packed_fwd(const __grid_consta
       if (diag && n_rows < TT) {
         // rows of V behind the sequence's end belong to others: zeros, so that a
         // non-finite value there times a probability of 0 stays out of O
-        ok = warp_wait(&v_full[kt & 1], (kt >> 1) & 1, abort_flag, p.err, KID_PACKED, 30) && ok;
-        if (r >= n_rows && g == 0) zero_row<NA>(smem_u32(base + F_OFF_V + (kt & 1) * TILE_BYTES), r);
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(v_full, kt & 1, abort_flag, p.err, KID_PACKED, 30)))) break;
+        if (r >= n_rows) zero_row<NA>(smem_u32(base + F_OFF_V), r);
         fence_proxy_async_smem();
       }
       const uint64_t sl2 = pack2(sl, sl), nm2 = pack2(-m_run, -m_run);
       uint64_t acc[2] = {0, 0};
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        uint32_t pk[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const uint64_t y = fma2(pack2(v[hf][2 * j], v[hf][2 * j + 1]), sl2, nm2);
-          const float e0 = fast_exp2(lo2(y)), e1 = fast_exp2(hi2(y));
-          acc[j & 1] = add2(acc[j & 1], pack2(e0, e1));
-          pk[j] = pack_bf16x2(e0, e1);
+        for (int c = 2 * hf; c < 2 * hf + 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint64_t x = fma2(pack2(v[c][2 * j], v[c][2 * j + 1]), sl2, nm2);
+            const float e0 = fast_exp2(lo2(x)), e1 = fast_exp2(hi2(x));
+            acc[j & 1] = add2(acc[j & 1], pack2(e0, e1));
+            pk[j] = pack_bf16x2(e0, e1);
+          }
+          tmem_st16(trow + c * 16, pk);  // over scores that this warp has read
         }
-        tmem_st16(trow + g * 32 + hf * 16, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_half[2 * t + hf]);
+        if (lane == 0) mbar_arrive(&p_half[hf]);
         __syncwarp();
       }
       acc[0] = add2(acc[0], acc[1]);
       l_run += lo2(acc[0]) + hi2(acc[0]);
-      if (*abort_flag) ok = false;
     }
-    // O / sum through the freed Q tile's shared memory and TMA stores (coalesced rows); all
-    // eight warps reach the barriers, the store is issued only when no wait failed
-    ok = warp_wait(&o_full[t], qt & 1, abort_flag, p.err, KID_PACKED, 29) && ok;
-    float* x = xch + ((qt + 1) & 1) * 256;
-    x[g * 128 + r] = l_run;
-    meet();
-    l_run += x[(g ^ 1) * 128 + r];
-    if (ok) {
+    // O / sum through the freed Q tile's shared memory and two TMA stores (coalesced rows);
+    // all four warps reach the barrier, the store is issued only when no wait failed
+    if (ok && __all_sync(0xffffffffu, mbar_wait(o_full, (nk - 1) & 1, abort_flag, p.err, KID_PACKED, 29))) {
       tc_fence_after();
       const float inv = 1.0f / l_run;
-      const uint32_t tile = smem_u32(base + F_OFF_Q + t * TILE_BYTES);
+      const uint32_t tile = smem_u32(base + F_OFF_Q);
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t v[32];
-        tmem_ld32(trow + 128 + g * (D / 2) + c * 32, v);
+      for (int c = 0; c < D / 32; c += 2) {
+        uint32_t v[2][32];
+        tmem_ld32(trow + 128 + c * 32, v[0]);
+        tmem_ld32(trow + 128 + c * 32 + 32, v[1]);
         tmem_wait_ld();
-        stage_row32(tile, r, g * (D / 64) + c, v, inv);
+        stage_row32(tile, r, c, v[0], inv);
+        stage_row32(tile, r, c + 1, v[1], inv);
       }
-      if (r < n_rows && g == 0)
+      if (r < n_rows)
         p.lse[(size_t)h * p.total + row0 + qt * TT + r] = (m_run + log2f(l_run)) * 0.6931471805599453f;
     }
     fence_proxy_async_smem();
-    asm volatile("bar.sync %0, %1;" ::"r"(10 + t), "n"(F_SM) : "memory");
+    asm volatile("bar.sync 1, 128;" ::: "memory");
     if (!*abort_flag)
-      store_tile<D>(&p.to, p.o, p.ldo, smem_u32(base + F_OFF_Q + t * TILE_BYTES), row0 + qt * TT, h * D, n_rows,
-                    threadIdx.x - F_FIRST * 32 - t * F_SM, F_SM);
+      store_tile<D>(&p.to, p.o, p.ldo, smem_u32(base + F_OFF_Q), row0 + qt * TT, h * D, n_rows, threadIdx.x, 128);
   }
 
   // On an aborted run the products already issued must finish before TMEM is freed.
@@ -389,7 +349,7 @@ __global__ void __launch_bounds__(F_THREADS, 1) k_packed_fwd(const __grid_consta
   __syncthreads();
   if (warp == F_MMA) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 256);
   }
 }
 
@@ -1094,10 +1054,10 @@ int allow_smem(K kernel, int bytes, int (&configured)[64]) {
 }
 
 template <int D>
-int launch_fwd(const FwdParams& p, int n_pairs, cudaStream_t s) {
+int launch_fwd(const FwdParams& p, int n_tiles, cudaStream_t s) {
   static int configured[64] = {0};
   NF4_TRY(allow_smem(k_packed_fwd<D>, SMEM_TC, configured));
-  k_packed_fwd<D><<<(unsigned)n_pairs * p.nq, F_THREADS, SMEM_TC, s>>>(p);
+  k_packed_fwd<D><<<(unsigned)n_tiles * p.nq, F_THREADS, SMEM_TC, s>>>(p);
   note_launch();
   NF4_CUDA_TRY(cudaGetLastError());
   return NF4LS_OK;
@@ -1178,7 +1138,7 @@ extern "C" int nf4ls_packed_attention_fwd(const nf4ls_pack* pack, const nf4ls_pa
   NF4_TRY(tile_map(&p.tk, t->k, kvd, pack->total, t->ld_k));
   NF4_TRY(tile_map(&p.tv, t->v, kvd, pack->total, t->ld_v));
   NF4_TRY(tile_map(&p.to, t->o, qd, pack->total, t->ld_o));
-  p.tiles = tile_list(pack, pack->off_query_pairs);
+  p.tiles = tile_list(pack, pack->off_query_tiles);
   p.o = static_cast<__nv_bfloat16*>(t->o);
   p.lse = t->lse;
   p.ldo = t->ld_o;
@@ -1188,7 +1148,7 @@ extern "C" int nf4ls_packed_attention_fwd(const nf4ls_pack* pack, const nf4ls_pa
   p.scale_log2 = heads->scale * 1.4426950408889634f;
   p.err = device_error_ptr();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return d == 64 ? launch_fwd<64>(p, pack->n_pairs, s) : launch_fwd<128>(p, pack->n_pairs, s);
+  return d == 64 ? launch_fwd<64>(p, pack->n_tiles, s) : launch_fwd<128>(p, pack->n_tiles, s);
 }
 
 extern "C" int nf4ls_packed_attention_bwd(const nf4ls_pack* pack, const nf4ls_packed_heads* heads,

@@ -13,8 +13,8 @@ namespace nf4ls {
 
 int check_pack(const nf4ls_pack* p, const char* who) {
   if (!p) return fail(NF4LS_INVALID_ARG, "%s: null pack", who);
-  if (p->n_seqs < 1 || p->total < 0 || p->n_tiles < 0 || p->max_len < 0 || p->n_tiles > p->total || p->n_pairs < 0 ||
-      p->n_pairs > p->n_tiles || (p->total > 0) != (p->n_tiles > 0) || (p->total > 0) != (p->n_pairs > 0))
+  if (p->n_seqs < 1 || p->total < 0 || p->n_tiles < 0 || p->max_len < 0 || p->n_tiles > p->total ||
+      (p->total > 0) != (p->n_tiles > 0))
     return fail(NF4LS_INVALID_ARG, "%s: not a pack that nf4ls_pack_layout filled", who);
   if (!p->plan_dev) return fail(NF4LS_INVALID_ARG, "%s: the pack has no plan on the device", who);
   if (!aligned(p->plan_dev, 256)) return fail(NF4LS_ALIGN, "%s: the plan must be 256-byte aligned", who);
@@ -30,7 +30,7 @@ extern "C" int nf4ls_pack_layout(const int32_t* lengths_host, int32_t n_seqs, nf
   if (!lengths_host || !out) return fail(NF4LS_INVALID_ARG, "nf4ls_pack_layout: null argument");
   if (n_seqs < 1 || n_seqs > NF4LS_PACK_MAX_SEQS)
     return fail(NF4LS_INVALID_ARG, "nf4ls_pack_layout: %d sequences, 1 to %d are supported", n_seqs, NF4LS_PACK_MAX_SEQS);
-  int64_t total = 0, tiles = 0, pairs = 0;
+  int64_t total = 0, tiles = 0;
   int32_t longest = 0;
   for (int32_t i = 0; i < n_seqs; ++i) {
     if (lengths_host[i] < 0) return fail(NF4LS_INVALID_ARG, "nf4ls_pack_layout: sequence %d has length %d", i, lengths_host[i]);
@@ -38,14 +38,12 @@ extern "C" int nf4ls_pack_layout(const int32_t* lengths_host, int32_t n_seqs, nf
     if (total > NF4LS_PACK_MAX_ROWS)
       return fail(NF4LS_INVALID_ARG, "nf4ls_pack_layout: more than %d rows", NF4LS_PACK_MAX_ROWS);
     tiles += (lengths_host[i] + 127) / 128;
-    pairs += (lengths_host[i] + 255) / 256;
     longest = std::max(longest, lengths_host[i]);
   }
   std::memset(out, 0, sizeof(*out));
   out->n_seqs = n_seqs;
   out->total = (int32_t)total;
   out->n_tiles = (int32_t)tiles;
-  out->n_pairs = (int32_t)pairs;
   out->max_len = longest;
   uint64_t off = 0;
   auto take = [&](uint64_t bytes) {
@@ -58,7 +56,6 @@ extern "C" int nf4ls_pack_layout(const int32_t* lengths_host, int32_t n_seqs, nf
   out->off_seq = take(4ull * total);
   out->off_query_tiles = take(16ull * tiles);
   out->off_key_tiles = take(16ull * tiles);
-  out->off_query_pairs = take(16ull * pairs);
   out->plan_bytes = off;
   return NF4LS_OK;
 }
@@ -68,7 +65,7 @@ extern "C" int nf4ls_pack_fill(const int32_t* lengths_host, const nf4ls_pack* pa
   if (!lengths_host || !pack || !plan_host) return fail(NF4LS_INVALID_ARG, "nf4ls_pack_fill: null argument");
   nf4ls_pack want;
   NF4_TRY(nf4ls_pack_layout(lengths_host, pack->n_seqs, &want));
-  if (want.total != pack->total || want.n_tiles != pack->n_tiles || want.n_pairs != pack->n_pairs || want.plan_bytes != pack->plan_bytes)
+  if (want.total != pack->total || want.n_tiles != pack->n_tiles || want.plan_bytes != pack->plan_bytes)
     return fail(NF4LS_INVALID_ARG, "nf4ls_pack_fill: the lengths are not those of the pack");
   if (bytes < want.plan_bytes)
     return fail(NF4LS_INVALID_ARG, "nf4ls_pack_fill: %zu bytes, the plan needs %llu", bytes,
@@ -100,14 +97,6 @@ extern "C" int nf4ls_pack_fill(const int32_t* lengths_host, const nf4ls_pack* pa
     auto left = [](const PackTile& a) { return (a.len + 127) / 128 - a.tile; };
     std::stable_sort(tiles.begin(), tiles.end(), [&](const PackTile& a, const PackTile& b) { return left(a) > left(b); });
     if (!tiles.empty()) std::memcpy(base + want.off_key_tiles, tiles.data(), tiles.size() * sizeof(PackTile));
-    // Every second tile with the one behind it (if there is one) on its way: the forward's
-    // two tiles of a block.
-    std::vector<PackTile> pairs;
-    for (const PackTile& t : tiles)
-      if (t.tile % 2 == 0) pairs.push_back(t);
-    auto work = [](const PackTile& a) { return a.len > (a.tile + 1) * 128 ? 2 * a.tile + 3 : a.tile + 1; };
-    std::stable_sort(pairs.begin(), pairs.end(), [&](const PackTile& a, const PackTile& b) { return work(a) > work(b); });
-    if (!pairs.empty()) std::memcpy(base + want.off_query_pairs, pairs.data(), pairs.size() * sizeof(PackTile));
   } catch (const std::bad_alloc&) {
     return fail(NF4LS_INVALID_ARG, "nf4ls_pack_fill: out of host memory");
   }
