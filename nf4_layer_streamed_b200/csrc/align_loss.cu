@@ -33,13 +33,10 @@ struct Stat {
   float m, s;
 };
 __device__ __forceinline__ float safe_ref(float m) { return m == -INFINITY ? 0.0f : m; }
-__device__ __forceinline__ Stat merge(Stat a, Stat b) {
-  const float m = fmaxf(a.m, b.m), ref = safe_ref(m);
-  return {m, a.s * exp2_fast((a.m - ref) * kLog2e) + b.s * exp2_fast((b.m - ref) * kLog2e)};
-}
-
 // The difference to the maximum is taken before the scaling by log2(e): a row whose values
-// are all the type's lowest would overflow the other way round.
+// are all the type's lowest would overflow the other way round.  The exponential unit's
+// values are too small by 5e-8 of themselves on average, which a mean over rows keeps: sums
+// are rescaled by expf instead (on average within 1e-8), and only once behind the loop.
 __device__ __forceinline__ void add8(Stat& st, const uint4& u) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   float x[8];
@@ -50,7 +47,7 @@ __device__ __forceinline__ void add8(Stat& st, const uint4& u) {
   }
   const float cm = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
   if (cm > st.m) {
-    st.s *= exp2_fast((st.m - cm) * kLog2e);
+    st.s *= expf(st.m - cm);
     st.m = cm;
   }
   const float ref = safe_ref(st.m);
@@ -61,7 +58,7 @@ __device__ __forceinline__ void add8(Stat& st, const uint4& u) {
 }
 __device__ __forceinline__ void add1(Stat& st, float x) {
   if (x > st.m) {
-    st.s *= exp2_fast((st.m - x) * kLog2e);
+    st.s *= expf(st.m - x);
     st.m = x;
   }
   st.s += exp2_fast((x - safe_ref(st.m)) * kLog2e);
@@ -80,7 +77,7 @@ struct RowSplit {
 
 // Statistics of a row by the whole block (fixed order: reruns give the same bits).
 __device__ __forceinline__ Stat block_stats(const __nv_bfloat16* row, int V) {
-  __shared__ Stat red[LT / 32];
+  __shared__ float red_m[LT / 32], red_s[LT / 32];
   const int t = threadIdx.x;
   const RowSplit sp(row, V);
   Stat st = {-INFINITY, 0.0f};
@@ -96,14 +93,24 @@ __device__ __forceinline__ Stat block_stats(const __nv_bfloat16* row, int V) {
   }
   for (; j < sp.n16; j += LT) add8(st, v[j]);
   if (sp.tail0 + t < V) add1(st, __bfloat162float(row[sp.tail0 + t]));
+  // the row's maximum first, so that a thread's sum is scaled to it once
+  float m = st.m;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    st = merge(st, {__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o)});
-  if ((t & 31) == 0) red[t >> 5] = st;
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((t & 31) == 0) red_m[t >> 5] = m;
   __syncthreads();
-  st = red[0];
-  for (int i = 1; i < LT / 32; ++i) st = merge(st, red[i]);
-  return st;
+  m = red_m[0];
+#pragma unroll
+  for (int i = 1; i < LT / 32; ++i) m = fmaxf(m, red_m[i]);
+  float s = st.s * expf(st.m - safe_ref(m));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((t & 31) == 0) red_s[t >> 5] = s;
+  __syncthreads();
+  s = red_s[0];
+#pragma unroll
+  for (int i = 1; i < LT / 32; ++i) s += red_s[i];
+  return {m, s};
 }
 
 // out = coef (onehot(target) - exp(x - m) / s) for the row; in may be out.
