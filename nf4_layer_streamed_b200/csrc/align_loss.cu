@@ -168,10 +168,6 @@ __device__ __forceinline__ double target_logp(float xt, Stat st) {
   return (double)xt - (double)st.m - log((double)st.s);
 }
 
-// The next launch of the stream may begin (it waits before it reads anything), and the wait.
-__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // A block per row.  (Clusters that share a row measured 140 us for 2048 rows of 128 k logits,
 // this 73: small independent blocks, four to an SM, hide the reductions' waits best.)
 __global__ void __launch_bounds__(LT) k_token_logp(const __nv_bfloat16* __restrict__ logits, int64_t ld, int V,
@@ -348,20 +344,9 @@ __global__ void __launch_bounds__(PT) k_sum_rows(const float* __restrict__ v, in
   }
 }
 
-// A launch; early: it may begin while the one before it still runs (its kernel waits itself).
 template <typename... P, typename... A>
 int launch(void (*k)(P...), int64_t blocks, int threads, bool early, cudaStream_t s, A... args) {
-  cudaLaunchAttribute at[1];
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.stream = s;
-  cfg.attrs = at;
-  if (early) {
-    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  NF4_CUDA_TRY(cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...));
+  NF4_CUDA_TRY(launch_kernel(k, blocks, threads, 0, early, s, args...));
   note_launch();
   return NF4LS_OK;
 }

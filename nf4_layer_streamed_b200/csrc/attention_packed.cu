@@ -414,6 +414,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM;  // swizzle atoms, k-steps and bytes of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base;
+  next_may_start();  // the key side's blocks, on the SMs that the last of these leave free
   if (!smem_base(smem_raw, &base, p.err)) return;
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + B_OFF_BAR);
   uint64_t* q_full = bars;          // Q, dO
@@ -797,6 +798,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
           tma_load_2d(base + B_OFF_R3 + s3 * TILE_BYTES + j * ATOM, &p.tq, &q_full[s3], h * D + 64 * j, row0 + qt * TT);
         issued_q = i + 1;
         if (i >= 2 && !mbar_wait(&do_empty[s2], ((i >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 32)) break;
+        if (i == 0) wait_for_previous();  // the query side's statistics
         mbar_arrive_expect_tx(&do_full[s2], TB + 1024);
         for (int j = 0; j < NA; ++j)
           tma_load_2d(base + B_OFF_R2 + s2 * TILE_BYTES + j * ATOM, &p.tdo, &do_full[s2], h * D + 64 * j, row0 + qt * TT);
@@ -804,6 +806,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
                   &do_full[s2]);
         issued_do = i + 1;
       }
+      if (n_st == 0) wait_for_previous();  // no block ends before the query side has
       if (*abort_flag) {  // let the copies already issued land before the CTA exits
         mbar_wait_drain(kv_full, 0);
         for (int i = max(0, issued_q - 3); i < issued_q; ++i) mbar_wait_drain(&q_full[i % 3], (i / 3) & 1);
@@ -1074,9 +1077,8 @@ int launch_bwd(BwdParams& p, const PackTile* query_tiles, const PackTile* key_ti
   note_launch();
   NF4_CUDA_TRY(cudaGetLastError());
   p.tiles = key_tiles;
-  k_packed_dkv<D><<<(unsigned)p.n_tiles * p.nkv * 2, B_THREADS, SMEM_BWD, s>>>(p);
+  NF4_CUDA_TRY(launch_kernel(k_packed_dkv<D>, (int64_t)p.n_tiles * p.nkv * 2, B_THREADS, SMEM_BWD, true, s, p));
   note_launch();
-  NF4_CUDA_TRY(cudaGetLastError());
   return NF4LS_OK;
 }
 

@@ -381,4 +381,26 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
       : "memory");
 }
 
+// The next launch of the stream may begin (it waits before it reads anything), and the wait.
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A launch; early: it may begin while the one before it still runs (its kernel waits itself).
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*k)(P...), int64_t blocks, int threads, size_t smem, bool early, cudaStream_t s,
+                          A... args) {
+  cudaLaunchAttribute at[1];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  if (early) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...);
+}
+
 }  // namespace nf4ls
