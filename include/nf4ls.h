@@ -590,6 +590,7 @@ int nf4ls_attention_bwd(const nf4ls_layer_cfg* cfg, const void* q_dev, const voi
 
 typedef struct {
     int32_t n_seqs, total, n_tiles, max_len;
+    int64_t n_blocks; /* pairs of a query tile and a key tile at or before it */
     uint64_t off_cu, off_positions, off_seq, off_query_tiles, off_key_tiles, plan_bytes;
     const void* plan_dev;
 } nf4ls_pack;

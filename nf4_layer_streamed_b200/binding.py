@@ -76,7 +76,7 @@ class DiskInfo(ctypes.Structure):
 
 class Pack(ctypes.Structure):
     _fields_ = [("n_seqs", ctypes.c_int32), ("total", ctypes.c_int32), ("n_tiles", ctypes.c_int32),
-                ("max_len", ctypes.c_int32),
+                ("max_len", ctypes.c_int32), ("n_blocks", ctypes.c_int64),
                 ("off_cu", ctypes.c_uint64), ("off_positions", ctypes.c_uint64),
                 ("off_seq", ctypes.c_uint64), ("off_query_tiles", ctypes.c_uint64),
                 ("off_key_tiles", ctypes.c_uint64), ("plan_bytes", ctypes.c_uint64),

@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(PT) k_sum_rows(const float* __restrict__ v, in
 
 template <typename... P, typename... A>
 int launch(void (*k)(P...), int64_t blocks, int threads, bool early, cudaStream_t s, A... args) {
-  NF4_CUDA_TRY(launch_kernel(k, blocks, threads, 0, early, s, args...));
+  NF4_CUDA_TRY(launch_kernel(k, blocks, {threads, 0, early, 1}, s, args...));
   note_launch();
   return NF4LS_OK;
 }

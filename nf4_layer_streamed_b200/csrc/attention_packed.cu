@@ -1,5 +1,6 @@
 // Causal grouped-query attention over a packed batch (forward and gradients) on the
 // 5th-generation tensor cores: the sequences lie one behind the other and have any length.
+#include <algorithm>
 #include <cstring>
 #include <type_traits>
 
@@ -702,14 +703,13 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   }
 }
 
-// KEY side: dK, dV of one key tile of one kv head, by a cluster of two CTAs that split the
-// group's query heads (the first ceil(group / 2) heads and the rest).  Each CTA then
+// KEY side: dK, dV of one key tile of one kv head, by one CTA or (SPLIT) by a cluster of two
+// that split the group's query heads (the first ceil(group / 2) heads and the rest).  Each then
 // finishes one of the two tensors: it stages the other tensor's fp32 partial sums in its own
 // shared memory and sends them in one bulk copy into the peer's, and adds the peer's to its
 // own in the order first CTA + second CTA.
-template <int D>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
-    k_packed_dkv(const __grid_constant__ BwdParams p) {
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(B_THREADS, 1) k_packed_dkv(const __grid_constant__ BwdParams p) {
   constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base;
@@ -731,14 +731,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = warp_number(), lane = threadIdx.x & 31;
-  const int item = blockIdx.x >> 1, kvh = item % p.nkv;
+  const int item = SPLIT ? blockIdx.x >> 1 : blockIdx.x, kvh = item % p.nkv;
   const PackTile pt = p.tiles[item / p.nkv];
   const int kt = pt.tile, row0 = pt.row0;
   const int n_keys = min(TT, pt.len - kt * TT);
-  const uint32_t crank = cluster_ctarank();
+  const uint32_t crank = SPLIT ? cluster_ctarank() : 0;
   const int grp = p.nq / p.nkv, n_qt = (pt.len + TT - 1) / TT;
   const int n_last = pt.len - (n_qt - 1) * TT;  // rows of the sequence's last query tile
-  const int hpc = (grp + 1) / 2, h_begin = (int)crank * hpc, h_count = min(grp, h_begin + hpc) - h_begin;
+  const int hpc = SPLIT ? (grp + 1) / 2 : grp, h_begin = (int)crank * hpc, h_count = min(grp, h_begin + hpc) - h_begin;
   // (head, query tile) items of this CTA
   const int per_head = n_qt - kt, n_st = h_count * per_head;
 
@@ -965,69 +965,88 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(B_THREADS, 1)
     }
     const bool have = n_st > 0 && ok && warp_wait(acc_full, 0, abort_flag, p.err, KID_PACKED, 63);
     if (have) tc_fence_after();
-    // The partial sums cross over: the first CTA finishes dV and the second dK, so each sends
-    // the other tensor (fp32 rows of D floats, 16-byte chunks swizzled by row) from the start
-    // of its freed rings into the space behind it in the peer's.
-    constexpr uint32_t PB = 128u * D * 4u;  // one tensor's partial sums
-    static_assert(2 * PB <= 5u * TILE_BYTES, "the rings hold both sides of the exchange");
-    const uint32_t ring = smem_u32(base + B_OFF_R3);
-    const uint32_t t_send = trow + (crank == 0 ? T_DK : T_DV), t_keep = trow + (crank == 0 ? T_DV : T_DK);
-    const uint32_t prow = (uint32_t)r * (D * 4);
     const bool has_dims = g < D / 32;  // dims 32 g ..
-    if (has_dims) {
-      uint32_t v[32];
-      if (have) {
-        tmem_ld32(t_send + g * 32, v);
-        tmem_wait_ld();
-      }
-#pragma unroll
-      for (int q4 = 0; q4 < 8; ++q4) {
-        const uint32_t o = ring + prow + ((uint32_t)((g * 8 + q4) ^ (r & 7)) << 4);
-        if (have)
-          st_shared_v4(o, v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
-        else
-          st_shared_v4(o, 0u, 0u, 0u, 0u);
-      }
-    }
-    fence_proxy_async_smem();
-    if (tid == 0) mbar_arrive_expect_tx(peer_full, PB);
-    bar_ew();
-    // both CTAs have finished their products: both rings are free
-    cluster_sync_all();
-    if (tid == 0) {
-      const uint32_t other = crank ^ 1u;
-      bulk_copy_to_peer(mapa_shared(ring + PB, other), ring, PB, mapa_shared(smem_u32(peer_full), other));
-    }
-    (void)warp_wait(peer_full, 0, abort_flag, p.err, KID_PACKED, 64);
-    // this CTA's tensor (its sums plus the peer's) through the freed K tile's shared memory
-    // and TMA stores; dK takes the softmax scale
     const uint32_t tile = smem_u32(base + B_OFF_A);
-    const float sc = crank == 0 ? 1.0f : p.scale;
-    if (has_dims) {
-      float v[32];
-      uint32_t vr[32];
-      if (have) {
-        tmem_ld32(t_keep + g * 32, vr);
+    if constexpr (!SPLIT) {
+      // through the freed K and V tiles' shared memory and TMA stores; dK takes the softmax scale
+      if (have && has_dims) {
+        uint32_t v[32];
+        tmem_ld32(trow + T_DV + g * 32, v);
         tmem_wait_ld();
+        stage_row32(tile, r, g, v, 1.0f);
+        tmem_ld32(trow + T_DK + g * 32, v);
+        tmem_wait_ld();
+        stage_row32(tile + TILE_BYTES, r, g, v, p.scale);
       }
-#pragma unroll
-      for (int q4 = 0; q4 < 8; ++q4) {
-        const uint4 in = ld_shared_v4(ring + PB + prow + ((uint32_t)((g * 8 + q4) ^ (r & 7)) << 4));
-        const float iv[4] = {__uint_as_float(in.x), __uint_as_float(in.y), __uint_as_float(in.z), __uint_as_float(in.w)};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * q4 + e] = ((have ? __uint_as_float(vr[4 * q4 + e]) : 0.f) + iv[e]) * sc;
+      fence_proxy_async_smem();
+      bar_ew();
+      if (!*abort_flag) {  // the whole tiles' stores by one thread each
+        store_tile<D>(&p.tdv, p.dv, p.ld_dv, tile, row0 + kt * TT, kvh * D, n_keys, tid, B_EW);
+        store_tile<D>(&p.tdk, p.dk, p.ld_dk, tile + TILE_BYTES, row0 + kt * TT, kvh * D, n_keys, (tid + 32) % B_EW, B_EW);
       }
-      stage_row32(tile, r, g, v);
+    } else {
+      // The partial sums cross over: the first CTA finishes dV and the second dK, so each sends
+      // the other tensor (fp32 rows of D floats, 16-byte chunks swizzled by row) from the start
+      // of its freed rings into the space behind it in the peer's.
+      constexpr uint32_t PB = 128u * D * 4u;  // one tensor's partial sums
+      static_assert(2 * PB <= 5u * TILE_BYTES, "the rings hold both sides of the exchange");
+      const uint32_t ring = smem_u32(base + B_OFF_R3);
+      const uint32_t t_send = trow + (crank == 0 ? T_DK : T_DV), t_keep = trow + (crank == 0 ? T_DV : T_DK);
+      const uint32_t prow = (uint32_t)r * (D * 4);
+      if (has_dims) {
+        uint32_t v[32];
+        if (have) {
+          tmem_ld32(t_send + g * 32, v);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int q4 = 0; q4 < 8; ++q4) {
+          const uint32_t o = ring + prow + ((uint32_t)((g * 8 + q4) ^ (r & 7)) << 4);
+          if (have)
+            st_shared_v4(o, v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
+          else
+            st_shared_v4(o, 0u, 0u, 0u, 0u);
+        }
+      }
+      fence_proxy_async_smem();
+      if (tid == 0) mbar_arrive_expect_tx(peer_full, PB);
+      bar_ew();
+      // both CTAs have finished their products: both rings are free
+      cluster_sync_all();
+      if (tid == 0) {
+        const uint32_t other = crank ^ 1u;
+        bulk_copy_to_peer(mapa_shared(ring + PB, other), ring, PB, mapa_shared(smem_u32(peer_full), other));
+      }
+      (void)warp_wait(peer_full, 0, abort_flag, p.err, KID_PACKED, 64);
+      // this CTA's tensor (its sums plus the peer's) through the freed K tile's shared memory
+      // and TMA stores; dK takes the softmax scale
+      const float sc = crank == 0 ? 1.0f : p.scale;
+      if (has_dims) {
+        float v[32];
+        uint32_t vr[32];
+        if (have) {
+          tmem_ld32(t_keep + g * 32, vr);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int q4 = 0; q4 < 8; ++q4) {
+          const uint4 in = ld_shared_v4(ring + PB + prow + ((uint32_t)((g * 8 + q4) ^ (r & 7)) << 4));
+          const float iv[4] = {__uint_as_float(in.x), __uint_as_float(in.y), __uint_as_float(in.z), __uint_as_float(in.w)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * q4 + e] = ((have ? __uint_as_float(vr[4 * q4 + e]) : 0.f) + iv[e]) * sc;
+        }
+        stage_row32(tile, r, g, v);
+      }
+      fence_proxy_async_smem();
+      bar_ew();
+      if (!*abort_flag)
+        store_tile<D>(crank == 0 ? &p.tdv : &p.tdk, crank == 0 ? p.dv : p.dk, crank == 0 ? p.ld_dv : p.ld_dk, tile,
+                      row0 + kt * TT, kvh * D, n_keys, tid, B_EW);
+      // the peer has its copy of this CTA's partial sums before this shared memory goes
+      cluster_sync_all();
     }
-    fence_proxy_async_smem();
-    bar_ew();
-    if (!*abort_flag)
-      store_tile<D>(crank == 0 ? &p.tdv : &p.tdk, crank == 0 ? p.dv : p.dk, crank == 0 ? p.ld_dv : p.ld_dk, tile,
-                    row0 + kt * TT, kvh * D, n_keys, tid, B_EW);
-    // the peer has its copy of this CTA's partial sums before this shared memory goes
-    cluster_sync_all();
   }
-  if (warp < B_FIRST) {  // the other warps join the two cluster barriers too
+  if (SPLIT && warp < B_FIRST) {  // the other warps join the two cluster barriers too
     __syncwarp();
     cluster_sync_all();
     cluster_sync_all();
@@ -1066,18 +1085,44 @@ int launch_fwd(const FwdParams& p, int n_tiles, cudaStream_t s) {
   return NF4LS_OK;
 }
 
+// Two CTAs for a key tile, or one?  Halves of an item (2.7 k cycles): a CTA takes 2 each and 5
+// of its own, or 8 with the exchange of a pair.  All at once the longest counts; else the sum
+// over the SMs, with half a CTA left over at the end.  8 kv heads of 4 query heads, one CTA
+// against two: 2048 rows in one sequence 152 and 118 us, in four 63 and 66, in eight 48 and
+// 56; one of 512 rows 38 and 29.
+bool split_heads(const nf4ls_pack* pack, int nkv, int group, int sms) {
+  if (group == 1) return false;
+  auto halves = [&](int heads, int64_t ctas, int own) -> int64_t {
+    const int64_t longest = 2ll * heads * ((pack->max_len + TT - 1) / TT) + own;
+    if (ctas <= sms) return longest;
+    const int64_t sum = 2 * pack->n_blocks * nkv * group + ctas * own;
+    return std::max(longest, sum / sms + sum / ctas / 2);
+  };
+  const int64_t tiles = (int64_t)pack->n_tiles * nkv;
+  return halves((group + 1) / 2, 2 * tiles, 8) < halves(group, tiles, 5);
+}
+
 template <int D>
-int launch_bwd(BwdParams& p, const PackTile* query_tiles, const PackTile* key_tiles, cudaStream_t s) {
-  static int conf_q[64] = {0}, conf_k[64] = {0};
+int launch_bwd(BwdParams& p, const nf4ls_pack* pack, const PackTile* query_tiles, const PackTile* key_tiles, cudaStream_t s) {
+  static int conf_q[64] = {0}, conf_k[2][64] = {{0}};
   NF4_TRY(allow_smem(k_packed_dq<D>, SMEM_BWD, conf_q));
-  NF4_TRY(allow_smem(k_packed_dkv<D>, SMEM_BWD, conf_k));
   // the query side writes the statistics that the key side reads
   p.tiles = query_tiles;
   k_packed_dq<D><<<(unsigned)p.n_tiles * p.nq, B_THREADS, SMEM_BWD, s>>>(p);
   note_launch();
   NF4_CUDA_TRY(cudaGetLastError());
   p.tiles = key_tiles;
-  NF4_CUDA_TRY(launch_kernel(k_packed_dkv<D>, (int64_t)p.n_tiles * p.nkv * 2, B_THREADS, SMEM_BWD, true, s, p));
+  int dev = 0, sms = 0;
+  NF4_CUDA_TRY(cudaGetDevice(&dev));
+  NF4_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  const int64_t tiles = (int64_t)p.n_tiles * p.nkv;
+  if (split_heads(pack, p.nkv, p.nq / p.nkv, sms)) {
+    NF4_TRY(allow_smem(k_packed_dkv<D, true>, SMEM_BWD, conf_k[1]));
+    NF4_CUDA_TRY(launch_kernel(k_packed_dkv<D, true>, tiles * 2, {B_THREADS, SMEM_BWD, true, 2}, s, p));
+  } else {
+    NF4_TRY(allow_smem(k_packed_dkv<D, false>, SMEM_BWD, conf_k[0]));
+    NF4_CUDA_TRY(launch_kernel(k_packed_dkv<D, false>, tiles, {B_THREADS, SMEM_BWD, true, 1}, s, p));
+  }
   note_launch();
   return NF4LS_OK;
 }
@@ -1202,5 +1247,5 @@ extern "C" int nf4ls_packed_attention_bwd(const nf4ls_pack* pack, const nf4ls_pa
   p.err = device_error_ptr();
   const PackTile *qt = tile_list(pack, pack->off_query_tiles), *kt = tile_list(pack, pack->off_key_tiles);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return d == 64 ? launch_bwd<64>(p, qt, kt, s) : launch_bwd<128>(p, qt, kt, s);
+  return d == 64 ? launch_bwd<64>(p, pack, qt, kt, s) : launch_bwd<128>(p, pack, qt, kt, s);
 }

@@ -386,19 +386,28 @@ __device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // A launch; early: it may begin while the one before it still runs (its kernel waits itself).
+struct LaunchHow {
+  int threads;
+  size_t smem;
+  bool early;
+  int cluster;  // blocks of one, 1: none
+};
 template <typename... P, typename... A>
-cudaError_t launch_kernel(void (*k)(P...), int64_t blocks, int threads, size_t smem, bool early, cudaStream_t s,
-                          A... args) {
-  cudaLaunchAttribute at[1];
+cudaError_t launch_kernel(void (*k)(P...), int64_t blocks, const LaunchHow& how, cudaStream_t s, A... args) {
+  cudaLaunchAttribute at[2];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3((unsigned)how.threads);
+  cfg.dynamicSmemBytes = how.smem;
   cfg.stream = s;
   cfg.attrs = at;
-  if (early) {
+  if (how.early) {
     at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (how.cluster > 1) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs++].val.clusterDim = {(unsigned)how.cluster, 1, 1};
   }
   return cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...);
 }

@@ -14,7 +14,7 @@ namespace nf4ls {
 int check_pack(const nf4ls_pack* p, const char* who) {
   if (!p) return fail(NF4LS_INVALID_ARG, "%s: null pack", who);
   if (p->n_seqs < 1 || p->total < 0 || p->n_tiles < 0 || p->max_len < 0 || p->n_tiles > p->total ||
-      (p->total > 0) != (p->n_tiles > 0))
+      (p->total > 0) != (p->n_tiles > 0) || p->n_blocks < p->n_tiles)
     return fail(NF4LS_INVALID_ARG, "%s: not a pack that nf4ls_pack_layout filled", who);
   if (!p->plan_dev) return fail(NF4LS_INVALID_ARG, "%s: the pack has no plan on the device", who);
   if (!aligned(p->plan_dev, 256)) return fail(NF4LS_ALIGN, "%s: the plan must be 256-byte aligned", who);
@@ -30,14 +30,16 @@ extern "C" int nf4ls_pack_layout(const int32_t* lengths_host, int32_t n_seqs, nf
   if (!lengths_host || !out) return fail(NF4LS_INVALID_ARG, "nf4ls_pack_layout: null argument");
   if (n_seqs < 1 || n_seqs > NF4LS_PACK_MAX_SEQS)
     return fail(NF4LS_INVALID_ARG, "nf4ls_pack_layout: %d sequences, 1 to %d are supported", n_seqs, NF4LS_PACK_MAX_SEQS);
-  int64_t total = 0, tiles = 0;
+  int64_t total = 0, tiles = 0, blocks = 0;
   int32_t longest = 0;
   for (int32_t i = 0; i < n_seqs; ++i) {
     if (lengths_host[i] < 0) return fail(NF4LS_INVALID_ARG, "nf4ls_pack_layout: sequence %d has length %d", i, lengths_host[i]);
     total += lengths_host[i];
     if (total > NF4LS_PACK_MAX_ROWS)
       return fail(NF4LS_INVALID_ARG, "nf4ls_pack_layout: more than %d rows", NF4LS_PACK_MAX_ROWS);
-    tiles += (lengths_host[i] + 127) / 128;
+    const int64_t n = (lengths_host[i] + 127) / 128;
+    tiles += n;
+    blocks += n * (n + 1) / 2;
     longest = std::max(longest, lengths_host[i]);
   }
   std::memset(out, 0, sizeof(*out));
@@ -45,6 +47,7 @@ extern "C" int nf4ls_pack_layout(const int32_t* lengths_host, int32_t n_seqs, nf
   out->total = (int32_t)total;
   out->n_tiles = (int32_t)tiles;
   out->max_len = longest;
+  out->n_blocks = blocks;
   uint64_t off = 0;
   auto take = [&](uint64_t bytes) {
     const uint64_t o = off;

@@ -114,6 +114,33 @@ def test_many_short_sequences_and_a_long_one():
         within(g, w, t, name)
 
 
+@pytest.mark.parametrize("heads", [(6, 2, 128), (5, 1, 64), (10, 5, 128)], ids=str)
+def test_gradients_of_many_sequences(heads):
+    """So many key tiles that each is one block's work, where a few are two blocks'."""
+    n_q, n_kv, d = heads
+    lengths = [129, 1, 200] * 24
+    q, k, v, do = make(lengths, n_q, n_kv, d, extra_rows=3)
+    pack = api.PackedRows(lengths)
+    o, lse = api.packed_attention_fwd(pack, q, k, v, n_q, n_kv, d)
+    total = sum(lengths)
+    buf = torch.full((total + 3, (n_q + 2 * n_kv) * d), 7.0, dtype=torch.bfloat16, device=DEV)
+    outs = (buf[:, :n_q * d], buf[:, n_q * d:(n_q + n_kv) * d], buf[:, (n_q + n_kv) * d:])
+    got = api.packed_attention_bwd(pack, q, k, v, o, do, lse, n_q, n_kv, d, out=outs)
+    ref = reference_grad(lengths, q, k, v, o, do, lse, n_q, n_kv, d, d ** -0.5)
+    for name, g, w, t in zip(("dq", "dk", "dv"), got, ref[:3], ref[3:]):
+        within(g[:total], w, t, name)
+    assert (buf[total:] == 7.0).all()
+    g0 = buf.clone()
+    rows = torch.ones(total + 3, dtype=torch.bool, device=DEV)
+    rows[130:330] = False  # the third sequence, whose rows the tiles of the second one reach
+    q1, k1, v1, do1 = (x.clone() for x in (q, k, v, do))
+    for x in (q1, k1, v1, do1):
+        x[130:330] = math.nan
+    o1, l1 = api.packed_attention_fwd(pack, q1, k1, v1, n_q, n_kv, d)
+    api.packed_attention_bwd(pack, q1, k1, v1, o1, do1, l1, n_q, n_kv, d, out=outs)
+    assert torch.equal(buf[rows], g0[rows])
+
+
 @pytest.mark.parametrize("factor", [0.01, 30.0])
 def test_flat_and_sharp_rows(factor):
     """Scores all alike, and scores of hundreds of nats that grow along the keys (the

@@ -29,6 +29,7 @@ def test_plan_lists_every_row_and_tile_once(lengths):
             index += 1
     q, k = _tiles(p, p.pack.off_query_tiles), _tiles(p, p.pack.off_key_tiles)
     assert sorted(q) == sorted(want) and sorted(k) == sorted(want)
+    assert p.pack.n_blocks == sum(t + 1 for _, _, t, _ in q)
     work_q = [t for _, _, t, _ in q]
     work_k = [(n + 127) // 128 - t for _, n, t, _ in k]
     assert work_q == sorted(work_q, reverse=True) and work_k == sorted(work_k, reverse=True)
