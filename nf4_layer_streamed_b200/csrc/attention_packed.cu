@@ -406,10 +406,15 @@ __device__ __forceinline__ bool smem_base(uint8_t* raw, uint8_t** base, int* err
   return false;
 }
 
-// QUERY side: dQ of one query tile of one head.  The Q and dO tiles are copied into TMEM
-// (bf16 pairs, one query row per lane), so that S and dP read only K and V from shared
-// memory (4 KB per 64 tensor-core cycles instead of 8 KB, which is all that shared memory
-// delivers, while the next tiles land in it).
+// QUERY side: dQ of query tiles of one head each ("items"), a block an SM that goes through its
+// share of them: the next one's tiles land and its first products run under the end of this
+// one.  (A block for each, whose first products waited 5 k cycles for 160 KB of tiles: both
+// kernels 81 instead of 72 us for 2048 rows, 1839 instead of 1777 for 16.4k.)  The Q and dO
+// tiles are copied into TMEM (bf16 pairs, one query row per lane), so that S and dP read only
+// K and V from shared memory: 4 KB per 64 tensor-core cycles instead of 8 KB, which is all
+// that shared memory delivers, while the next tiles land in it.  The K ring also carries an
+// item's O tile (for delta), behind its first K tile, and, behind the last, the place through
+// which its dQ leaves.
 template <int D>
 __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constant__ BwdParams p) {
   constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM;  // swizzle atoms, k-steps and bytes of a tile
@@ -419,36 +424,35 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   if (!smem_base(smem_raw, &base, p.err)) return;
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + B_OFF_BAR);
   uint64_t* q_full = bars;          // Q, dO
-  uint64_t* o_full = bars + 1;      // the O tile (for delta), in the third K stage
-  uint64_t* o_read = bars + 2;      // ... and it has been read (one arrival per elementwise warp)
-  uint64_t* qa_full = bars + 3;     // Q and dO are in TMEM (one arrival per elementwise warp)
-  uint64_t* k_full = bars + 4;      // 3
-  uint64_t* k_empty = bars + 7;     // 3
-  uint64_t* v_full = bars + 10;     // 2
-  uint64_t* v_empty = bars + 12;    // 2
-  uint64_t* s_full = bars + 14;
-  uint64_t* s_read = bars + 15;     // S is in registers (one arrival per elementwise warp)
-  uint64_t* dp_full = bars + 16;
-  uint64_t* ds_full = bars + 17;    // dS is in TMEM (one arrival per elementwise warp)
-  uint64_t* acc_full = bars + 18;
-  uint64_t* drain = bars + 19;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
+  uint64_t* q_read = bars + 1;      // ... and they are in TMEM, and in delta
+  uint64_t* qa_full = bars + 2;     // Q and dO are in TMEM (one arrival per elementwise warp)
+  uint64_t* k_full = bars + 3;      // 3
+  uint64_t* k_empty = bars + 6;     // 3
+  uint64_t* v_full = bars + 9;      // 2
+  uint64_t* v_empty = bars + 11;    // 2
+  uint64_t* s_full = bars + 13;
+  uint64_t* s_read = bars + 14;     // S is in registers (one arrival per elementwise warp)
+  uint64_t* dp_full = bars + 15;
+  uint64_t* ds_full = bars + 16;    // dS is in TMEM (one arrival per elementwise warp)
+  uint64_t* acc_full = bars + 17;
+  uint64_t* drain = bars + 18;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = warp_number(), lane = threadIdx.x & 31;
-  const int h = blockIdx.x % p.nq;
-  const PackTile pt = p.tiles[blockIdx.x / p.nq];
-  const int qt = pt.tile, row0 = pt.row0;
-  const int n_rows = min(TT, pt.len - qt * TT);
-  const int kvh = h / (p.nq / p.nkv);
-  const int n_kt = qt + 1;  // key tiles at or before the diagonal
+  // Item number n of this block: heads fastest, then the plan's tiles, most key tiles first;
+  // every second round of blocks goes backwards, so that long items meet short ones.
+  const int n_items = p.n_tiles * p.nq, G = gridDim.x;
+  auto item_of = [&](int n) -> int {
+    const int64_t at = (int64_t)n * G + ((n & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    return at < n_items ? (int)at : -1;  // only the last round has fewer items than blocks
+  };
 
   // by the producer: the MMA warp goes straight to the allocation, which takes a whole,
   // converged warp (beside a branch of its own first lane it faulted)
   if (warp == B_PROD && lane == 0) {
     mbar_init(q_full, 1);
-    mbar_init(o_full, 1);
-    mbar_init(o_read, B_EW / 32);
+    mbar_init(q_read, 1);
     mbar_init(qa_full, B_EW / 32);
     for (int i = 0; i < 3; ++i) {
       mbar_init(&k_full[i], 1);
@@ -477,6 +481,9 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   constexpr uint32_t T_S = 0, T_DP = 128, T_DQ = 256, T_Q = 384, T_DO = 448;  // dS packed over dP
+  // entries of the K ring before this item, of the V ring (and tiles): c3 + n_kt + 2, c + n_kt
+  // behind it; K tile kt is entry c3 + k_entry(kt)
+  auto k_entry = [](int kt) { return kt == 0 ? 0 : kt + 1; };
 
   if (warp == B_PROD) {
     if (lane == 0) {
@@ -485,36 +492,53 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
       tma_prefetch_desc(&p.tv);
       tma_prefetch_desc(&p.tdo);
       tma_prefetch_desc(&p.to);
-      mbar_arrive_expect_tx(q_full, 2 * TB);
-      for (int j = 0; j < NA; ++j) {
-        tma_load_2d(base + B_OFF_A + j * ATOM, &p.tq, q_full, h * D + 64 * j, row0 + qt * TT);
-        tma_load_2d(base + B_OFF_A + TILE_BYTES + j * ATOM, &p.tdo, q_full, h * D + 64 * j, row0 + qt * TT);
-      }
-      int issued_k = 0, issued_v = 0;
-      for (int kt = 0; kt < n_kt; ++kt) {
-        const int sk = kt % 3, sv = kt & 1;
-        if (kt == 2 && !mbar_wait(o_read, 0, abort_flag, p.err, KID_PACKED, 40)) break;
-        if (kt >= 3 && !mbar_wait(&k_empty[sk], (kt / 3 - 1) & 1, abort_flag, p.err, KID_PACKED, 41)) break;
-        mbar_arrive_expect_tx(&k_full[sk], TB);
-        for (int j = 0; j < NA; ++j)
-          tma_load_2d(base + B_OFF_R3 + sk * TILE_BYTES + j * ATOM, &p.tk, &k_full[sk], kvh * D + 64 * j, row0 + kt * TT);
-        issued_k = kt + 1;
-        if (kt >= 2 && !mbar_wait(&v_empty[sv], ((kt >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 42)) break;
-        mbar_arrive_expect_tx(&v_full[sv], TB);
-        for (int j = 0; j < NA; ++j)
-          tma_load_2d(base + B_OFF_R2 + sv * TILE_BYTES + j * ATOM, &p.tv, &v_full[sv], kvh * D + 64 * j, row0 + kt * TT);
-        issued_v = kt + 1;
-        if (kt == 0) {
-          mbar_arrive_expect_tx(o_full, TB);
-          for (int j = 0; j < NA; ++j)
-            tma_load_2d(base + B_OFF_R3 + 2 * TILE_BYTES + j * ATOM, &p.to, o_full, h * D + 64 * j, row0 + qt * TT);
+      int n_q = 0, e3 = 0, e2 = 0;  // issued: items' Q and dO, entries of the rings
+      // the next entry of the K ring is free: its stage, or -1
+      auto ring3 = [&]() -> int {
+        const int st = e3 % 3;
+        return e3 < 3 || mbar_wait(&k_empty[st], (e3 / 3 - 1) & 1, abort_flag, p.err, KID_PACKED, 41) ? st : -1;
+      };
+      auto load = [&](const CUtensorMap* map, uint8_t* to, uint64_t* full, int col, int row) {
+        mbar_arrive_expect_tx(full, TB);
+        for (int j = 0; j < NA; ++j) tma_load_2d(to + j * ATOM, map, full, col + 64 * j, row);
+      };
+      bool ok = true;
+      for (int n = 0, item; ok && (item = item_of(n)) >= 0; ++n) {
+        const int h = item % p.nq, col = h * D, kvc = h / (p.nq / p.nkv) * D;
+        const PackTile pt = p.tiles[item / p.nq];
+        const int row = pt.row0 + pt.tile * TT, n_kt = pt.tile + 1;
+        if (n > 0 && !mbar_wait(q_read, (n - 1) & 1, abort_flag, p.err, KID_PACKED, 40)) break;
+        mbar_arrive_expect_tx(q_full, 2 * TB);
+        for (int j = 0; j < NA; ++j) {
+          tma_load_2d(base + B_OFF_A + j * ATOM, &p.tq, q_full, col + 64 * j, row);
+          tma_load_2d(base + B_OFF_A + TILE_BYTES + j * ATOM, &p.tdo, q_full, col + 64 * j, row);
         }
+        n_q = n + 1;
+        for (int kt = 0; kt < n_kt; ++kt) {
+          int st = ring3();
+          if (!(ok = st >= 0)) break;
+          load(&p.tk, base + B_OFF_R3 + st * TILE_BYTES, &k_full[st], kvc, pt.row0 + kt * TT);
+          ++e3;
+          const int sv = e2 & 1;
+          if (e2 >= 2 && !(ok = mbar_wait(&v_empty[sv], ((e2 >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 42))) break;
+          load(&p.tv, base + B_OFF_R2 + sv * TILE_BYTES, &v_full[sv], kvc, pt.row0 + kt * TT);
+          ++e2;
+          if (kt == 0) {
+            if (!(ok = (st = ring3()) >= 0)) break;
+            load(&p.to, base + B_OFF_R3 + st * TILE_BYTES, &k_full[st], col, row);
+            ++e3;
+          }
+        }
+        if (!ok) break;
+        const int st = ring3();  // the place for dQ
+        if (st < 0) break;
+        mbar_arrive(&k_full[st]);
+        ++e3;
       }
       if (*abort_flag) {  // let the copies already issued land before the CTA exits
-        mbar_wait_drain(q_full, 0);
-        if (issued_v > 0) mbar_wait_drain(o_full, 0);
-        for (int i = max(0, issued_k - 3); i < issued_k; ++i) mbar_wait_drain(&k_full[i % 3], (i / 3) & 1);
-        for (int i = max(0, issued_v - 2); i < issued_v; ++i) mbar_wait_drain(&v_full[i & 1], (i >> 1) & 1);
+        if (n_q > 0) mbar_wait_drain(q_full, (n_q - 1) & 1);
+        for (int i = max(0, e3 - 3); i < e3; ++i) mbar_wait_drain(&k_full[i % 3], (i / 3) & 1);
+        for (int i = max(0, e2 - 2); i < e2; ++i) mbar_wait_drain(&v_full[i & 1], (i >> 1) & 1);
       }
     }
   } else if (warp == B_MMA) {
@@ -527,45 +551,50 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
       tc_fence_after();
       return ok;
     };
-    auto scores = [&](int i) {  // S(i): over the head dim, Q in TMEM
-      const uint32_t sK = s3 + (i % 3) * TILE_BYTES;
+    auto scores = [&](int e) -> bool {  // S of the K tile in entry e: over the head dim, Q in TMEM
+      if (!wait(&k_full[e % 3], e / 3, 44)) return false;
+      const uint32_t sK = s3 + (e % 3) * TILE_BYTES;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
         umma_ts(el, tmem + T_S, tmem + T_Q + ks * 8, sdesc_sw128(sK + (ks >> 2) * ATOM + (ks & 3) * 32, 16, 1024),
                 idesc_s, ks ? 1u : 0u);
       commit_by(el, s_full);
+      return true;
     };
-    auto dprobs = [&](int i) {  // dP(i)
-      const uint32_t sV = s2 + (i & 1) * TILE_BYTES;
+    auto dprobs = [&](int e) -> bool {  // dP of the V tile in entry e
+      if (!wait(&v_full[e & 1], e >> 1, 45)) return false;
+      const uint32_t sV = s2 + (e & 1) * TILE_BYTES;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
         umma_ts(el, tmem + T_DP, tmem + T_DO + ks * 8, sdesc_sw128(sV + (ks >> 2) * ATOM + (ks & 3) * 32, 16, 1024),
                 idesc_s, ks ? 1u : 0u);
       commit_by(el, dp_full);
-      commit_by(el, &v_empty[i & 1]);
+      commit_by(el, &v_empty[e & 1]);
+      return true;
     };
-    bool ok = wait(qa_full, 0, 43) && !*abort_flag;
-    if (ok && (ok = wait(&k_full[0], 0, 44))) scores(0);
-    if (ok && (ok = wait(&v_full[0], 0, 45))) dprobs(0);
-    for (int i = 0; ok && i < n_kt; ++i) {
-      if (i + 1 < n_kt) {
-        if (!(ok = wait(&k_full[(i + 1) % 3], (i + 1) / 3, 44))) break;
-        if (!(ok = wait(s_read, i, 46))) break;
-        scores(i + 1);
-      }
-      if (!(ok = wait(ds_full, i, 47))) break;
-      const uint32_t sK = s3 + (i % 3) * TILE_BYTES;
+    bool ok = true;
+    int c3 = 0, c = 0;
+    for (int n = 0, item; ok && (item = item_of(n)) >= 0; ++n) {
+      const int n_kt = p.tiles[item / p.nq].tile + 1;
+      // (the elementwise warps have then read the last item's S; its dP(last) goes first)
+      if (!(ok = wait(qa_full, n, 43) && !*abort_flag)) break;
+      if (!(ok = scores(c3) && dprobs(c))) break;
+      for (int i = 0; i < n_kt; ++i) {
+        if (i + 1 < n_kt && !(ok = wait(s_read, c + i, 46) && scores(c3 + k_entry(i + 1)))) break;
+        if (!(ok = wait(ds_full, c + i, 47))) break;
+        const int e = c3 + k_entry(i);
+        const uint32_t sK = s3 + (e % 3) * TILE_BYTES;
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks)  // 16 keys per step
-        umma_ts(el, tmem + T_DQ, tmem + packed32(T_DP, ks), sdesc_sw128(sK + ks * 2048, ATOM, 1024), idesc_a,
-                (i | ks) ? 1u : 0u);
-      commit_by(el, &k_empty[i % 3]);
-      if (i + 1 < n_kt) {
-        if (!(ok = wait(&v_full[(i + 1) & 1], (i + 1) >> 1, 45))) break;
-        dprobs(i + 1);
+        for (int ks = 0; ks < 8; ++ks)  // 16 keys per step
+          umma_ts(el, tmem + T_DQ, tmem + packed32(T_DP, ks), sdesc_sw128(sK + ks * 2048, ATOM, 1024), idesc_a,
+                  (i | ks) ? 1u : 0u);
+        commit_by(el, &k_empty[e % 3]);
+        if (i + 1 < n_kt && !(ok = dprobs(c + i + 1))) break;
       }
+      if (ok) commit_by(el, acc_full);
+      c3 += n_kt + 2;
+      c += n_kt;
     }
-    if (ok) commit_by(el, acc_full);
   } else if (warp >= B_FIRST) {
     // ------------------------------------------------------------------ elementwise + epilogue
     const int tid = threadIdx.x - B_FIRST * 32;
@@ -580,115 +609,152 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     const int atom = g >> 1, c0 = (g & 1) * 4;
     const uint8_t* q_row = base + B_OFF_A + atom * ATOM + r * 128;
     const uint8_t* dO_row = base + B_OFF_A + TILE_BYTES + atom * ATOM + r * 128;
-    const uint8_t* o_row = base + B_OFF_R3 + 2 * TILE_BYTES + atom * ATOM + r * 128;
+    // A failed wait leaves no item's loop: the other warps would wait at a meeting for good.
+    bool ok = true;
+    auto to_tmem = [&](int n) {
+      ok = ok && warp_wait(q_full, n & 1, abort_flag, p.err, KID_PACKED, 50);
+      if (ok && has_dims) {
+        uint32_t w[16];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>((t ? dO_row : q_row) + (((c0 + c) ^ (r & 7)) << 4));
+            w[4 * c] = x.x, w[4 * c + 1] = x.y, w[4 * c + 2] = x.z, w[4 * c + 3] = x.w;
+          }
+          tmem_st16(trow + (t ? T_DO : T_Q) + g * 16, w);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qa_full);  // also on failure: the MMA warp then sees the abort
+      __syncwarp();
+    };
     // rows behind the sequence's end: no lse to read; their lanes compute values that
     // nothing stores
-    const float lse2 = r < n_rows ? p.lse[(size_t)h * p.total + row0 + qt * TT + r] * 1.4426950408889634f : 0.f;
-    bool ok = warp_wait(q_full, 0, abort_flag, p.err, KID_PACKED, 50);
-    if (ok && has_dims) {
-      uint32_t qv[16], dv[16];
+    auto lse_of = [&](int h, const PackTile& pt) -> float {
+      const int at = pt.tile * TT + r;
+      return at < pt.len ? p.lse[(size_t)h * p.total + pt.row0 + at] * 1.4426950408889634f : 0.f;
+    };
+    const uint64_t sl2 = pack2(p.scale_log2, p.scale_log2);
+    int item = item_of(0), h = item % p.nq, c3 = 0, c = 0;
+    PackTile pt = p.tiles[item / p.nq];
+    float lse2 = lse_of(h, pt);
+    to_tmem(0);
+    for (int n = 0;; ++n) {
+      const int qt = pt.tile, n_kt = qt + 1, n_rows = min(TT, pt.len - qt * TT);
+      {
+        const int e = c3 + 1;
+        ok = ok && warp_wait(&k_full[e % 3], (e / 3) & 1, abort_flag, p.err, KID_PACKED, 51);
+        if (ok && has_dims) {
+          const uint8_t* o_row = base + B_OFF_R3 + (e % 3) * TILE_BYTES + atom * ATOM + r * 128;
+          float s = 0.f;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t off = (uint32_t)(((c0 + c) ^ (r & 7)) << 4);
-        const uint4 d = *reinterpret_cast<const uint4*>(dO_row + off);
-        const uint4 q = *reinterpret_cast<const uint4*>(q_row + off);
-        qv[4 * c] = q.x, qv[4 * c + 1] = q.y, qv[4 * c + 2] = q.z, qv[4 * c + 3] = q.w;
-        dv[4 * c] = d.x, dv[4 * c + 1] = d.y, dv[4 * c + 2] = d.z, dv[4 * c + 3] = d.w;
-      }
-      tmem_st16(trow + T_Q + g * 16, qv);
-      tmem_st16(trow + T_DO + g * 16, dv);
-      tmem_wait_st();
-    }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(qa_full);  // also on failure: the MMA warp then sees the abort
-    if (ok) ok = warp_wait(o_full, 0, abort_flag, p.err, KID_PACKED, 51);
-    if (ok && has_dims) {
-      float s = 0.f;
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t off = (uint32_t)(((c0 + c) ^ (r & 7)) << 4);
+            const uint4 a = *reinterpret_cast<const uint4*>(o_row + off);
+            const uint4 d = *reinterpret_cast<const uint4*>(dO_row + off);
+            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, dw[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t off = (uint32_t)(((c0 + c) ^ (r & 7)) << 4);
-        const uint4 a = *reinterpret_cast<const uint4*>(o_row + off);
-        const uint4 d = *reinterpret_cast<const uint4*>(dO_row + off);
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, dw[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s += bf16_lo(aw[j]) * bf16_lo(dw[j]) + bf16_hi(aw[j]) * bf16_hi(dw[j]);
-      }
-      red[g * 128 + r] = s;
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(o_read);
-    bar_ew();
-    float dl = 0.f;
-    if (ok)
-      for (int i = 0; i < D / 32; ++i) dl += red[i * 128 + r];
-    if (ok && g == 0) {
-      float* st = p.stats + ((size_t)h * p.n_tiles + pt.index) * (2 * TT);
-      st[r] = -lse2;
-      st[TT + r] = -dl;
-    }
-    const uint64_t sl2 = pack2(p.scale_log2, p.scale_log2), nlse2 = pack2(-lse2, -lse2), ndl2 = pack2(-dl, -dl);
-    for (int kt = 0; ok && kt < n_kt; ++kt) {
-      const bool diag = kt == qt;
-      if (!(ok = warp_wait(s_full, kt & 1, abort_flag, p.err, KID_PACKED, 52))) break;
-      tc_fence_after();
-      uint32_t sv[32];
-      tmem_ld32(trow + T_S + g * 32, sv);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(s_read);
-      if (diag && n_rows < TT) {
-        // rows of K behind the sequence's end: zeros for the product dS K (S is done with them)
-        if (r >= n_rows && g == 0) zero_row<NA>(smem_u32(base + B_OFF_R3 + (kt % 3) * TILE_BYTES), r);
-        fence_proxy_async_smem();
-      }
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        const uint64_t x = fma2(pack2(sv[j], sv[j + 1]), sl2, nlse2);
-        sv[j] = __float_as_uint(fast_exp2(lo2(x)));
-        sv[j + 1] = __float_as_uint(fast_exp2(hi2(x)));
-      }
-      if (!(ok = warp_wait(dp_full, kt & 1, abort_flag, p.err, KID_PACKED, 53))) break;
-      tc_fence_after();
-      uint32_t dp[32];
-      tmem_ld32(trow + T_DP + g * 32, dp);
-      tmem_wait_ld();
-      either(diag, [&](auto masked) {  // keys 32 g .. of the tile
-        uint32_t dd[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const uint64_t ds = mul2(pack2(sv[2 * j], sv[2 * j + 1]), add2(pack2(dp[2 * j], dp[2 * j + 1]), ndl2));
-          float d0 = lo2(ds), d1 = hi2(ds);
-          if (masked) {
-            const int c = g * 32 + 2 * j;
-            d0 = c <= r ? d0 : 0.f;
-            d1 = c + 1 <= r ? d1 : 0.f;
+            for (int j = 0; j < 4; ++j) s += bf16_lo(aw[j]) * bf16_lo(dw[j]) + bf16_hi(aw[j]) * bf16_hi(dw[j]);
           }
-          dd[j] = pack_bf16x2(d0, d1);
+          red[g * 128 + r] = s;
         }
-        tmem_st16(trow + T_DP + g * 32, dd);  // over dP values this warp has read
-      });
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
-    }
-    // dQ through the Q tile's shared memory (Q is in TMEM) and TMA stores; every elementwise
-    // warp reaches the barrier, the store is issued only when no wait failed
-    if (ok && warp_wait(acc_full, 0, abort_flag, p.err, KID_PACKED, 54)) {
+        bar_ew();
+        if (tid == 0) {
+          mbar_arrive(q_read);
+          mbar_arrive(&k_empty[e % 3]);
+        }
+        __syncwarp();
+      }
+      float dl = 0.f;
+      if (ok)
+        for (int i = 0; i < D / 32; ++i) dl += red[i * 128 + r];
+      if (ok && g == 0) {
+        float* st = p.stats + ((size_t)h * p.n_tiles + pt.index) * (2 * TT);
+        st[r] = -lse2;
+        st[TT + r] = -dl;
+      }
+      const uint64_t nlse2 = pack2(-lse2, -lse2), ndl2 = pack2(-dl, -dl);
+      for (int kt = 0; ok && kt < n_kt; ++kt) {
+        const bool diag = kt == qt;
+        if (!(ok = warp_wait(s_full, (c + kt) & 1, abort_flag, p.err, KID_PACKED, 52))) break;
+        tc_fence_after();
+        uint32_t sv[32];
+        tmem_ld32(trow + T_S + g * 32, sv);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_read);
+        if (diag && n_rows < TT) {
+          // rows of K behind the sequence's end: zeros for the product dS K (S is done with them)
+          if (r >= n_rows && g == 0)
+            zero_row<NA>(smem_u32(base + B_OFF_R3 + ((c3 + k_entry(kt)) % 3) * TILE_BYTES), r);
+          fence_proxy_async_smem();
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          const uint64_t x = fma2(pack2(sv[j], sv[j + 1]), sl2, nlse2);
+          sv[j] = __float_as_uint(fast_exp2(lo2(x)));
+          sv[j + 1] = __float_as_uint(fast_exp2(hi2(x)));
+        }
+        if (!(ok = warp_wait(dp_full, (c + kt) & 1, abort_flag, p.err, KID_PACKED, 53))) break;
+        tc_fence_after();
+        uint32_t dp[32];
+        tmem_ld32(trow + T_DP + g * 32, dp);
+        tmem_wait_ld();
+        either(diag, [&](auto masked) {  // keys 32 g .. of the tile
+          uint32_t dd[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint64_t ds = mul2(pack2(sv[2 * j], sv[2 * j + 1]), add2(pack2(dp[2 * j], dp[2 * j + 1]), ndl2));
+            float d0 = lo2(ds), d1 = hi2(ds);
+            if (masked) {
+              const int c = g * 32 + 2 * j;
+              d0 = c <= r ? d0 : 0.f;
+              d1 = c + 1 <= r ? d1 : 0.f;
+            }
+            dd[j] = pack_bf16x2(d0, d1);
+          }
+          tmem_st16(trow + T_DP + g * 32, dd);  // over dP values this warp has read
+        });
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_full);
+      }
+      const int next = item_of(n + 1), h_now = h, row = pt.row0 + qt * TT;
+      float lse_next = 0.f;
+      if (next >= 0) {
+        h = next % p.nq;
+        pt = p.tiles[next / p.nq];
+        lse_next = lse_of(h, pt);
+      }
+      ok = ok && warp_wait(acc_full, n & 1, abort_flag, p.err, KID_PACKED, 54);
       tc_fence_after();
-      if (has_dims) {
+      if (next >= 0) to_tmem(n + 1);  // the next item's first products run under this one's end
+      const int e = c3 + n_kt + 1;
+      const uint32_t out = smem_u32(base + B_OFF_R3 + (e % 3) * TILE_BYTES);
+      ok = ok && warp_wait(&k_full[e % 3], (e / 3) & 1, abort_flag, p.err, KID_PACKED, 55);
+      if (ok && has_dims) {
         uint32_t v[32];
         tmem_ld32(trow + T_DQ + g * 32, v);
         tmem_wait_ld();
-        stage_row32(smem_u32(base + B_OFF_A), r, g, v, p.scale);
+        stage_row32(out, r, g, v, p.scale);
       }
+      fence_proxy_async_smem();
+      bar_ew();
+      // the store is issued only when no wait failed
+      if (!*abort_flag) store_tile<D>(&p.tdq, p.dq, p.ld_dq, out, row, h_now * D, n_rows, tid, B_EW);
+      if (next < 0) break;
+      if (n_rows < TT) bar_ew();  // every thread has read its part of the staged tile
+      if (tid == 0) mbar_arrive(&k_empty[e % 3]);
+      __syncwarp();
+      lse2 = lse_next;
+      c3 += n_kt + 2;
+      c += n_kt;
     }
-    fence_proxy_async_smem();
-    bar_ew();
-    if (!*abort_flag)
-      store_tile<D>(&p.tdq, p.dq, p.ld_dq, smem_u32(base + B_OFF_A), row0 + qt * TT, h * D, n_rows, tid, B_EW);
   }
   __syncthreads();
   if (warp == B_MMA && *abort_flag) {  // products already issued finish before TMEM is freed
@@ -1106,15 +1172,15 @@ template <int D>
 int launch_bwd(BwdParams& p, const nf4ls_pack* pack, const PackTile* query_tiles, const PackTile* key_tiles, cudaStream_t s) {
   static int conf_q[64] = {0}, conf_k[2][64] = {{0}};
   NF4_TRY(allow_smem(k_packed_dq<D>, SMEM_BWD, conf_q));
-  // the query side writes the statistics that the key side reads
-  p.tiles = query_tiles;
-  k_packed_dq<D><<<(unsigned)p.n_tiles * p.nq, B_THREADS, SMEM_BWD, s>>>(p);
-  note_launch();
-  NF4_CUDA_TRY(cudaGetLastError());
-  p.tiles = key_tiles;
   int dev = 0, sms = 0;
   NF4_CUDA_TRY(cudaGetDevice(&dev));
   NF4_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  // the query side writes the statistics that the key side reads
+  p.tiles = query_tiles;
+  k_packed_dq<D><<<std::min(p.n_tiles * p.nq, sms), B_THREADS, SMEM_BWD, s>>>(p);
+  note_launch();
+  NF4_CUDA_TRY(cudaGetLastError());
+  p.tiles = key_tiles;
   const int64_t tiles = (int64_t)p.n_tiles * p.nkv;
   if (split_heads(pack, p.nkv, p.nq / p.nkv, sms)) {
     NF4_TRY(allow_smem(k_packed_dkv<D, true>, SMEM_BWD, conf_k[1]));
