@@ -689,7 +689,7 @@ int nf4ls_rope_apply(const nf4ls_rope_cfg* cfg, const nf4ls_rope_rows* t, nf4ls_
  *   reference model's sums (ref_logp_dev fp32 [n_seqs]; the adapter-off pass);  h = beta gap;
  *   SIGMOID  -(1 - e) log sigmoid(h) - e log sigmoid(-h), e = label_smoothing;
  *   HINGE    max(0, 1 - h);
- *   SQUARED  (gap - 1 / (2 beta))^2;
+ *   SQUARED  (gap - 1 / (2 beta))^2;   (these two take no account of label_smoothing)
  * loss = mean over the pairs.  The forward writes loss [1], seq_logp [n_seqs], margin
  * [n_pairs] (h), coef [n_seqs] (d loss / d S), logp [total] and row_stats [total, 4] (each
  * row's maximum, sum of exp(x - max), what the rounding of logp left out, and 0; 16-byte

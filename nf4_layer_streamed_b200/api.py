@@ -658,7 +658,8 @@ def preference_loss_fwd(pack: PackedRows, logits: torch.Tensor, targets: torch.T
                         stream=None) -> PreferenceForward:
     """Preference loss over the pairs of sequences (2 i preferred to 2 i + 1) of a pack from
     its logits [total, vocab], the rows' targets (int32 [total], negative: no loss) and the
-    reference model's log probability of each sequence (fp32 [n_seqs])."""
+    reference model's log probability of each sequence (fp32 [n_seqs]).  label_smoothing
+    in [0, 0.5) is the sigmoid loss's; the hinge and the squared loss do not use it."""
     pack = _need_pack(pack)
     if kind not in PREFERENCE_KINDS:
         raise ValueError(f"kind {kind!r}: one of {', '.join(PREFERENCE_KINDS)}")

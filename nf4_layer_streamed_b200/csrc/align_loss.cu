@@ -384,8 +384,6 @@ extern "C" int nf4ls_preference_fwd(const nf4ls_pack* pack, const nf4ls_preferen
   if (!(c->beta > 0.0f) || !std::isfinite(c->beta)) return fail(NF4LS_INVALID_ARG, "%s: beta must be positive", who);
   if (!(c->label_smoothing >= 0.0f && c->label_smoothing < 0.5f))
     return fail(NF4LS_INVALID_ARG, "%s: label_smoothing outside [0, 0.5)", who);
-  if (c->label_smoothing != 0.0f && c->kind != NF4LS_PREF_SIGMOID)
-    return fail(NF4LS_INVALID_ARG, "%s: label_smoothing belongs to the sigmoid loss", who);
   NF4_TRY(check_logits(t, pack->total, who));
   if (!ref_logp_dev || !out->loss || !out->seq_logp || !out->margin || !out->coef ||
       (pack->total > 0 && (!out->logp || !out->row_stats)))

@@ -101,6 +101,18 @@ def test_preference(vocab, kind, eps):
     assert torch.equal(inplace, d)
 
 
+@pytest.mark.parametrize("kind", ["hinge", "squared"])
+def test_smoothing_is_the_sigmoid_losss(kind):
+    lengths = [5, 7, 2, 1]
+    x, t, g = make(sum(lengths), 999, seed=4)
+    pack, ref = api.PackedRows(lengths), torch.randn(4, generator=g, device=DEV)
+    outs = []
+    for eps in (0.0, 0.1):
+        f = api.preference_loss_fwd(pack, x, t, ref, 0.1, kind=kind, label_smoothing=eps)
+        outs.append((f.loss, f.margin, f.coef, api.preference_loss_bwd(pack, x, t, f)))
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and outs[0][2].abs().max() > 0
+
+
 @pytest.mark.parametrize("vocab", VOCABS)
 @pytest.mark.parametrize("kl", [0.0, 0.05])
 def test_policy(vocab, kl):
