@@ -75,8 +75,14 @@ struct RowSplit {
   }
 };
 
-// Statistics of a row by the whole block (fixed order: reruns give the same bits).
-__device__ __forceinline__ Stat block_stats(const __nv_bfloat16* row, int V) {
+// Statistics of a row by the whole block (fixed order: reruns give the same bits).  The
+// threads' sums are short and their rounding errors average out; those of the last, sequential
+// one would be most of a row's error (7e-8): it is taken in 64 bits.
+struct RowStat {
+  float m;
+  double s;
+};
+__device__ __forceinline__ RowStat block_stats(const __nv_bfloat16* row, int V) {
   __shared__ float red_m[LT / 32], red_s[LT / 32];
   const int t = threadIdx.x;
   const RowSplit sp(row, V);
@@ -107,17 +113,17 @@ __device__ __forceinline__ Stat block_stats(const __nv_bfloat16* row, int V) {
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if ((t & 31) == 0) red_s[t >> 5] = s;
   __syncthreads();
-  s = red_s[0];
+  double sum = 0.0;
 #pragma unroll
-  for (int i = 1; i < LT / 32; ++i) s += red_s[i];
-  return {m, s};
+  for (int i = 0; i < LT / 32; ++i) sum += (double)red_s[i];
+  return {m, sum};
 }
 
 // out = coef (onehot(target) - exp(x - m) / s) for the row; in may be out.
-__device__ __forceinline__ void block_grad(const __nv_bfloat16* in, __nv_bfloat16* out, int V, Stat st, int target,
-                                           float coef) {
+__device__ __forceinline__ void block_grad(const __nv_bfloat16* in, __nv_bfloat16* out, int V, float m, float sum,
+                                           int target, float coef) {
   const int t = threadIdx.x;
-  const float ref = safe_ref(st.m), k = -coef / st.s;
+  const float ref = safe_ref(m), k = -coef / sum;
   auto g = [&](float x, int i) {
     const float v = exp2_fast((x - ref) * kLog2e) * k;
     return i == target ? v + coef : v;
@@ -164,9 +170,7 @@ __device__ __forceinline__ void block_zero(__nv_bfloat16* out, int V) {
 
 // x[target] and m are bf16 values: the difference and the logarithm in 64 bits lose
 // nothing that sums over long sequences would miss.
-__device__ __forceinline__ double target_logp(float xt, Stat st) {
-  return (double)xt - (double)st.m - log((double)st.s);
-}
+__device__ __forceinline__ double target_logp(float xt, RowStat st) { return (double)xt - (double)st.m - log(st.s); }
 
 // A block per row.  (Clusters that share a row measured 140 us for 2048 rows of 128 k logits,
 // this 73: small independent blocks, four to an SM, hide the reductions' waits best.)
@@ -184,11 +188,11 @@ __global__ void __launch_bounds__(LT) k_token_logp(const __nv_bfloat16* __restri
     return;
   }
   const __nv_bfloat16* x = logits + (size_t)row * ld;
-  const Stat st = block_stats(x, V);
+  const RowStat st = block_stats(x, V);
   if (threadIdx.x == 0) {
     const double lp = target_logp(__bfloat162float(x[target]), st);
     const float hi = (float)lp;
-    stats[row] = make_float4(st.m, st.s, isfinite(hi) ? (float)(lp - (double)hi) : 0.f, 0.f);
+    stats[row] = make_float4(st.m, (float)st.s, isfinite(hi) ? (float)(lp - (double)hi) : 0.f, 0.f);
     logp[row] = hi;
   }
 }
@@ -271,7 +275,7 @@ __global__ void __launch_bounds__(LT, 4) k_logits_grad(const __nv_bfloat16* logi
     return;
   }
   const float4 st = stats[row];
-  block_grad(logits + (size_t)row * ld, out, V, {st.x, st.y}, target, c);
+  block_grad(logits + (size_t)row * ld, out, V, st.x, st.y, target, c);
 }
 
 struct PolicyParams {
@@ -285,20 +289,21 @@ struct PolicyParams {
   float *logp, *row_loss;
 };
 
-// By one thread: the row's loss, into memory, and the coefficient of its gradient.
-__device__ __forceinline__ float policy_row(const PolicyParams& p, int row, float xt, Stat st) {
+// By one thread: the row's loss, into memory, and the coefficient of its gradient; in 64 bits,
+// since the terms of a mean over rows cancel.
+__device__ __forceinline__ float policy_row(const PolicyParams& p, int row, float xt, RowStat st) {
   const double lp = target_logp(xt, st);
-  const float a = p.adv[row], w = p.weights[row];
-  const float r = expf((float)(lp - (double)p.old_logp[row]));
-  const float held_r = fminf(fmaxf(r, 1.0f - p.clip_low), 1.0f + p.clip_high);
-  const float free_s = r * a, held = held_r * a;
+  const double a = p.adv[row], w = p.weights[row];
+  const double r = exp(lp - (double)p.old_logp[row]);
+  const double held_r = fmin(fmax(r, 1.0 - (double)p.clip_low), 1.0 + (double)p.clip_high);
+  const double free_s = r * a, held = held_r * a;
   const bool passes = free_s <= held;  // the gradient flows through the unclipped term
   // no KL term where its coefficient is 0 (ref_logp may then be null)
-  const float gap = p.kl > 0.0f ? (float)((double)p.ref_logp[row] - lp) : 0.0f, e1 = expm1f(gap);
-  const float surrogate = isnan(r) ? r : (passes ? free_s : held);
+  const double gap = p.kl > 0.0f ? (double)p.ref_logp[row] - lp : 0.0, e1 = expm1(gap);
+  const double surrogate = isnan(r) ? r : (passes ? free_s : held);
   p.logp[row] = (float)lp;
-  p.row_loss[row] = w * (p.kl * (e1 - gap) - surrogate);
-  return w * (-p.kl * e1 - (passes ? free_s : 0.0f)) * p.scale;
+  p.row_loss[row] = (float)(w * (p.kl * (e1 - gap) - surrogate));
+  return (float)(w * (-p.kl * e1 - (passes ? free_s : 0.0)) * p.scale);
 }
 
 __global__ void __launch_bounds__(LT, 4) k_policy(const PolicyParams p) {
@@ -317,7 +322,7 @@ __global__ void __launch_bounds__(LT, 4) k_policy(const PolicyParams p) {
   }
   const __nv_bfloat16* x = p.logits + (size_t)row * p.ld;
   const float xt = __bfloat162float(x[target]);
-  const Stat st = block_stats(x, p.V);
+  const RowStat st = block_stats(x, p.V);
   if (threadIdx.x == 0) c_sh = policy_row(p, row, xt, st);
   if (!out) return;
   __syncthreads();
@@ -325,7 +330,7 @@ __global__ void __launch_bounds__(LT, 4) k_policy(const PolicyParams p) {
   if (c == 0.0f)
     block_zero(out, p.V);
   else
-    block_grad(x, out, p.V, st, target, c);
+    block_grad(x, out, p.V, st.m, (float)st.s, target, c);
 }
 
 __global__ void __launch_bounds__(PT) k_sum_rows(const float* __restrict__ v, int n, float* __restrict__ out) {
