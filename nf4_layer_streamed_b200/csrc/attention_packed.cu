@@ -409,7 +409,7 @@ __device__ __forceinline__ bool smem_base(uint8_t* raw, uint8_t** base, int* err
 // QUERY side: dQ of query tiles of one head each ("items"), a block an SM that goes through its
 // share of them: the next one's tiles land and its first products run under the end of this
 // one.  (A block for each, whose first products waited 5 k cycles for 160 KB of tiles: both
-// kernels 81 instead of 72 us for 2048 rows, 1839 instead of 1777 for 16.4k.)  The Q and dO
+// kernels 81 instead of 72 us for 2048 rows, 1839 instead of 1777 for 12.2k.)  The Q and dO
 // tiles are copied into TMEM (bf16 pairs, one query row per lane), so that S and dP read only
 // K and V from shared memory: 4 KB per 64 tensor-core cycles instead of 8 KB, which is all
 // that shared memory delivers, while the next tiles land in it.  The K ring also carries an
