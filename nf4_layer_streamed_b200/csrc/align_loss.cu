@@ -19,7 +19,15 @@ namespace nf4ls {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int LT = 512;  // threads of a row's block
+
+// A block per row, as many as an SM's 2048 threads hold.  Short rows are latency (a block's
+// loads, reduction and the row's own terms): blocks of 256 threads, eight an SM, against 512
+// and four: 8000 rows of 16k logits 91 and 113 us (policy), 4000 rows 33 and 39 (statistics),
+// 38 and 42 (gradient); 2048 rows of 49k 38 and 38, 57 and 54.  Rows so long that those in
+// work do not stay in L2 from a policy row's first pass to its second: two blocks an SM of 768
+// threads that hold 96 KB of their row in shared memory, 1999 rows of 128k 177 us instead of
+// 196; of 65k 103 instead of 97.
+constexpr int kShortRow = 24576, kLongRow = 98304;  // logits
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -82,22 +90,30 @@ struct RowStat {
   float m;
   double s;
 };
-__device__ __forceinline__ RowStat block_stats(const __nv_bfloat16* row, int V) {
-  __shared__ float red_m[LT / 32], red_s[LT / 32];
+template <int T>
+__device__ __forceinline__ RowStat block_stats(const __nv_bfloat16* row, int V, uint4* keep = nullptr,
+                                               int n_keep = 0) {
+  __shared__ float red_m[T / 32], red_s[T / 32];
   const int t = threadIdx.x;
   const RowSplit sp(row, V);
   Stat st = {-INFINITY, 0.0f};
   if (t < sp.head) add1(st, __bfloat162float(row[t]));
   const uint4* v = reinterpret_cast<const uint4*>(row + sp.head);
   int j = t;
-  for (; j + 3 * LT < sp.n16; j += 4 * LT) {
-    const uint4 a = v[j], b = v[j + LT], c = v[j + 2 * LT], d = v[j + 3 * LT];
+  for (; j + 3 * T < sp.n16; j += 4 * T) {
+    const uint4 a = v[j], b = v[j + T], c = v[j + 2 * T], d = v[j + 3 * T];
+    if (j < n_keep) {
+      keep[j] = a;
+      keep[j + T] = b;
+      keep[j + 2 * T] = c;
+      keep[j + 3 * T] = d;
+    }
     add8(st, a);
     add8(st, b);
     add8(st, c);
     add8(st, d);
   }
-  for (; j < sp.n16; j += LT) add8(st, v[j]);
+  for (; j < sp.n16; j += T) add8(st, v[j]);
   if (sp.tail0 + t < V) add1(st, __bfloat162float(row[sp.tail0 + t]));
   // the row's maximum first, so that a thread's sum is scaled to it once
   float m = st.m;
@@ -107,7 +123,7 @@ __device__ __forceinline__ RowStat block_stats(const __nv_bfloat16* row, int V) 
   __syncthreads();
   m = red_m[0];
 #pragma unroll
-  for (int i = 1; i < LT / 32; ++i) m = fmaxf(m, red_m[i]);
+  for (int i = 1; i < T / 32; ++i) m = fmaxf(m, red_m[i]);
   float s = st.s * expf(st.m - safe_ref(m));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -115,13 +131,14 @@ __device__ __forceinline__ RowStat block_stats(const __nv_bfloat16* row, int V) 
   __syncthreads();
   double sum = 0.0;
 #pragma unroll
-  for (int i = 0; i < LT / 32; ++i) sum += (double)red_s[i];
+  for (int i = 0; i < T / 32; ++i) sum += (double)red_s[i];
   return {m, sum};
 }
 
 // out = coef (onehot(target) - exp(x - m) / s) for the row; in may be out.
+template <int T>
 __device__ __forceinline__ void block_grad(const __nv_bfloat16* in, __nv_bfloat16* out, int V, float m, float sum,
-                                           int target, float coef) {
+                                           int target, float coef, const uint4* keep = nullptr, int n_keep = 0) {
   const int t = threadIdx.x;
   const float ref = safe_ref(m), k = -coef / sum;
   auto g = [&](float x, int i) {
@@ -131,7 +148,7 @@ __device__ __forceinline__ void block_grad(const __nv_bfloat16* in, __nv_bfloat1
   const RowSplit sp(in, V);
   if (((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
     // rows that start at different places within 16 bytes: element by element
-    for (int i = t; i < V; i += LT) out[i] = __float2bfloat16_rn(g(__bfloat162float(in[i]), i));
+    for (int i = t; i < V; i += T) out[i] = __float2bfloat16_rn(g(__bfloat162float(in[i]), i));
     return;
   }
   if (t < sp.head) out[t] = __float2bfloat16_rn(g(__bfloat162float(in[t]), t));
@@ -146,25 +163,27 @@ __device__ __forceinline__ void block_grad(const __nv_bfloat16* in, __nv_bfloat1
     o[j] = make_uint4(r[0], r[1], r[2], r[3]);
   };
   // last pieces first: the statistics pass over the same row has left them in L2
-  int j = t + (sp.n16 - 1 - t) / LT * LT;  // this thread's last piece (below t: none)
-  for (; j >= t + 3 * LT; j -= 4 * LT) {
-    const uint4 a = v[j], b = v[j - LT], c = v[j - 2 * LT], d = v[j - 3 * LT];
+  int j = t < sp.n16 ? t + (sp.n16 - 1 - t) / T * T : -1;  // this thread's last piece
+  for (; j >= 0 && (j - t) / T % 4 != 3; j -= T) piece(v[j], j);  // behind the whole steps of four
+  for (; j >= 0; j -= 4 * T) {
+    const uint4* from = j < n_keep ? keep : v;
+    const uint4 a = from[j], b = from[j - T], c = from[j - 2 * T], d = from[j - 3 * T];
     piece(a, j);
-    piece(b, j - LT);
-    piece(c, j - 2 * LT);
-    piece(d, j - 3 * LT);
+    piece(b, j - T);
+    piece(c, j - 2 * T);
+    piece(d, j - 3 * T);
   }
-  for (; j >= t && j < sp.n16; j -= LT) piece(v[j], j);
   const int i = sp.tail0 + t;
   if (i < V) out[i] = __float2bfloat16_rn(g(__bfloat162float(in[i]), i));
 }
 
+template <int T>
 __device__ __forceinline__ void block_zero(__nv_bfloat16* out, int V) {
   const RowSplit sp(out, V);
   const int t = threadIdx.x;
   if (t < sp.head) out[t] = __float2bfloat16_rn(0.f);
   uint4* o = reinterpret_cast<uint4*>(out + sp.head);
-  for (int j = t; j < sp.n16; j += blockDim.x) o[j] = make_uint4(0u, 0u, 0u, 0u);
+  for (int j = t; j < sp.n16; j += T) o[j] = make_uint4(0u, 0u, 0u, 0u);
   if (sp.tail0 + t < V) out[sp.tail0 + t] = __float2bfloat16_rn(0.f);
 }
 
@@ -174,7 +193,8 @@ __device__ __forceinline__ double target_logp(float xt, RowStat st) { return (do
 
 // A block per row.  (Clusters that share a row measured 140 us for 2048 rows of 128 k logits,
 // this 73: small independent blocks, four to an SM, hide the reductions' waits best.)
-__global__ void __launch_bounds__(LT) k_token_logp(const __nv_bfloat16* __restrict__ logits, int64_t ld, int V,
+template <int T>
+__global__ void __launch_bounds__(T) k_token_logp(const __nv_bfloat16* __restrict__ logits, int64_t ld, int V,
                                                    const int32_t* __restrict__ targets, float4* __restrict__ stats,
                                                    float* __restrict__ logp) {
   next_may_start();
@@ -188,7 +208,7 @@ __global__ void __launch_bounds__(LT) k_token_logp(const __nv_bfloat16* __restri
     return;
   }
   const __nv_bfloat16* x = logits + (size_t)row * ld;
-  const RowStat st = block_stats(x, V);
+  const RowStat st = block_stats<T>(x, V);
   if (threadIdx.x == 0) {
     const double lp = target_logp(__bfloat162float(x[target]), st);
     const float hi = (float)lp;
@@ -259,7 +279,8 @@ __global__ void __launch_bounds__(PT) k_preference(const int32_t* __restrict__ c
   }
 }
 
-__global__ void __launch_bounds__(LT, 4) k_logits_grad(const __nv_bfloat16* logits, int64_t ld, int V,
+template <int T>
+__global__ void __launch_bounds__(T, 2048 / T) k_logits_grad(const __nv_bfloat16* logits, int64_t ld, int V,
                                                     const int32_t* __restrict__ targets,
                                                     const float4* __restrict__ stats, const int32_t* __restrict__ seq,
                                                     const float* __restrict__ coef, float scale, __nv_bfloat16* dlogits,
@@ -271,11 +292,11 @@ __global__ void __launch_bounds__(LT, 4) k_logits_grad(const __nv_bfloat16* logi
   __nv_bfloat16* out = dlogits + (size_t)row * ld_d;
   const float c = target >= 0 && target < V ? coef[seq[row]] * scale : 0.0f;
   if (c == 0.0f) {
-    block_zero(out, V);
+    block_zero<T>(out, V);
     return;
   }
   const float4 st = stats[row];
-  block_grad(logits + (size_t)row * ld, out, V, st.x, st.y, target, c);
+  block_grad<T>(logits + (size_t)row * ld, out, V, st.x, st.y, target, c);
 }
 
 struct PolicyParams {
@@ -306,7 +327,9 @@ __device__ __forceinline__ float policy_row(const PolicyParams& p, int row, floa
   return (float)(w * (-p.kl * e1 - (passes ? free_s : 0.0)) * p.scale);
 }
 
-__global__ void __launch_bounds__(LT, 4) k_policy(const PolicyParams p) {
+// KEEP: pieces of 16 bytes of a row that stay in shared memory between its two passes.
+template <int T, int KEEP>
+__global__ void __launch_bounds__(T, 2048 / T) k_policy(const PolicyParams p) {
   __shared__ float c_sh;
   next_may_start();
   const int row = blockIdx.x;
@@ -317,20 +340,22 @@ __global__ void __launch_bounds__(LT, 4) k_policy(const PolicyParams p) {
       p.logp[row] = 0.f;
       p.row_loss[row] = 0.f;
     }
-    if (out) block_zero(out, p.V);
+    if (out) block_zero<T>(out, p.V);
     return;
   }
   const __nv_bfloat16* x = p.logits + (size_t)row * p.ld;
   const float xt = __bfloat162float(x[target]);
-  const RowStat st = block_stats(x, p.V);
+  extern __shared__ uint4 keep[];
+  const int n_keep = out ? min(KEEP, RowSplit(x, p.V).n16) / (4 * T) * (4 * T) : 0;
+  const RowStat st = block_stats<T>(x, p.V, keep, n_keep);
   if (threadIdx.x == 0) c_sh = policy_row(p, row, xt, st);
   if (!out) return;
   __syncthreads();
   const float c = c_sh;
   if (c == 0.0f)
-    block_zero(out, p.V);
+    block_zero<T>(out, p.V);
   else
-    block_grad(x, out, p.V, st.m, (float)st.s, target, c);
+    block_grad<T>(x, out, p.V, st.m, (float)st.s, target, c, keep, n_keep);
 }
 
 __global__ void __launch_bounds__(PT) k_sum_rows(const float* __restrict__ v, int n, float* __restrict__ out) {
@@ -398,7 +423,8 @@ extern "C" int nf4ls_preference_fwd(const nf4ls_pack* pack, const nf4ls_preferen
   auto* stats = reinterpret_cast<float4*>(out->row_stats);
   if (pack->total > 0) {
     const auto* x = static_cast<const __nv_bfloat16*>(t->logits_dev);
-    NF4_TRY(launch(k_token_logp, pack->total, LT, false, s, x, t->ld, t->vocab, t->targets_dev, stats, out->logp));
+    const bool brief = t->vocab < kShortRow;
+    NF4_TRY(launch(brief ? k_token_logp<256> : k_token_logp<512>, pack->total, brief ? 256 : 512, false, s, x, t->ld, t->vocab, t->targets_dev, stats, out->logp));
   }
   const int32_t* cu = reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(pack->plan_dev) + pack->off_cu);
   NF4_TRY(launch(k_preference, 1, PT, true, s, cu, pack->n_seqs, out->logp, stats, ref_logp_dev, c->beta,
@@ -417,7 +443,9 @@ extern "C" int nf4ls_preference_bwd(const nf4ls_pack* pack, const nf4ls_logits* 
   if (!aligned(saved->row_stats, 16)) return fail(NF4LS_ALIGN, "%s: row_stats must be 16-byte aligned", who);
   NF4_TRY(check_grad(t, dlogits_dev, ld_d, who));
   const int32_t* seq = reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(pack->plan_dev) + pack->off_seq);
-  NF4_TRY(launch(k_logits_grad, pack->total, LT, true, static_cast<cudaStream_t>(stream),
+  const bool brief = t->vocab < kShortRow;
+  NF4_TRY(launch(brief ? k_logits_grad<256> : k_logits_grad<512>, pack->total, brief ? 256 : 512, true,
+                 static_cast<cudaStream_t>(stream),
                  static_cast<const __nv_bfloat16*>(t->logits_dev), t->ld, t->vocab, t->targets_dev,
                  reinterpret_cast<const float4*>(saved->row_stats), seq, saved->coef, grad_scale,
                  static_cast<__nv_bfloat16*>(dlogits_dev), ld_d));
@@ -458,7 +486,22 @@ extern "C" int nf4ls_policy_loss(const nf4ls_policy_cfg* c, int32_t rows, const 
     p.scale = c->grad_scale;
     p.logp = logp_dev;
     p.row_loss = row_loss_dev;
-    NF4_TRY(launch(k_policy, rows, LT, false, s, p));
+    if (p.V < kShortRow) {
+      NF4_TRY(launch(k_policy<256, 0>, rows, 256, false, s, p));
+    } else if (p.V < kLongRow) {
+      NF4_TRY(launch(k_policy<512, 0>, rows, 512, false, s, p));
+    } else {
+      constexpr int T = 768, KEEP = 8 * T;  // without a gradient too: the same bits
+      static int configured[64] = {0};
+      int dev = 0;
+      NF4_CUDA_TRY(cudaGetDevice(&dev));
+      if (dev >= 64 || !configured[dev]) {
+        NF4_CUDA_TRY(cudaFuncSetAttribute(k_policy<T, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, KEEP * 16));
+        if (dev < 64) configured[dev] = 1;
+      }
+      NF4_CUDA_TRY(launch_kernel(k_policy<T, KEEP>, rows, {T, p.dlogits ? KEEP * 16 : 0, false, 1}, s, p));
+      note_launch();
+    }
   }
   NF4_TRY(launch(k_sum_rows, 1, PT, true, s, row_loss_dev, rows, loss_dev));
   return NF4LS_OK;

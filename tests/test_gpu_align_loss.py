@@ -116,8 +116,17 @@ def test_smoothing_is_the_sigmoid_losss(kind):
 @pytest.mark.parametrize("vocab", VOCABS)
 @pytest.mark.parametrize("kl", [0.0, 0.05])
 def test_policy(vocab, kl):
-    n = 61
-    x, t, g = make(n, vocab, seed=1, ld=vocab + 9, offset=1)
+    policy(61, vocab, kl, vocab + 9, 1)
+
+
+@pytest.mark.parametrize("vocab", [24575, 49152, 106496, 110003])
+def test_policy_of_many_long_rows(vocab):
+    """More rows than blocks fit on the GPU at once, of lengths that take each kind of block."""
+    policy(701, vocab, 0.05, vocab + 8 + -vocab % 8, 0)
+
+
+def policy(n, vocab, kl, ld, offset):
+    x, t, g = make(n, vocab, seed=1, ld=ld, offset=offset)
     lp, has = logp64(x, t, vocab)
     r = lambda s: torch.randn(n, generator=g, device=DEV) * s  # noqa: E731
     old, ref, adv = (lp.detach() + 0.3 * r(1.0)).float(), (lp.detach() + r(0.5)).float(), r(1.0)
