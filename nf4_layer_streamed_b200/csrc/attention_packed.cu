@@ -291,7 +291,9 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
         if (r >= n_rows) zero_row<NA>(smem_u32(base + F_OFF_V), r);
         fence_proxy_async_smem();
       }
-      const uint64_t sl2 = pack2(sl, sl), nm2 = pack2(-m_run, -m_run);
+      // no score above -inf so far (products beyond fp32): probabilities of 0, not NaN
+      const float ref = m_run == -INFINITY ? 0.0f : m_run;
+      const uint64_t sl2 = pack2(sl, sl), nm2 = pack2(-ref, -ref);
       uint64_t acc[2] = {0, 0};
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {

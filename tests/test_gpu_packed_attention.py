@@ -182,6 +182,27 @@ def test_scale_argument_and_gradient_against_differences():
         assert abs(got - diff) <= 4 * R * grads[i].double().norm().item() * 1.0, (i, got, diff)
 
 
+def test_scores_below_the_range():
+    """Keys of the type's lowest value, whose scores are -inf in fp32: they have no part in rows that
+    see others too, also where they fill whole tiles."""
+    lengths, n_q, n_kv, d, n = [300, 20], 4, 2, 64, 140
+    q, k, v, do = make(lengths, n_q, n_kv, d)
+    q, k = q.abs(), k.clone()
+    k[:n] = torch.finfo(torch.bfloat16).min
+    pack = api.PackedRows(lengths)
+    o, lse = api.packed_attention_fwd(pack, q, k, v, n_q, n_kv, d)
+    assert (lse[:, :n] == -math.inf).all() and o[:n].isnan().all()
+    qh, kh, vh = (x[n:300].double().reshape(300 - n, h, d).transpose(0, 1) for x, h in ((q, n_q), (k, n_kv), (v, n_kv)))
+    kh, vh = kh.repeat_interleave(2, 0), vh.repeat_interleave(2, 0)
+    s = (qh @ kh.transpose(1, 2) * d ** -0.5).masked_fill(torch.ones(300 - n, 300 - n, dtype=torch.bool, device=DEV).triu(1), -math.inf)
+    p = torch.softmax(s, 2)
+    want, mag = ((p @ x).transpose(0, 1).flatten(1) for x in (vh, vh.abs()))
+    within(o[n:300], want, R * want.abs() + (R + F) * mag, "o")
+    within(lse[:, n:300], torch.logsumexp(s, 2), 6e-5 + 2.0 ** -22 * torch.logsumexp(s, 2).abs(), "lse")
+    alone, alone_lse = api.packed_attention_fwd(api.PackedRows([20]), q[300:], k[300:], v[300:], n_q, n_kv, d)
+    assert torch.equal(o[300:320], alone) and torch.equal(lse[:, 300:], alone_lse)
+
+
 def test_other_sequences_and_rows_behind_are_left_alone():
     lengths, n_q, n_kv, d = [200, 77, 130], 4, 2, 128
     q, k, v, do = make(lengths, n_q, n_kv, d, extra_rows=9)
