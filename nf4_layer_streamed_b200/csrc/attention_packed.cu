@@ -415,8 +415,9 @@ __device__ __forceinline__ bool smem_base(uint8_t* raw, uint8_t** base, int* err
 // tiles are copied into TMEM (bf16 pairs, one query row per lane), so that S and dP read only
 // K and V from shared memory: 4 KB per 64 tensor-core cycles instead of 8 KB, which is all
 // that shared memory delivers, while the next tiles land in it.  The K ring also carries an
-// item's O tile (for delta), behind its first K tile, and, behind the last, the place through
-// which its dQ leaves.
+// item's O tile (for delta), before its first K tile (behind it, the last item's products
+// still hold its place when it is wanted), and, behind the last, the place through which its
+// dQ leaves.
 template <int D>
 __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constant__ BwdParams p) {
   constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM;  // swizzle atoms, k-steps and bytes of a tile
@@ -484,8 +485,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   constexpr uint32_t T_S = 0, T_DP = 128, T_DQ = 256, T_Q = 384, T_DO = 448;  // dS packed over dP
   // entries of the K ring before this item, of the V ring (and tiles): c3 + n_kt + 2, c + n_kt
-  // behind it; K tile kt is entry c3 + k_entry(kt)
-  auto k_entry = [](int kt) { return kt == 0 ? 0 : kt + 1; };
+  // behind it; O is entry c3, K tile kt entry c3 + 1 + kt
 
   if (warp == B_PROD) {
     if (lane == 0) {
@@ -516,8 +516,12 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
           tma_load_2d(base + B_OFF_A + TILE_BYTES + j * ATOM, &p.tdo, q_full, col + 64 * j, row);
         }
         n_q = n + 1;
+        int st = ring3();
+        if (st < 0) break;
+        load(&p.to, base + B_OFF_R3 + st * TILE_BYTES, &k_full[st], col, row);
+        ++e3;
         for (int kt = 0; kt < n_kt; ++kt) {
-          int st = ring3();
+          st = ring3();
           if (!(ok = st >= 0)) break;
           load(&p.tk, base + B_OFF_R3 + st * TILE_BYTES, &k_full[st], kvc, pt.row0 + kt * TT);
           ++e3;
@@ -525,15 +529,8 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
           if (e2 >= 2 && !(ok = mbar_wait(&v_empty[sv], ((e2 >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 42))) break;
           load(&p.tv, base + B_OFF_R2 + sv * TILE_BYTES, &v_full[sv], kvc, pt.row0 + kt * TT);
           ++e2;
-          if (kt == 0) {
-            if (!(ok = (st = ring3()) >= 0)) break;
-            load(&p.to, base + B_OFF_R3 + st * TILE_BYTES, &k_full[st], col, row);
-            ++e3;
-          }
         }
-        if (!ok) break;
-        const int st = ring3();  // the place for dQ
-        if (st < 0) break;
+        if (!ok || (st = ring3()) < 0) break;  // the place for dQ
         mbar_arrive(&k_full[st]);
         ++e3;
       }
@@ -580,11 +577,11 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
       const int n_kt = p.tiles[item / p.nq].tile + 1;
       // (the elementwise warps have then read the last item's S; its dP(last) goes first)
       if (!(ok = wait(qa_full, n, 43) && !*abort_flag)) break;
-      if (!(ok = scores(c3) && dprobs(c))) break;
+      if (!(ok = scores(c3 + 1) && dprobs(c))) break;
       for (int i = 0; i < n_kt; ++i) {
-        if (i + 1 < n_kt && !(ok = wait(s_read, c + i, 46) && scores(c3 + k_entry(i + 1)))) break;
+        if (i + 1 < n_kt && !(ok = wait(s_read, c + i, 46) && scores(c3 + i + 2))) break;
         if (!(ok = wait(ds_full, c + i, 47))) break;
-        const int e = c3 + k_entry(i);
+        const int e = c3 + 1 + i;
         const uint32_t sK = s3 + (e % 3) * TILE_BYTES;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)  // 16 keys per step
@@ -647,7 +644,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     for (int n = 0;; ++n) {
       const int qt = pt.tile, n_kt = qt + 1, n_rows = min(TT, pt.len - qt * TT);
       {
-        const int e = c3 + 1;
+        const int e = c3;
         ok = ok && warp_wait(&k_full[e % 3], (e / 3) & 1, abort_flag, p.err, KID_PACKED, 51);
         if (ok && has_dims) {
           const uint8_t* o_row = base + B_OFF_R3 + (e % 3) * TILE_BYTES + atom * ATOM + r * 128;
@@ -692,7 +689,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
         if (diag && n_rows < TT) {
           // rows of K behind the sequence's end: zeros for the product dS K (S is done with them)
           if (r >= n_rows && g == 0)
-            zero_row<NA>(smem_u32(base + B_OFF_R3 + ((c3 + k_entry(kt)) % 3) * TILE_BYTES), r);
+            zero_row<NA>(smem_u32(base + B_OFF_R3 + ((c3 + 1 + kt) % 3) * TILE_BYTES), r);
           fence_proxy_async_smem();
         }
 #pragma unroll
