@@ -380,10 +380,11 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
 // tiles in order; key side: query heads of the group, then query tiles), so results are
 // bit-reproducible.
 
-// warp 0: MMA issuer, warp 1: TMA producer (first, as in the forward); warps 4-19:
+// warp 0: MMA issuer, warp 1: TMA producer (the scheduler prefers its oldest warp: as the last
+// of the block they waited up to 600 cycles for an issue slot), warp 2: stores dQ; warps 4-19:
 // elementwise and epilogue (TMEM lane quarter w % 4, columns 32 (w / 4 - 1) .. of a block;
 // four on each scheduler hide one another's waits where two did not)
-constexpr int B_THREADS = 640, B_MMA = 0, B_PROD = 1, B_FIRST = 4, B_EW = 512;
+constexpr int B_THREADS = 640, B_MMA = 0, B_PROD = 1, B_STORE = 2, B_FIRST = 4, B_EW = 512;
 constexpr int B_OFF_A = 0;                              // Q, dO (query side) or K, V (key side)
 constexpr int B_OFF_R3 = 2 * TILE_BYTES;                // 3 stages: K (query side) or Q (key side)
 constexpr int B_OFF_R2 = B_OFF_R3 + 3 * TILE_BYTES;     // 2 stages: V (query side) or dO (key side)
@@ -438,8 +439,9 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   uint64_t* dp_full = bars + 15;
   uint64_t* ds_full = bars + 16;    // dS is in TMEM (one arrival per elementwise warp)
   uint64_t* acc_full = bars + 17;
-  uint64_t* drain = bars + 18;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
+  uint64_t* out_full = bars + 18;   // dQ is in its place in the K ring (one arrival per elementwise warp)
+  uint64_t* drain = bars + 19;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = warp_number(), lane = threadIdx.x & 31;
@@ -470,6 +472,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     mbar_init(dp_full, 1);
     mbar_init(ds_full, B_EW / 32);
     mbar_init(acc_full, 1);
+    mbar_init(out_full, B_EW / 32);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -594,6 +597,23 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
       c3 += n_kt + 2;
       c += n_kt;
     }
+  } else if (warp == B_STORE) {
+    // dQ to memory by TMA stores, while the other warps are at the next item
+    bool ok = true;
+    int c3 = 0;
+    for (int n = 0, item; ok && (item = item_of(n)) >= 0; ++n) {
+      const PackTile pt = p.tiles[item / p.nq];
+      const int e = c3 + pt.tile + 2;
+      if (!(ok = warp_wait(out_full, n & 1, abort_flag, p.err, KID_PACKED, 56))) break;
+      // nothing is stored once a wait has failed
+      if (!*abort_flag)
+        store_tile<D>(&p.tdq, p.dq, p.ld_dq, smem_u32(base + B_OFF_R3 + (e % 3) * TILE_BYTES), pt.row0 + pt.tile * TT,
+                      item % p.nq * D, min(TT, pt.len - pt.tile * TT), lane, 32);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_empty[e % 3]);
+      __syncwarp();
+      c3 = e + 1;
+    }
   } else if (warp >= B_FIRST) {
     // ------------------------------------------------------------------ elementwise + epilogue
     const int tid = threadIdx.x - B_FIRST * 32;
@@ -643,7 +663,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     to_tmem(0);
     for (int n = 0;; ++n) {
       const int qt = pt.tile, n_kt = qt + 1, n_rows = min(TT, pt.len - qt * TT);
-      {
+      {  // (red: its last readers have since handed over an item's dS)
         const int e = c3;
         ok = ok && warp_wait(&k_full[e % 3], (e / 3) & 1, abort_flag, p.err, KID_PACKED, 51);
         if (ok && has_dims) {
@@ -723,7 +743,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full);
       }
-      const int next = item_of(n + 1), h_now = h, row = pt.row0 + qt * TT;
+      const int next = item_of(n + 1);
       float lse_next = 0.f;
       if (next >= 0) {
         h = next % p.nq;
@@ -743,13 +763,10 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
         stage_row32(out, r, g, v, p.scale);
       }
       fence_proxy_async_smem();
-      bar_ew();
-      // the store is issued only when no wait failed
-      if (!*abort_flag) store_tile<D>(&p.tdq, p.dq, p.ld_dq, out, row, h_now * D, n_rows, tid, B_EW);
-      if (next < 0) break;
-      if (n_rows < TT) bar_ew();  // every thread has read its part of the staged tile
-      if (tid == 0) mbar_arrive(&k_empty[e % 3]);
       __syncwarp();
+      if (lane == 0) mbar_arrive(out_full);
+      __syncwarp();
+      if (next < 0) break;
       lse2 = lse_next;
       c3 += n_kt + 2;
       c += n_kt;
