@@ -98,13 +98,14 @@ __device__ __forceinline__ void store_tile(const CUtensorMap* map, __nv_bfloat16
 // One block per 128-query tile of one head and sequence, two blocks on an SM, online
 // softmax over the key tiles up to the diagonal:
 //   S = Q K^T; p = 2^(S scale log2e - m), the reference maximum m of a row moving only when a
-//   tile's maximum exceeds it by more than 2^8; O += P V, P as bf16 over the scores it came
+//   tile's maximum exceeds it by more than 8, a factor of 2^8; O += P V, P as bf16 over the scores it came
 //   from; o = O / sum p.
 // Within a tile these depend on one another; the second block's products run meanwhile, and
 // the first half of P V under the second half's exponentials.  16.4k rows of 8B heads, the
-// tensor core's work 444 us: 740 us; 2048 rows: 25.8 us.  What bounds it is the hand-over
-// (scores to registers, P back, a wait each way), about 700 cycles of a tile's 1400, which
-// two blocks do not always fill.  Built and measured beside it (long, short): two tiles of
+// tensor core's work 444 us: 740 us; 2048 rows: 25.8 us.  A tile is 1024 cycles of the tensor
+// core and as many of the exponential unit; a block takes 3400 for it, since scores to
+// registers, exponentials, P back and a wait at each hand-over follow one another, and two
+// blocks keep both units 60% busy.  Built and measured beside it (long, short): two tiles of
 // one block taking turns under one issuer, 751 and 31 us; blocks that go through a list of
 // tiles, 801 and 25.6 us (the list's state spills the scores); a row shared by two warps,
 // 854 and 28 us; three of eight exponentials by a cubic on the multiplier instead of the
@@ -372,9 +373,10 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
 // it, and dS(i), which needs dP(i), under the product behind that.  (With columns of its
 // own for dS and dO left in shared memory, dP(i+1) need not wait for dQ(i), but dP then
 // reads both operands from shared memory: 2% slower.)  The key side hands P and dS over in
-// halves, so that the product of the first half runs under the making of the second.  The tiles come
-// through two rings: those that the first and the last product of an item read (K; Q)
-// live longest and have three stages, the others (V; dO) two.
+// halves, so that the product of the first half runs under the making of the second.  The
+// tiles come through two rings: those that the first and the last product of an item read
+// (K; Q) live longest and have three stages, the others (V; dO) two.  12.2k rows of 8B heads,
+// the tensor core's work of both sides 1258 us: 1580 us, 1777 under the power cap.
 // The query side also forms delta = rowsum(dO * O) and writes it beside lse log2e for the
 // key side, which runs after it.  Accumulation runs in a fixed order (query side: key
 // tiles in order; key side: query heads of the group, then query tiles), so results are

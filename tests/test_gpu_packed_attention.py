@@ -139,6 +139,21 @@ def test_gradients_of_many_sequences(heads):
     o1, l1 = api.packed_attention_fwd(pack, q1, k1, v1, n_q, n_kv, d)
     api.packed_attention_bwd(pack, q1, k1, v1, o1, do1, l1, n_q, n_kv, d, out=outs)
     assert torch.equal(buf[rows], g0[rows])
+    # the same bits again, eagerly and from two captured calls in flight at once
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    got = [api.packed_attention_bwd(pack, q, k, v, o, do, lse, n_q, n_kv, d)]
+    for g in graphs:
+        with torch.cuda.graph(g):
+            got.append(api.packed_attention_bwd(pack, q, k, v, o, do, lse, n_q, n_kv, d))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(3):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for grads in got:
+        assert torch.equal(torch.cat(grads, 1), g0[:total])
+    assert api.device_error()[0] == 0
 
 
 @pytest.mark.parametrize("factor", [0.01, 30.0])
