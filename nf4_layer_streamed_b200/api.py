@@ -444,14 +444,15 @@ def _elsewhere(device, stream, *tensors):
     call allocates then belongs to that stream), else None."""
     if device.type != "cuda":
         raise ValueError(f"tensors on {device}: must be CUDA tensors")
+    index = device.index
     for t in tensors:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:  # -1: on the host
             raise ValueError(f"a tensor on {t.device}, the call is on {device}")
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"stream: on {stream.device}, the call is on {device}")
         return torch.cuda.stream(stream)
-    return None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+    return None if index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _rows_like(t: torch.Tensor, rows: int) -> torch.Tensor:
@@ -495,7 +496,7 @@ def packed_attention_fwd(pack: PackedRows, q, k, v, n_q: int, n_kv: int, head_di
             return packed_attention_fwd(pack, q, k, v, n_q, n_kv, head_dim, scale, out)
     if out is None:
         out, ld_o = _rows_like(q, rows), qd
-    lse = q.new_empty((n_q, rows), dtype=torch.float32)
+    lse = torch.empty_strided((n_q, rows), (rows, 1), dtype=torch.float32, device=dev)
     if rows:
         B.call("nf4ls_packed_attention_fwd", pack._ref, heads,
                _ATTENTION.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), 0, 0, 0, 0,
@@ -531,7 +532,7 @@ def packed_attention_bwd(pack: PackedRows, q, k, v, o, do, lse, n_q: int, n_kv: 
         dv, ld_dv = _rows_like(v, rows), kvd
     if rows:
         nb = B.lib().nf4ls_packed_attention_ws_bytes(pack._ref, heads)
-        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        ws = torch.empty_strided((nb,), (1,), dtype=torch.uint8, device=dev)
         B.call("nf4ls_packed_attention_bwd", pack._ref, heads,
                _ATTENTION.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(),
                                dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ld_q, ld_k, ld_v, ld_o, ld_do, ld_dq,
