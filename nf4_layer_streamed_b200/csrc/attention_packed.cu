@@ -149,6 +149,9 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
   // by the producer: the MMA warp goes straight to the allocation, which takes a whole,
   // converged warp (beside a branch of its own first lane it faulted)
   if (warp == F_PROD && lane == 0) {
+    tma_prefetch_desc(&p.tq);
+    tma_prefetch_desc(&p.tk);
+    tma_prefetch_desc(&p.tv);
     mbar_init(q_full, 1);
     mbar_init(k_full, 1);
     mbar_init(k_empty, 1);
@@ -175,9 +178,6 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
   if (warp == F_PROD) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      tma_prefetch_desc(&p.tq);
-      tma_prefetch_desc(&p.tk);
-      tma_prefetch_desc(&p.tv);
       mbar_arrive_expect_tx(q_full, TB);
       for (int j = 0; j < NA; ++j) tma_load_2d(base + F_OFF_Q + j * ATOM, &p.tq, q_full, h * D + 64 * j, row0 + qt * TT);
       int issued_k = 0, issued_v = 0;
@@ -458,6 +458,11 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   // by the producer: the MMA warp goes straight to the allocation, which takes a whole,
   // converged warp (beside a branch of its own first lane it faulted)
   if (warp == B_PROD && lane == 0) {
+    tma_prefetch_desc(&p.tq);
+    tma_prefetch_desc(&p.tk);
+    tma_prefetch_desc(&p.tv);
+    tma_prefetch_desc(&p.tdo);
+    tma_prefetch_desc(&p.to);
     mbar_init(q_full, 1);
     mbar_init(q_read, 1);
     mbar_init(qa_full, B_EW / 32);
@@ -494,11 +499,6 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
 
   if (warp == B_PROD) {
     if (lane == 0) {
-      tma_prefetch_desc(&p.tq);
-      tma_prefetch_desc(&p.tk);
-      tma_prefetch_desc(&p.tv);
-      tma_prefetch_desc(&p.tdo);
-      tma_prefetch_desc(&p.to);
       int n_q = 0, e3 = 0, e2 = 0;  // issued: items' Q and dO, entries of the rings
       // the next entry of the K ring is free: its stage, or -1
       auto ring3 = [&]() -> int {
@@ -829,6 +829,10 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dkv(const __grid_consta
   // by the producer: the MMA warp goes straight to the allocation, which takes a whole,
   // converged warp (beside a branch of its own first lane it faulted)
   if (warp == B_PROD && lane == 0) {
+    tma_prefetch_desc(&p.tq);
+    tma_prefetch_desc(&p.tk);
+    tma_prefetch_desc(&p.tv);
+    tma_prefetch_desc(&p.tdo);
     mbar_init(kv_full, 1);
     for (int i = 0; i < 3; ++i) {
       mbar_init(&q_full[i], 1);
@@ -863,10 +867,6 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dkv(const __grid_consta
 
   if (warp == B_PROD) {
     if (lane == 0) {
-      tma_prefetch_desc(&p.tq);
-      tma_prefetch_desc(&p.tk);
-      tma_prefetch_desc(&p.tv);
-      tma_prefetch_desc(&p.tdo);
       mbar_arrive_expect_tx(kv_full, 2 * TB);
       for (int j = 0; j < NA; ++j) {
         tma_load_2d(base + B_OFF_A + j * ATOM, &p.tk, kv_full, kvh * D + 64 * j, row0 + kt * TT);
@@ -882,10 +882,10 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dkv(const __grid_consta
           tma_load_2d(base + B_OFF_R3 + s3 * TILE_BYTES + j * ATOM, &p.tq, &q_full[s3], h * D + 64 * j, row0 + qt * TT);
         issued_q = i + 1;
         if (i >= 2 && !mbar_wait(&do_empty[s2], ((i >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 32)) break;
-        if (i == 0) wait_for_previous();  // the query side's statistics
         mbar_arrive_expect_tx(&do_full[s2], TB + 1024);
         for (int j = 0; j < NA; ++j)
           tma_load_2d(base + B_OFF_R2 + s2 * TILE_BYTES + j * ATOM, &p.tdo, &do_full[s2], h * D + 64 * j, row0 + qt * TT);
+        if (i == 0) wait_for_previous();  // the query side's statistics
         bulk_load(base + B_OFF_X + s2 * 1024, p.stats + ((size_t)h * p.n_tiles + pt.index - kt + qt) * (2 * TT), 1024,
                   &do_full[s2]);
         issued_do = i + 1;
