@@ -501,7 +501,7 @@ extern "C" int nf4ls_policy_loss(const nf4ls_policy_cfg* c, int32_t rows, const 
         NF4_CUDA_TRY(cudaFuncSetAttribute(k_policy<T, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, KEEP * 16));
         if (dev < 64) configured[dev] = 1;
       }
-      NF4_CUDA_TRY(launch_kernel(k_policy<T, KEEP>, rows, {T, p.dlogits ? KEEP * 16 : 0, false, 1}, s, p));
+      NF4_CUDA_TRY(launch_kernel(k_policy<T, KEEP>, rows, {T, p.dlogits ? (size_t)KEEP * 16 : 0, false, 1}, s, p));
       note_launch();
     }
   }

@@ -23,15 +23,24 @@ struct FwdParams {
 };
 
 struct BwdParams {
-  CUtensorMap tq, tk, tv, tdo, to;  // inputs (to: the output O of the forward)
+  CUtensorMap tq, tk, tv, tdo;  // inputs
   CUtensorMap tdq, tdk, tdv;        // the gradients, same boxes (TMA stores)
-  const PackTile* tiles;            // query tiles or key tiles, most work first
-  const float* lse;
-  float* stats;  // [nq, n_tiles, 2, 128]: -lse log2(e) and -delta, by the query side for the key side
+  const PackTile *query_tiles, *key_tiles;  // most work first
+  float* stats;    // [nq, n_tiles, 2, 128]: -lse log2(e) and -delta
+  unsigned* next;  // query side: items handed out beyond each block's first
   __nv_bfloat16 *dq, *dk, *dv;
   int ld_dq, ld_dk, ld_dv, total, n_tiles, nq, nkv;
   float scale, scale_log2;
   int* err;
+};
+
+struct StatsParams {
+  const PackTile* tiles;
+  const __nv_bfloat16 *o, *d_o;  // the forward's output and its gradient
+  const float* lse;
+  float* stats;    // as above
+  unsigned* next;  // set to 0
+  int ld_o, ld_do, total, n_tiles, nq;
 };
 
 // Zeros row r of a tile of NA 64-dim atoms (a whole row is the same under any swizzle).
@@ -376,11 +385,10 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
 // halves, so that the product of the first half runs under the making of the second.  The
 // tiles come through two rings: those that the first and the last product of an item read
 // (K; Q) live longest and have three stages, the others (V; dO) two.  12.2k rows of 8B heads,
-// the tensor core's work of both sides 1258 us: 1580 us, 1777 under the power cap.
-// The query side also forms delta = rowsum(dO * O) and writes it beside lse log2e for the
-// key side, which runs after it.  Accumulation runs in a fixed order (query side: key
-// tiles in order; key side: query heads of the group, then query tiles), so results are
-// bit-reproducible.
+// the tensor core's work of both sides 1258 us: 1600 us, 1820 under the power cap.
+// A small kernel before them forms delta = rowsum(dO * O) and puts it beside lse log2e.
+// Accumulation runs in a fixed order (query side: key tiles in order; key side: query heads of
+// the group, then query tiles), so results are bit-reproducible.
 
 // warp 0: MMA issuer, warp 1: TMA producer (the scheduler prefers its oldest warp: as the last
 // of the block they waited up to 600 cycles for an issue slot), warp 2: stores dQ; warps 4-19:
@@ -411,26 +419,61 @@ __device__ __forceinline__ bool smem_base(uint8_t* raw, uint8_t** base, int* err
   return false;
 }
 
-// QUERY side: dQ of query tiles of one head each ("items"), a block an SM that goes through its
-// share of them: the next one's tiles land and its first products run under the end of this
-// one.  (A block for each, whose first products waited 5 k cycles for 160 KB of tiles: both
-// kernels 81 instead of 72 us for 2048 rows, 1839 instead of 1777 for 12.2k.)  The Q and dO
-// tiles are copied into TMEM (bf16 pairs, one query row per lane), so that S and dP read only
-// K and V from shared memory: 4 KB per 64 tensor-core cycles instead of 8 KB, which is all
-// that shared memory delivers, while the next tiles land in it.  The K ring also carries an
-// item's O tile (for delta), before its first K tile (behind it, the last item's products
-// still hold its place when it is wanted), and, behind the last, the place through which its
-// dQ leaves.
+// STATISTICS of the query rows for both sides: delta = rowsum(dO * O), and lse log2(e) beside
+// it, a block per query tile and head.  Bound by memory (2048 rows of 8B heads: 34 MB).
+// With them the two sides need nothing of one another and share the GPU; when the query side
+// formed them, the key side stood behind it (2048 rows 70 us, 63 so).
 template <int D>
-__global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(256, 5) k_packed_stats(const StatsParams p) {
+  constexpr int L = D / 8, STEP = 256 / L, N = TT / STEP;  // lanes of a row; rows at a time; rows of a thread
+  next_may_start();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.next = 0;
+  const PackTile pt = p.tiles[blockIdx.x];
+  const int li = threadIdx.x % L, r0 = threadIdx.x / L, h = blockIdx.y, n_rows = min(TT, pt.len - pt.tile * TT);
+  const size_t row0 = (size_t)pt.row0 + pt.tile * TT;
+  float* st = p.stats + ((size_t)h * p.n_tiles + pt.index) * (2 * TT);
+  uint4 a[N], d[N];  // all loads of a thread are in flight together
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int r = r0 + k * STEP;
+    const bool there = r < n_rows;
+    a[k] = there ? __ldg(reinterpret_cast<const uint4*>(p.o + (row0 + r) * p.ld_o + h * D) + li) : make_uint4(0u, 0u, 0u, 0u);
+    d[k] = there ? __ldg(reinterpret_cast<const uint4*>(p.d_o + (row0 + r) * p.ld_do + h * D) + li) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int r = r0 + k * STEP;
+    const uint32_t aw[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, dw[4] = {d[k].x, d[k].y, d[k].z, d[k].w};
+    float v = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v += bf16_lo(aw[j]) * bf16_lo(dw[j]) + bf16_hi(aw[j]) * bf16_hi(dw[j]);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (li == 0 && r < n_rows) {
+      st[r] = -p.lse[(size_t)h * p.total + row0 + r] * 1.4426950408889634f;
+      st[TT + r] = -v;
+    }
+  }
+}
+
+// QUERY side: dQ of query tiles of one head each ("items").  A block takes an item as it comes
+// to the end of its last one, most work first, so that the blocks that start late (behind key
+// tiles) do less, and the next one's tiles land and its first products run under the end of
+// this one.  (A block for each, whose first products wait 5 k cycles for its tiles, cost 13% of
+// both sides' time for 2048 rows, 3% for 12.2k.)
+// The Q and dO tiles are copied into TMEM (bf16 pairs, one query row per lane), so that S and
+// dP read only K and V from shared memory: 4 KB per 64 tensor-core cycles instead of 8 KB,
+// which is all that shared memory delivers, while the next tiles land in it.  The K ring's
+// last entry of an item is the place through which its dQ leaves.
+template <int D>
+__device__ __forceinline__ void query_side(const BwdParams& p, int block, int blocks) {
   constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM;  // swizzle atoms, k-steps and bytes of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base;
-  next_may_start();  // the key side's blocks, on the SMs that the last of these leave free
   if (!smem_base(smem_raw, &base, p.err)) return;
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + B_OFF_BAR);
   uint64_t* q_full = bars;          // Q, dO
-  uint64_t* q_read = bars + 1;      // ... and they are in TMEM, and in delta
+  uint64_t* q_read = bars + 1;      // ... and they have been read (one arrival per elementwise warp)
   uint64_t* qa_full = bars + 2;     // Q and dO are in TMEM (one arrival per elementwise warp)
   uint64_t* k_full = bars + 3;      // 3
   uint64_t* k_empty = bars + 6;     // 3
@@ -443,16 +486,22 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   uint64_t* acc_full = bars + 17;
   uint64_t* out_full = bars + 18;   // dQ is in its place in the K ring (one arrival per elementwise warp)
   uint64_t* drain = bars + 19;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
+  uint64_t* item_full = bars + 20;  // 2: this block's next item is known
+  uint64_t* item_empty = bars + 22; // 2: every warp has it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = warp_number(), lane = threadIdx.x & 31;
-  // Item number n of this block: heads fastest, then the plan's tiles, most key tiles first;
-  // every second round of blocks goes backwards, so that long items meet short ones.
-  const int n_items = p.n_tiles * p.nq, G = gridDim.x;
-  auto item_of = [&](int n) -> int {
-    const int64_t at = (int64_t)n * G + ((n & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
-    return at < n_items ? (int)at : -1;  // only the last round has fewer items than blocks
+  volatile int* items = reinterpret_cast<volatile int*>(base + B_OFF_X);  // 2
+  // Item number n of this block, by a whole warp, once for each n: heads fastest, then the
+  // plan's tiles, most key tiles first; -1: no more (or a wait failed).
+  auto take = [&](int n) -> int {
+    if (!warp_wait(&item_full[n & 1], (n >> 1) & 1, abort_flag, p.err, KID_PACKED, 57)) return -1;
+    const int item = items[n & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[n & 1]);
+    __syncwarp();
+    return item;
   };
 
   // by the producer: the MMA warp goes straight to the allocation, which takes a whole,
@@ -462,9 +511,8 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     tma_prefetch_desc(&p.tk);
     tma_prefetch_desc(&p.tv);
     tma_prefetch_desc(&p.tdo);
-    tma_prefetch_desc(&p.to);
     mbar_init(q_full, 1);
-    mbar_init(q_read, 1);
+    mbar_init(q_read, B_EW / 32);
     mbar_init(qa_full, B_EW / 32);
     for (int i = 0; i < 3; ++i) {
       mbar_init(&k_full[i], 1);
@@ -473,6 +521,8 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     for (int i = 0; i < 2; ++i) {
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], B_EW / 32 + 2);  // and the MMA and the storing warp
     }
     mbar_init(s_full, 1);
     mbar_init(s_read, B_EW / 32);
@@ -494,8 +544,8 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   constexpr uint32_t T_S = 0, T_DP = 128, T_DQ = 256, T_Q = 384, T_DO = 448;  // dS packed over dP
-  // entries of the K ring before this item, of the V ring (and tiles): c3 + n_kt + 2, c + n_kt
-  // behind it; O is entry c3, K tile kt entry c3 + 1 + kt
+  // c: key tiles (entries of the V ring) before an item; c3: entries of the K ring, which has
+  // one more an item, the place for its dQ
 
   if (warp == B_PROD) {
     if (lane == 0) {
@@ -509,10 +559,18 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
         mbar_arrive_expect_tx(full, TB);
         for (int j = 0; j < NA; ++j) tma_load_2d(to + j * ATOM, map, full, col + 64 * j, row);
       };
+      const int n_items = p.n_tiles * p.nq;
       bool ok = true;
-      for (int n = 0, item; ok && (item = item_of(n)) >= 0; ++n) {
+      for (int n = 0;; ++n) {
+        if (n >= 2 && !mbar_wait(&item_empty[n & 1], ((n >> 1) - 1) & 1, abort_flag, p.err, KID_PACKED, 58)) break;
+        if (n == 1) wait_for_previous();  // the counter
+        const unsigned more = n == 0 ? block : blocks + atomicAdd(p.next, 1u);
+        const int item = more < (unsigned)n_items ? (int)more : -1;
+        items[n & 1] = item;
+        mbar_arrive(&item_full[n & 1]);
+        if (item < 0) break;
         const int h = item % p.nq, col = h * D, kvc = h / (p.nq / p.nkv) * D;
-        const PackTile pt = p.tiles[item / p.nq];
+        const PackTile pt = p.query_tiles[item / p.nq];
         const int row = pt.row0 + pt.tile * TT, n_kt = pt.tile + 1;
         if (n > 0 && !mbar_wait(q_read, (n - 1) & 1, abort_flag, p.err, KID_PACKED, 40)) break;
         mbar_arrive_expect_tx(q_full, 2 * TB);
@@ -521,10 +579,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
           tma_load_2d(base + B_OFF_A + TILE_BYTES + j * ATOM, &p.tdo, q_full, col + 64 * j, row);
         }
         n_q = n + 1;
-        int st = ring3();
-        if (st < 0) break;
-        load(&p.to, base + B_OFF_R3 + st * TILE_BYTES, &k_full[st], col, row);
-        ++e3;
+        int st = 0;
         for (int kt = 0; kt < n_kt; ++kt) {
           st = ring3();
           if (!(ok = st >= 0)) break;
@@ -578,15 +633,15 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     };
     bool ok = true;
     int c3 = 0, c = 0;
-    for (int n = 0, item; ok && (item = item_of(n)) >= 0; ++n) {
-      const int n_kt = p.tiles[item / p.nq].tile + 1;
+    for (int n = 0, item; ok && (item = take(n)) >= 0; ++n) {
+      const int n_kt = p.query_tiles[item / p.nq].tile + 1;
       // (the elementwise warps have then read the last item's S; its dP(last) goes first)
       if (!(ok = wait(qa_full, n, 43) && !*abort_flag)) break;
-      if (!(ok = scores(c3 + 1) && dprobs(c))) break;
+      if (!(ok = scores(c3) && dprobs(c))) break;
       for (int i = 0; i < n_kt; ++i) {
-        if (i + 1 < n_kt && !(ok = wait(s_read, c + i, 46) && scores(c3 + i + 2))) break;
+        if (i + 1 < n_kt && !(ok = wait(s_read, c + i, 46) && scores(c3 + i + 1))) break;
         if (!(ok = wait(ds_full, c + i, 47))) break;
-        const int e = c3 + 1 + i;
+        const int e = c3 + i;
         const uint32_t sK = s3 + (e % 3) * TILE_BYTES;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)  // 16 keys per step
@@ -596,16 +651,16 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
         if (i + 1 < n_kt && !(ok = dprobs(c + i + 1))) break;
       }
       if (ok) commit_by(el, acc_full);
-      c3 += n_kt + 2;
+      c3 += n_kt + 1;
       c += n_kt;
     }
   } else if (warp == B_STORE) {
     // dQ to memory by TMA stores, while the other warps are at the next item
     bool ok = true;
     int c3 = 0;
-    for (int n = 0, item; ok && (item = item_of(n)) >= 0; ++n) {
-      const PackTile pt = p.tiles[item / p.nq];
-      const int e = c3 + pt.tile + 2;
+    for (int n = 0, item; ok && (item = take(n)) >= 0; ++n) {
+      const PackTile pt = p.query_tiles[item / p.nq];
+      const int e = c3 + pt.tile + 1;
       if (!(ok = warp_wait(out_full, n & 1, abort_flag, p.err, KID_PACKED, 56))) break;
       // nothing is stored once a wait has failed
       if (!*abort_flag)
@@ -618,19 +673,16 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
     }
   } else if (warp >= B_FIRST) {
     // ------------------------------------------------------------------ elementwise + epilogue
-    const int tid = threadIdx.x - B_FIRST * 32;
     const int wq = warp & 3, g = (warp - B_FIRST) >> 2;
     const int r = wq * 32 + lane;  // query row = TMEM lane
     const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
-    // First Q and dO into TMEM (the MMA warp starts on them), then delta = rowsum(dO * O);
-    // group g < D / 32 takes dims 32 g .. of its row: 16-byte chunks c0 .. c0 + 3 of swizzle
-    // atom g / 2 of the tiles, TMEM columns 16 g ..; the parts of delta are added through smem
-    float* red = reinterpret_cast<float*>(base + B_OFF_X);
+    // An item begins with Q and dO into TMEM (the MMA warp starts on them): group g < D / 32
+    // takes dims 32 g .. of its row, 16-byte chunks c0 .. c0 + 3 of swizzle atom g / 2 of the
+    // tiles, to TMEM columns 16 g ..
     const bool has_dims = g < D / 32;
     const int atom = g >> 1, c0 = (g & 1) * 4;
     const uint8_t* q_row = base + B_OFF_A + atom * ATOM + r * 128;
     const uint8_t* dO_row = base + B_OFF_A + TILE_BYTES + atom * ATOM + r * 128;
-    // A failed wait leaves no item's loop: the other warps would wait at a meeting for good.
     bool ok = true;
     auto to_tmem = [&](int n) {
       ok = ok && warp_wait(q_full, n & 1, abort_flag, p.err, KID_PACKED, 50);
@@ -649,55 +701,31 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(qa_full);  // also on failure: the MMA warp then sees the abort
+      if (lane == 0) {
+        mbar_arrive(q_read);
+        mbar_arrive(qa_full);  // also on failure: the MMA warp then sees the abort
+      }
       __syncwarp();
     };
-    // rows behind the sequence's end: no lse to read; their lanes compute values that
-    // nothing stores
-    auto lse_of = [&](int h, const PackTile& pt) -> float {
-      const int at = pt.tile * TT + r;
-      return at < pt.len ? p.lse[(size_t)h * p.total + pt.row0 + at] * 1.4426950408889634f : 0.f;
+    // (rows behind the sequence's end have no statistics: their lanes compute values that
+    // nothing stores)
+    auto stats_of = [&](int item, const PackTile& pt) -> float2 {
+      const float* st = p.stats + ((size_t)(item % p.nq) * p.n_tiles + pt.index) * (2 * TT);
+      return make_float2(__ldcg(st + r), __ldcg(st + TT + r));  // written while this block may have run
     };
     const uint64_t sl2 = pack2(p.scale_log2, p.scale_log2);
-    int item = item_of(0), h = item % p.nq, c3 = 0, c = 0;
-    PackTile pt = p.tiles[item / p.nq];
-    float lse2 = lse_of(h, pt);
-    to_tmem(0);
-    for (int n = 0;; ++n) {
+    int item = take(0), c3 = 0, c = 0;
+    PackTile pt = {};
+    float2 stat = {};
+    if (item >= 0) {
+      pt = p.query_tiles[item / p.nq];
+      to_tmem(0);
+      wait_for_previous();  // the statistics
+      stat = stats_of(item, pt);
+    }
+    for (int n = 0; item >= 0; ++n) {
       const int qt = pt.tile, n_kt = qt + 1, n_rows = min(TT, pt.len - qt * TT);
-      {  // (red: its last readers have since handed over an item's dS)
-        const int e = c3;
-        ok = ok && warp_wait(&k_full[e % 3], (e / 3) & 1, abort_flag, p.err, KID_PACKED, 51);
-        if (ok && has_dims) {
-          const uint8_t* o_row = base + B_OFF_R3 + (e % 3) * TILE_BYTES + atom * ATOM + r * 128;
-          float s = 0.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t off = (uint32_t)(((c0 + c) ^ (r & 7)) << 4);
-            const uint4 a = *reinterpret_cast<const uint4*>(o_row + off);
-            const uint4 d = *reinterpret_cast<const uint4*>(dO_row + off);
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, dw[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s += bf16_lo(aw[j]) * bf16_lo(dw[j]) + bf16_hi(aw[j]) * bf16_hi(dw[j]);
-          }
-          red[g * 128 + r] = s;
-        }
-        bar_ew();
-        if (tid == 0) {
-          mbar_arrive(q_read);
-          mbar_arrive(&k_empty[e % 3]);
-        }
-        __syncwarp();
-      }
-      float dl = 0.f;
-      if (ok)
-        for (int i = 0; i < D / 32; ++i) dl += red[i * 128 + r];
-      if (ok && g == 0) {
-        float* st = p.stats + ((size_t)h * p.n_tiles + pt.index) * (2 * TT);
-        st[r] = -lse2;
-        st[TT + r] = -dl;
-      }
-      const uint64_t nlse2 = pack2(-lse2, -lse2), ndl2 = pack2(-dl, -dl);
+      const uint64_t nlse2 = pack2(stat.x, stat.x), ndl2 = pack2(stat.y, stat.y);
       for (int kt = 0; ok && kt < n_kt; ++kt) {
         const bool diag = kt == qt;
         if (!(ok = warp_wait(s_full, (c + kt) & 1, abort_flag, p.err, KID_PACKED, 52))) break;
@@ -711,7 +739,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
         if (diag && n_rows < TT) {
           // rows of K behind the sequence's end: zeros for the product dS K (S is done with them)
           if (r >= n_rows && g == 0)
-            zero_row<NA>(smem_u32(base + B_OFF_R3 + ((c3 + 1 + kt) % 3) * TILE_BYTES), r);
+            zero_row<NA>(smem_u32(base + B_OFF_R3 + ((c3 + kt) % 3) * TILE_BYTES), r);
           fence_proxy_async_smem();
         }
 #pragma unroll
@@ -745,17 +773,15 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full);
       }
-      const int next = item_of(n + 1);
-      float lse_next = 0.f;
-      if (next >= 0) {
-        h = next % p.nq;
-        pt = p.tiles[next / p.nq];
-        lse_next = lse_of(h, pt);
+      item = take(n + 1);
+      if (item >= 0) {
+        pt = p.query_tiles[item / p.nq];
+        stat = stats_of(item, pt);
       }
       ok = ok && warp_wait(acc_full, n & 1, abort_flag, p.err, KID_PACKED, 54);
       tc_fence_after();
-      if (next >= 0) to_tmem(n + 1);  // the next item's first products run under this one's end
-      const int e = c3 + n_kt + 1;
+      if (item >= 0) to_tmem(n + 1);  // the next item's first products run under this one's end
+      const int e = c3 + n_kt;
       const uint32_t out = smem_u32(base + B_OFF_R3 + (e % 3) * TILE_BYTES);
       ok = ok && warp_wait(&k_full[e % 3], (e / 3) & 1, abort_flag, p.err, KID_PACKED, 55);
       if (ok && has_dims) {
@@ -768,9 +794,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
       __syncwarp();
       if (lane == 0) mbar_arrive(out_full);
       __syncwarp();
-      if (next < 0) break;
-      lse2 = lse_next;
-      c3 += n_kt + 2;
+      c3 += n_kt + 1;
       c += n_kt;
     }
   }
@@ -793,7 +817,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dq(const __grid_constan
 // shared memory and sends them in one bulk copy into the peer's, and adds the peer's to its
 // own in the order first CTA + second CTA.
 template <int D, bool SPLIT>
-__global__ void __launch_bounds__(B_THREADS, 1) k_packed_dkv(const __grid_constant__ BwdParams p) {
+__device__ __forceinline__ void key_side(const BwdParams& p, int block) {
   constexpr int NA = D / 64, KS = D / 16, TB = NA * ATOM;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base;
@@ -815,8 +839,8 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dkv(const __grid_consta
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = warp_number(), lane = threadIdx.x & 31;
-  const int item = SPLIT ? blockIdx.x >> 1 : blockIdx.x, kvh = item % p.nkv;
-  const PackTile pt = p.tiles[item / p.nkv];
+  const int item = SPLIT ? block >> 1 : block, kvh = item % p.nkv;
+  const PackTile pt = p.key_tiles[item / p.nkv];
   const int kt = pt.tile, row0 = pt.row0;
   const int n_keys = min(TT, pt.len - kt * TT);
   const uint32_t crank = SPLIT ? cluster_ctarank() : 0;
@@ -885,12 +909,11 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dkv(const __grid_consta
         mbar_arrive_expect_tx(&do_full[s2], TB + 1024);
         for (int j = 0; j < NA; ++j)
           tma_load_2d(base + B_OFF_R2 + s2 * TILE_BYTES + j * ATOM, &p.tdo, &do_full[s2], h * D + 64 * j, row0 + qt * TT);
-        if (i == 0) wait_for_previous();  // the query side's statistics
+        if (i == 0) wait_for_previous();  // the statistics
         bulk_load(base + B_OFF_X + s2 * 1024, p.stats + ((size_t)h * p.n_tiles + pt.index - kt + qt) * (2 * TT), 1024,
                   &do_full[s2]);
         issued_do = i + 1;
       }
-      if (n_st == 0) wait_for_previous();  // no block ends before the query side has
       if (*abort_flag) {  // let the copies already issued land before the CTA exits
         mbar_wait_drain(kv_full, 0);
         for (int i = max(0, issued_q - 3); i < issued_q; ++i) mbar_wait_drain(&q_full[i % 3], (i / 3) & 1);
@@ -1148,6 +1171,18 @@ __global__ void __launch_bounds__(B_THREADS, 1) k_packed_dkv(const __grid_consta
   }
 }
 
+// Both sides in one launch: the key side's blocks, whose items are the longest, then the query
+// side's on the SMs that they leave free.  (In launches of their own, the second begun early,
+// the same for 2048 rows; 256 rows 3 us more of the GPU's and 2 of the host's time.)
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(B_THREADS, 1) k_packed_bwd(const __grid_constant__ BwdParams p) {
+  const int n_key = p.n_tiles * p.nkv * (SPLIT ? 2 : 1);
+  if ((int)blockIdx.x < n_key)
+    key_side<D, SPLIT>(p, blockIdx.x);
+  else
+    query_side<D>(p, blockIdx.x - n_key, gridDim.x - n_key);
+}
+
 template <typename K>
 int allow_smem(K kernel, int bytes, int (&configured)[64]) {
   int dev = 0;
@@ -1169,46 +1204,43 @@ int launch_fwd(const FwdParams& p, int n_tiles, cudaStream_t s) {
   return NF4LS_OK;
 }
 
-// Two CTAs for a key tile, or one?  Halves of an item (2.7 k cycles): a CTA takes 2 each and 5
-// of its own, or 8 with the exchange of a pair.  All at once the longest counts; else the sum
-// over the SMs, with half a CTA left over at the end.  8 kv heads of 4 query heads, one CTA
-// against two: 2048 rows in one sequence 152 and 118 us, in four 63 and 66, in eight 48 and
-// 56; one of 512 rows 38 and 29.
-bool split_heads(const nf4ls_pack* pack, int nkv, int group, int sms) {
+// Two CTAs for a key tile, or one?  In tenths of an item of the key side (2.7 k cycles): a CTA
+// takes 10 each and 25 of its own, or 40 with the exchange of a pair; the query side, which
+// fills the SMs that the key side leaves, 9 a key tile and 11 an item.  What counts is the
+// longest CTA, with a little to spare, or the sum over the SMs.  8 kv heads of 4 query heads,
+// one CTA against two: 2048 rows in one sequence 117 and 113 us, in four 49 and 57, in eight 38
+// and 48; one of 512 rows 31 and 22.
+bool split_heads(const nf4ls_pack* pack, int nq, int nkv, int sms) {
+  const int group = nq / nkv;
   if (group == 1) return false;
-  auto halves = [&](int heads, int64_t ctas, int own) -> int64_t {
-    const int64_t longest = 2ll * heads * ((pack->max_len + TT - 1) / TT) + own;
-    if (ctas <= sms) return longest;
-    const int64_t sum = 2 * pack->n_blocks * nkv * group + ctas * own;
-    return std::max(longest, sum / sms + sum / ctas / 2);
+  const int64_t blocks = pack->n_blocks * nq, tiles = (int64_t)pack->n_tiles * nkv;
+  auto time = [&](int heads, int64_t ctas, int own) -> int64_t {
+    const int64_t longest = 10ll * heads * ((pack->max_len + TT - 1) / TT) + own;
+    return std::max<int64_t>(longest * 17 / 16, (10 * blocks + ctas * own + 9 * blocks + 11ll * pack->n_tiles * nq) / sms);
   };
-  const int64_t tiles = (int64_t)pack->n_tiles * nkv;
-  return halves((group + 1) / 2, 2 * tiles, 8) < halves(group, tiles, 5);
+  return time((group + 1) / 2, 2 * tiles, 40) < time(group, tiles, 25);
+}
+
+template <int D, bool SPLIT>
+int launch_sides(const BwdParams& p, int sms, cudaStream_t s) {
+  static int configured[64] = {0};
+  NF4_TRY(allow_smem(k_packed_bwd<D, SPLIT>, SMEM_BWD, configured));
+  int64_t blocks = (int64_t)p.n_tiles * p.nkv * (SPLIT ? 2 : 1) + std::min<int64_t>((int64_t)p.n_tiles * p.nq, sms);
+  if (SPLIT) blocks += blocks & 1;  // a query side's block may have nothing to do
+  NF4_CUDA_TRY(launch_kernel(k_packed_bwd<D, SPLIT>, blocks, {B_THREADS, SMEM_BWD, true, SPLIT ? 2 : 1}, s, p));
+  note_launch();
+  return NF4LS_OK;
 }
 
 template <int D>
-int launch_bwd(BwdParams& p, const nf4ls_pack* pack, const PackTile* query_tiles, const PackTile* key_tiles, cudaStream_t s) {
-  static int conf_q[64] = {0}, conf_k[2][64] = {{0}};
-  NF4_TRY(allow_smem(k_packed_dq<D>, SMEM_BWD, conf_q));
+int launch_bwd(const BwdParams& p, const StatsParams& st, const nf4ls_pack* pack, cudaStream_t s) {
   int dev = 0, sms = 0;
   NF4_CUDA_TRY(cudaGetDevice(&dev));
   NF4_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  // the query side writes the statistics that the key side reads
-  p.tiles = query_tiles;
-  k_packed_dq<D><<<std::min(p.n_tiles * p.nq, sms), B_THREADS, SMEM_BWD, s>>>(p);
+  // the statistics; the second launch may begin while they are formed, and waits for them
+  NF4_CUDA_TRY(launch_kernel(k_packed_stats<D>, dim3((unsigned)p.n_tiles, (unsigned)p.nq), {256, 0, false, 1}, s, st));
   note_launch();
-  NF4_CUDA_TRY(cudaGetLastError());
-  p.tiles = key_tiles;
-  const int64_t tiles = (int64_t)p.n_tiles * p.nkv;
-  if (split_heads(pack, p.nkv, p.nq / p.nkv, sms)) {
-    NF4_TRY(allow_smem(k_packed_dkv<D, true>, SMEM_BWD, conf_k[1]));
-    NF4_CUDA_TRY(launch_kernel(k_packed_dkv<D, true>, tiles * 2, {B_THREADS, SMEM_BWD, true, 2}, s, p));
-  } else {
-    NF4_TRY(allow_smem(k_packed_dkv<D, false>, SMEM_BWD, conf_k[0]));
-    NF4_CUDA_TRY(launch_kernel(k_packed_dkv<D, false>, tiles, {B_THREADS, SMEM_BWD, true, 1}, s, p));
-  }
-  note_launch();
-  return NF4LS_OK;
+  return split_heads(pack, p.nq, p.nkv, sms) ? launch_sides<D, true>(p, sms, s) : launch_sides<D, false>(p, sms, s);
 }
 
 int check_heads(const nf4ls_pack* pack, const nf4ls_packed_heads* h, const char* who) {
@@ -1244,7 +1276,7 @@ using namespace nf4ls;
 
 extern "C" size_t nf4ls_packed_attention_ws_bytes(const nf4ls_pack* pack, const nf4ls_packed_heads* heads) {
   if (!pack || !heads || pack->n_tiles < 0 || heads->n_q < 1) return 0;
-  return (size_t)heads->n_q * pack->n_tiles * 2 * TT * sizeof(float);
+  return (size_t)heads->n_q * pack->n_tiles * 2 * TT * sizeof(float) + 256;  // the query side's counter behind them
 }
 
 extern "C" int nf4ls_packed_attention_fwd(const nf4ls_pack* pack, const nf4ls_packed_heads* heads,
@@ -1309,13 +1341,12 @@ extern "C" int nf4ls_packed_attention_bwd(const nf4ls_pack* pack, const nf4ls_pa
   NF4_TRY(tile_map(&p.tq, t->q, qd, pack->total, t->ld_q));
   NF4_TRY(tile_map(&p.tk, t->k, kvd, pack->total, t->ld_k));
   NF4_TRY(tile_map(&p.tv, t->v, kvd, pack->total, t->ld_v));
-  NF4_TRY(tile_map(&p.to, t->o, qd, pack->total, t->ld_o));
   NF4_TRY(tile_map(&p.tdo, t->d_o, qd, pack->total, t->ld_do));
   NF4_TRY(tile_map(&p.tdq, t->dq, qd, pack->total, t->ld_dq));
   NF4_TRY(tile_map(&p.tdk, t->dk, kvd, pack->total, t->ld_dk));
   NF4_TRY(tile_map(&p.tdv, t->dv, kvd, pack->total, t->ld_dv));
-  p.lse = t->lse;
   p.stats = static_cast<float*>(ws_dev);
+  p.next = reinterpret_cast<unsigned*>(p.stats + (size_t)heads->n_q * pack->n_tiles * 2 * TT);
   p.dq = static_cast<__nv_bfloat16*>(t->dq);
   p.dk = static_cast<__nv_bfloat16*>(t->dk);
   p.dv = static_cast<__nv_bfloat16*>(t->dv);
@@ -1329,7 +1360,10 @@ extern "C" int nf4ls_packed_attention_bwd(const nf4ls_pack* pack, const nf4ls_pa
   p.scale = heads->scale;
   p.scale_log2 = heads->scale * 1.4426950408889634f;
   p.err = device_error_ptr();
-  const PackTile *qt = tile_list(pack, pack->off_query_tiles), *kt = tile_list(pack, pack->off_key_tiles);
+  p.query_tiles = tile_list(pack, pack->off_query_tiles);
+  p.key_tiles = tile_list(pack, pack->off_key_tiles);
+  const StatsParams st = {p.query_tiles, static_cast<const __nv_bfloat16*>(t->o), static_cast<const __nv_bfloat16*>(t->d_o), t->lse,
+                          p.stats, p.next, t->ld_o, t->ld_do, p.total, p.n_tiles, p.nq};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return d == 64 ? launch_bwd<64>(p, pack, qt, kt, s) : launch_bwd<128>(p, pack, qt, kt, s);
+  return d == 64 ? launch_bwd<64>(p, st, pack, s) : launch_bwd<128>(p, st, pack, s);
 }

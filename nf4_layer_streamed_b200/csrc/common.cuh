@@ -393,10 +393,10 @@ struct LaunchHow {
   int cluster;  // blocks of one, 1: none
 };
 template <typename... P, typename... A>
-cudaError_t launch_kernel(void (*k)(P...), int64_t blocks, const LaunchHow& how, cudaStream_t s, A... args) {
+cudaError_t launch_kernel(void (*k)(P...), dim3 grid, const LaunchHow& how, cudaStream_t s, A... args) {
   cudaLaunchAttribute at[2];
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)how.threads);
   cfg.dynamicSmemBytes = how.smem;
   cfg.stream = s;
