@@ -608,8 +608,8 @@ int nf4ls_pack_fill(const int32_t* lengths_host, const nf4ls_pack* pack, void* p
  * The backward takes o and lse of the forward and do (dL/do) and writes dq, dk, dv, the
  * gradients with respect to q, k and v as given (dk and dv summed over the query heads
  * that share them).  ws: nf4ls_packed_attention_ws_bytes, 256-byte aligned, free again
- * once the call's kernels have finished.  Deterministic: no atomics, fixed reduction
- * orders.  No output may overlap an input. */
+ * once the call's kernels have finished.  Deterministic: every sum has a fixed
+ * order.  No output may overlap an input. */
 typedef struct {
     int32_t n_q, n_kv, head_dim;
     float scale;
