@@ -702,7 +702,8 @@ int nf4ls_rope_apply(const nf4ls_rope_cfg* cfg, const nf4ls_rope_rows* t, nf4ls_
  *   row loss = w (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (e^d - d - 1));
  * loss = sum of the row losses over the rows with a target (w carries the 1 / count).  One
  * launch reads a row, and, unless dlogits_dev is NULL, writes its gradient times
- * grad_scale; on the border of the clip range the gradient flows.  ref_logp may be NULL
+ * grad_scale; on the border of the clip range the gradient flows.  A NaN in a row's logits,
+ * old_logp or advantage makes its loss and its whole gradient row NaN.  ref_logp may be NULL
  * when kl_coef is 0.  logp_dev and row_loss_dev: fp32 [rows], written.
  * Sums run in a fixed order: the same inputs give the same bits. */
 #define NF4LS_PREF_SIGMOID 0

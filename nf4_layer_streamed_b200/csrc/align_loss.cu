@@ -323,10 +323,12 @@ __device__ __forceinline__ float policy_row(const PolicyParams& p, int row, floa
   const bool passes = free_s <= held;  // the gradient flows through the unclipped term
   // no KL term where its coefficient is 0 (ref_logp may then be null)
   const double gap = p.kl > 0.0f ? (double)p.ref_logp[row] - lp : 0.0, e1 = expm1(gap);
-  const double surrogate = isnan(r) ? r : (passes ? free_s : held);
+  // the comparison drops a NaN of r or A (not 0 x inf, a row of no advantage): it goes into both
+  const bool spoiled = isnan(r) || isnan(a);
+  const double surrogate = spoiled ? r + a : (passes ? free_s : held), flows = spoiled ? r + a : (passes ? free_s : 0.0);
   p.logp[row] = (float)lp;
   p.row_loss[row] = (float)(w * (p.kl * (e1 - gap) - surrogate));
-  return (float)(w * (-p.kl * e1 - (passes ? free_s : 0.0)) * p.scale);
+  return (float)(w * (-p.kl * e1 - flows) * p.scale);
 }
 
 // KEEP: pieces of 16 bytes of a row that stay in shared memory between its two passes.

@@ -304,3 +304,27 @@ def test_row_offsets_beyond_32_bits():
     api.preference_loss_bwd(pack, x, t, f, out=x)
     c = f.coef.double()[1].expand(50)
     check_grad(x[tail], keep, t[tail], has, c, 2.0 ** -22 * c.abs())
+
+
+@pytest.mark.parametrize("vocab", [1003, 49152, 128256])
+@pytest.mark.parametrize("kl", [0.0, 0.05])
+def test_policy_rows_that_are_not_finite(vocab, kl):
+    """NaN and +inf in a row's logits, or a NaN advantage, make the row's gradient NaN, not zero."""
+    x, t, g = make(8, vocab, seed=6)
+    t[:] = torch.tensor([3, 4, 5, 6, 7, 8, -1, 9], device=DEV)
+    lp, _ = logp64(x, t, vocab)
+    old, ref, adv, w = (lp + 0.1).float(), (lp - 0.2).float(), torch.linspace(-1, 1, 8, device=DEV), torch.full((8,), 0.125, device=DEV)
+    args = (old, ref if kl else None)
+    _, logp0, d0 = api.policy_loss(x, t, *args, adv, w, 0.2, 0.2, kl)
+    bad, adv1 = x.clone(), adv.clone()
+    bad[1, 50] = math.nan
+    bad[2, 60] = math.inf
+    bad[3, 6] = math.nan                # the target's
+    bad[6] = math.nan                   # a row without a target
+    adv1[4] = math.nan
+    for inplace in (False, True):
+        loss, logp, d = api.policy_loss(bad, t, *args, adv1, w, 0.2, 0.2, kl, out=bad if inplace else None)
+        assert torch.isnan(loss).all()
+        assert torch.isnan(logp[1:4]).all() and torch.equal(logp[[0, 4, 5, 7]], logp0[[0, 4, 5, 7]])
+        assert torch.isnan(d[1:5]).all()
+        assert (d[6] == 0).all() and torch.equal(d[[0, 5, 7]], d0[[0, 5, 7]])
