@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(PT) k_preference(const int32_t* __restrict__ c
         // -log sigmoid(h) = max(-h, 0) + log1p(exp(-|h|)); sigmoid(-h) without overflow
         const double e = exp(-fabs(h)), soft = log1p(e);
         const double away = h >= 0.0 ? e / (1.0 + e) : 1.0 / (1.0 + e);  // sigmoid(-h)
-        l = (1.0 - smoothing) * (fmax(-h, 0.0) + soft) + smoothing * (fmax(h, 0.0) + soft);
+        l = (1.0 - smoothing) * (fmax(-h, 0.0) + soft);
+        if (smoothing > 0.0f) l += smoothing * (fmax(h, 0.0) + soft);  // not 0 x inf for an infinite margin
         slope = beta * (smoothing * (1.0 - away) - (1.0 - smoothing) * away);
         if (isnan(h)) l = slope = h;
       } else if (kind == NF4LS_PREF_HINGE) {

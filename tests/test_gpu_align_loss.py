@@ -328,3 +328,37 @@ def test_policy_rows_that_are_not_finite(vocab, kl):
         assert torch.isnan(logp[1:4]).all() and torch.equal(logp[[0, 4, 5, 7]], logp0[[0, 4, 5, 7]])
         assert torch.isnan(d[1:5]).all()
         assert (d[6] == 0).all() and torch.equal(d[[0, 5, 7]], d0[[0, 5, 7]])
+
+
+@pytest.mark.parametrize("eps", [0.0, 0.1])
+def test_pairs_with_a_sequence_of_probability_zero(eps):
+    """A target whose logit is -inf: the margin is infinite.  Where the rejected sequence has it, the pair's loss is
+    0 without smoothing (not 0 x inf) and its gradient 0; where the preferred one has it, the loss is infinite."""
+    vocab, lengths, beta = 1003, [3, 4, 2, 5], 0.1
+    x, t, _ = make(14, vocab, seed=8)
+    t[:] = torch.arange(20, 34, device=DEV)
+    ref = torch.zeros(4, device=DEV)
+    pack = api.PackedRows(lengths)
+    f0 = api.preference_loss_fwd(pack, x, t, ref, beta, label_smoothing=eps)
+    d0 = api.preference_loss_bwd(pack, x, t, f0)
+    h = f0.margin[1].double()
+    other = -((1 - eps) * F.logsigmoid(h) + eps * F.logsigmoid(-h)).item()
+    for row, infinite in ((4, math.inf), (1, -math.inf)):
+        y = x.clone()
+        y[row, t[row].long()] = -math.inf
+        f = api.preference_loss_fwd(pack, y, t, ref, beta, label_smoothing=eps)
+        assert f.margin[0].item() == infinite and torch.equal(f.margin[1:], f0.margin[1:])
+        # slope of the pair's loss: beta (eps sigmoid(h) - (1 - eps) sigmoid(-h)), halved by the mean
+        c = beta * (eps if infinite > 0 else -(1 - eps)) / 2
+        assert f.coef[0].item() == pytest.approx(c, rel=2.0 ** -22, abs=0) and f.coef[1].item() == -f.coef[0].item()
+        if infinite > 0 and eps == 0.0:
+            assert f.loss.item() == pytest.approx(other / 2, rel=2.0 ** -23 * (1 + abs(h.item())))  # h is rounded to fp32
+        else:
+            assert f.loss.item() == math.inf
+        d = api.preference_loss_bwd(pack, y, t, f)
+        assert torch.isfinite(d).all() and torch.equal(d[7:], d0[7:])
+        if c == 0.0:
+            assert (d[:7] == 0).all()
+        has = torch.ones(7, dtype=torch.bool, device=DEV)
+        coef = torch.tensor([c] * 3 + [-c] * 4, dtype=torch.float64, device=DEV)
+        check_grad(d[:7], y[:7], t[:7], has, coef, 2.0 ** -22 * coef.abs())
