@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import struct
 from dataclasses import dataclass
@@ -464,13 +465,19 @@ def _current(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _heads(n_q, n_kv, head_dim, scale) -> B.PackedHeads:
+    # plain numbers: a tensor would be remembered by its identity, with the value it had then
+    return _heads_of(operator.index(n_q), operator.index(n_kv), operator.index(head_dim),
+                     None if scale is None else float(scale))
+
+
 @functools.lru_cache(maxsize=64)
-def _heads(n_q: int, n_kv: int, head_dim: int, scale) -> B.PackedHeads:
+def _heads_of(n_q: int, n_kv: int, head_dim: int, scale: float | None) -> B.PackedHeads:
     if head_dim not in (64, 128):
         raise ValueError(f"head_dim {head_dim}: 64 or 128")
     if n_kv < 1 or n_q < 1 or n_q % n_kv:
         raise ValueError(f"{n_q} query heads are not a multiple of {n_kv} key/value heads")
-    scale = head_dim ** -0.5 if scale is None else float(scale)
+    scale = head_dim ** -0.5 if scale is None else scale
     if not 0.0 < scale < 1e30:
         raise ValueError(f"scale {scale}: must be positive")
     return B.PackedHeads(n_q, n_kv, head_dim, scale)

@@ -147,3 +147,20 @@ def test_argument_structs_are_laid_out_like_the_bindings():
         values = [float(i + 1) if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(struct._fields_)]
         got = struct.from_buffer_copy(packed.pack(*values))
         assert [getattr(got, name) for name, _ in struct._fields_] == values and n == len(values)
+
+
+def test_head_configuration_is_taken_by_value():
+    """A 0-dim tensor that changes in place is read anew at every call (refused here when its value is)."""
+    pack, q, k, v = _attention_args()
+    scale, n_kv = torch.tensor(0.5), torch.tensor(2)
+    for call in (lambda: api.packed_attention_fwd(pack, q, k, v, 4, n_kv, 64, scale=scale),
+                 lambda: api.packed_attention_bwd(pack, q, k, v, q, q, torch.zeros(4, 12), 4, n_kv, 64, scale=scale)):
+        scale.fill_(0.5), n_kv.fill_(2)
+        with pytest.raises(ValueError, match="CUDA"):      # every other argument is good
+            call()
+        scale.fill_(-1.0)
+        with pytest.raises(ValueError, match="scale -1.0"):
+            call()
+        scale.fill_(0.5), n_kv.fill_(3)
+        with pytest.raises(ValueError, match="not a multiple of 3"):
+            call()
