@@ -521,7 +521,9 @@ def packed_attention_bwd(pack: PackedRows, q, k, v, o, do, lse, n_q: int, n_kv: 
     rows, qd, kvd = pack.total, n_q * head_dim, n_kv * head_dim
     ld_q, ld_k, ld_v = _rows2d(q, "q", rows, qd), _rows2d(k, "k", rows, kvd), _rows2d(v, "v", rows, kvd)
     ld_o, ld_do = _rows2d(o, "o", rows, qd), _rows2d(do, "do", rows, qd)
-    _need(lse, "lse", torch.float32, n_q * rows)
+    _need(lse, "lse", torch.float32)
+    if lse.shape != (n_q, rows):
+        raise ValueError(f"lse: expected [{n_q}, {rows}], got {tuple(lse.shape)}")
     dq, dk, dv = out if out is not None else (None, None, None)
     if out is not None:
         ld_dq, ld_dk, ld_dv = _rows2d(dq, "dq", rows, qd), _rows2d(dk, "dk", rows, kvd), _rows2d(dv, "dv", rows, kvd)

@@ -164,3 +164,11 @@ def test_head_configuration_is_taken_by_value():
         scale.fill_(0.5), n_kv.fill_(3)
         with pytest.raises(ValueError, match="not a multiple of 3"):
             call()
+
+
+@pytest.mark.parametrize("shape", [(12, 4), (48,), (1, 4, 12), (2, 24)])
+def test_gradients_refuse_statistics_of_another_layout(shape):
+    """lse is [n_q, total]: the same number of values in another order would be misread."""
+    pack, q, k, v = _attention_args()
+    with pytest.raises(ValueError, match="lse: expected"):
+        api.packed_attention_bwd(pack, q, k, v, q, q, torch.zeros(shape), 4, 2, 64)
