@@ -123,11 +123,13 @@ int check_rope(const nf4ls_rope_cfg* c, const char* who) {
   return NF4LS_OK;
 }
 
-int check_side(const void* x, const void* y, int ld_x, int ld_y, int width, const char* name, const char* who) {
+int check_side(const void* x, const void* y, int ld_x, int ld_y, int width, int rows, const char* name, const char* who) {
   if (!x || !y) return fail(NF4LS_INVALID_ARG, "%s: null %s", who, name);
   if (!aligned(x, 16) || !aligned(y, 16)) return fail(NF4LS_ALIGN, "%s: %s must be 16-byte aligned", who, name);
   if (ld_x < width || ld_y < width || ld_x % 8 || ld_y % 8)
     return fail(NF4LS_SHAPE, "%s: row strides %d, %d of %s (multiples of 8, at least %d)", who, ld_x, ld_y, name, width);
+  if (x == y && ld_x != ld_y && rows > 1)  // in place is the same rows; another stride is an overlap
+    return fail(NF4LS_INVALID_ARG, "%s: %s in place with another row stride", who, name);
   return NF4LS_OK;
 }
 
@@ -181,8 +183,8 @@ extern "C" int nf4ls_rope_apply(const nf4ls_rope_cfg* c, const nf4ls_rope_rows* 
     return fail(NF4LS_SHAPE, "%s: rows %d, heads %d + %d", who, t->rows, t->n_q, t->n_kv);
   if (!t->turns_dev || (t->rows > 0 && !t->positions_dev)) return fail(NF4LS_INVALID_ARG, "%s: null table or positions", who);
   if (!aligned(t->turns_dev, 16)) return fail(NF4LS_ALIGN, "%s: the table must be 16-byte aligned", who);
-  if (t->n_q) NF4_TRY(check_side(t->q, t->q_out, t->ld_q, t->ld_q_out, t->n_q * c->head_dim, "q", who));
-  if (t->n_kv) NF4_TRY(check_side(t->k, t->k_out, t->ld_k, t->ld_k_out, t->n_kv * c->head_dim, "k", who));
+  if (t->n_q) NF4_TRY(check_side(t->q, t->q_out, t->ld_q, t->ld_q_out, t->n_q * c->head_dim, t->rows, "q", who));
+  if (t->n_kv) NF4_TRY(check_side(t->k, t->k_out, t->ld_k, t->ld_k_out, t->n_kv * c->head_dim, t->rows, "k", who));
   const int units = c->head_dim / 16;
   if ((int64_t)t->rows * units > 0x7FFFFFFFll - 256) return fail(NF4LS_SHAPE, "%s: too many rows for one launch", who);
   if (t->rows == 0) return NF4LS_OK;

@@ -97,3 +97,13 @@ def test_c_call_checks_its_arguments_on_the_host():
     assert call() == -2
     cfg.rot_dim = 72
     assert call() == -2
+
+
+def test_c_call_refuses_in_place_with_another_row_stride():
+    cfg = B.RopeCfg(64, 32, 0, 0, 10000.0, 1.0, 0.0, 0.0, 0.0)
+    for side in ("q", "k"):
+        t = B.RopeRows(256, 256, 256, 512, 1024, 2048, 6, 4, 2, 256, 128, 256, 128, 0, 1.0)
+        setattr(t, side + "_out", getattr(t, side))
+        setattr(t, f"ld_{side}_out", 320)
+        assert B.call_status("nf4ls_rope_apply", ctypes.byref(cfg), ctypes.byref(t), None) == -1
+        assert f"{side} in place" in B.last_error()
