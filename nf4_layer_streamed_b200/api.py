@@ -361,12 +361,14 @@ class PackedRows:
     positions, seq (int32 [total]) and cu (int32 [n_seqs + 1]) are device views of it."""
 
     def __init__(self, lengths, device="cuda"):
-        n = np.asarray(lengths, dtype=np.int64)
-        if n.ndim != 1 or n.size == 0:
+        given = np.asarray(lengths)
+        if given.ndim != 1 or given.size == 0:
             raise ValueError("PackedRows: expected a non-empty list of lengths")
-        if n.min() < 0 or n.max() > (1 << 28):
+        if given.dtype.kind == "f" and not (np.floor(given) == given).all():
+            raise ValueError("PackedRows: lengths that are not whole numbers")
+        if given.min() < 0 or given.max() > (1 << 28):
             raise ValueError("PackedRows: lengths outside [0, 2^28]")
-        n32 = np.ascontiguousarray(n, dtype=np.int32)
+        n32 = np.ascontiguousarray(given, dtype=np.int32)
         self.pack = B.Pack()
         B.call("nf4ls_pack_layout", n32.ctypes.data, n32.size, ctypes.byref(self.pack))
         host = torch.empty(self.pack.plan_bytes, dtype=torch.uint8)

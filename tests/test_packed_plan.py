@@ -172,3 +172,14 @@ def test_gradients_refuse_statistics_of_another_layout(shape):
     pack, q, k, v = _attention_args()
     with pytest.raises(ValueError, match="lse: expected"):
         api.packed_attention_bwd(pack, q, k, v, q, q, torch.zeros(shape), 4, 2, 64)
+
+
+def test_lengths_are_whole_numbers():
+    for bad in ([1.5], [3, 2.999], np.array([4.0, np.nan]), torch.tensor([0.5, 8.0])):
+        with pytest.raises(ValueError, match="whole"):
+            api.PackedRows(bad, device="cpu")
+    for good in ([3, 2], (3.0, 2.0), np.array([3, 2], np.int16), torch.tensor([3, 2])):
+        assert api.PackedRows(good, device="cpu").cu.tolist() == [0, 3, 5]
+    for far in ([2.0 ** 70, 1.0], [float("inf")], np.array([2 ** 64 - 1], np.uint64)):
+        with pytest.raises(ValueError, match="outside"):
+            api.PackedRows(far, device="cpu")
