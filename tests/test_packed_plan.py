@@ -183,3 +183,17 @@ def test_lengths_are_whole_numbers():
     for far in ([2.0 ** 70, 1.0], [float("inf")], np.array([2 ** 64 - 1], np.uint64)):
         with pytest.raises(ValueError, match="outside"):
             api.PackedRows(far, device="cpu")
+
+
+def test_overlap_is_found_across_storages():
+    """A view that came back through dlpack shares memory, though its storage starts elsewhere."""
+    pack, q, k, v = _attention_args()
+    buf = torch.zeros(12, 512, dtype=torch.bfloat16)
+    alias = torch.from_dlpack(buf[:, 128:384])
+    with pytest.raises(ValueError, match="overlaps"):
+        api.packed_attention_fwd(pack, buf[:, :256], k, v, 4, 2, 64, out=alias)
+    with pytest.raises(ValueError, match="CUDA"):          # its neighbours' columns are no overlap
+        api.packed_attention_fwd(pack, q, buf[:, :128], buf[:, 384:], 4, 2, 64, out=alias)
+    rows = torch.zeros(20, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="overlaps"):
+        api.packed_attention_fwd(pack, rows[:12], k, v, 4, 2, 64, out=torch.from_dlpack(rows[8:]))
