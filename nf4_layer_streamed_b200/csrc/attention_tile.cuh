@@ -153,7 +153,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
         : "=r"(ok)
         : "r"(a), "r"(parity), "r"(first)
         : "memory");
-    if (__any_sync(0xffffffffu, ok)) return true;
+    if (__any_sync(0xffffffffu, ok)) {
+      __syncwarp();  // the vote orders no memory: this hands what the first lane acquired to the others
+      return true;
+    }
     if ((i & 15) == 15) {
       const unsigned long long t = global_ns();
       if (t0 == 0) t0 = t;
