@@ -362,3 +362,27 @@ def test_pairs_with_a_sequence_of_probability_zero(eps):
         has = torch.ones(7, dtype=torch.bool, device=DEV)
         coef = torch.tensor([c] * 3 + [-c] * 4, dtype=torch.float64, device=DEV)
         check_grad(d[:7], y[:7], t[:7], has, coef, 2.0 ** -22 * coef.abs())
+
+
+def check_half(half, d, vocab):
+    """Halving is exact in bf16, but for values at the end of its range."""
+    big = d.float().abs() > 1e-30
+    assert torch.equal(half.float()[big], 0.5 * d.float()[big])
+    assert (half.float()[~big].abs() <= 1e-30).all()
+    assert big.any() or vocab == 1
+
+
+@pytest.mark.parametrize("vocab", VOCABS)
+def test_grad_scale_scales_every_element(vocab):
+    lengths = [5, 17, 1, 0, 40, 12]
+    n = sum(lengths)
+    x, t, g = make(n, vocab, seed=7, offset=vocab % 3)
+    pack = api.PackedRows(lengths)
+    r = torch.randn(n, generator=g, device=DEV)
+    f = api.preference_loss_fwd(pack, x, t, torch.randn(6, generator=g, device=DEV), 0.1)
+    check_half(api.preference_loss_bwd(pack, x, t, f, grad_scale=0.5), api.preference_loss_bwd(pack, x, t, f), vocab)
+    args = (x, t, f.logp, f.logp + 0.1 * r, r, torch.full((n,), 0.1, device=DEV), 0.2, 0.2, 0.05)
+    loss, logp, d = api.policy_loss(*args)
+    half_loss, half_logp, half = api.policy_loss(*args, grad_scale=0.5)
+    check_half(half, d, vocab)
+    assert torch.equal(half_loss, loss) and torch.equal(half_logp, logp)
