@@ -311,3 +311,26 @@ def test_row_offsets_beyond_32_bits():
     ref = reference_grad(lengths[1:], q[tail], k[tail], v[tail], o[tail], do[tail], lse[:, tail], n_q, n_kv, d, d ** -0.5)
     for name, x, w, t in zip(("dq", "dk", "dv"), outs, ref[:3], ref[3:]):
         within(x[tail], w, t, name)
+
+
+@pytest.mark.parametrize("lengths,heads,scale", [
+    ([300, 129, 1], (4, 1, 64), 0.3), ([300, 129, 1], (4, 1, 64), 0.03), ([512], (8, 2, 128), 0.13),
+    ([129, 1, 200] * 24, (6, 2, 128), 0.13), ([129, 1, 200] * 24, (5, 1, 64), 0.3), ([257], (2, 2, 128), 0.02)], ids=str)
+def test_scale_of_every_output(lengths, heads, scale):
+    """Scales that are not 1 / sqrt(head_dim), element by element, where a key tile is two blocks' work and where
+    it is one's.  A score is off by (d + 2) 2^-24 scale sum |q||k|: for N(0, 1) operands the sum is below
+    1.5 x 0.64 d (d = 64) and 1.3 x 0.64 d (d = 128), so 7.2e-5 nats at 0.3 and 64 dims, 1.1e-4 at 0.13 and 128:
+    within 2^-13, the share F that the bounds count."""
+    n_q, n_kv, d = heads
+    q, k, v, do = make(lengths, n_q, n_kv, d, seed=11)
+    pack = api.PackedRows(lengths)
+    o, lse = api.packed_attention_fwd(pack, q, k, v, n_q, n_kv, d, scale=scale)
+    want, wl, tol = reference(lengths, q, k, v, n_q, n_kv, d, scale)
+    within(o, want, tol, "o")
+    within(lse, wl, F + 2.0 ** -22 * wl.abs(), "lse")
+    got = api.packed_attention_bwd(pack, q, k, v, o, do, lse, n_q, n_kv, d, scale=scale)
+    ref = reference_grad(lengths, q, k, v, o, do, lse, n_q, n_kv, d, scale)
+    for name, g, w, t in zip(("dq", "dk", "dv"), got, ref[:3], ref[3:]):
+        within(g, w, t, name)
+        # the bounds tell the scale: half of these gradients, or their opposite, lies outside them
+        assert ((0.5 * w).abs() > t).any() and (w.abs() > t).any()
