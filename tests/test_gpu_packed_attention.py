@@ -334,3 +334,44 @@ def test_scale_of_every_output(lengths, heads, scale):
         within(g, w, t, name)
         # the bounds tell the scale: half of these gradients, or their opposite, lies outside them
         assert ((0.5 * w).abs() > t).any() and (w.abs() > t).any()
+
+
+@pytest.mark.parametrize("copies", [1, 40])
+def test_gradients_of_scores_below_the_range(copies):
+    """Keys whose scores are -inf in fp32, single ones and a whole tile, in rows that see others too: the
+    probabilities there are 0, and so is their share of every gradient."""
+    lengths, n_q, n_kv, d = [300, 20] * copies, 4, 2, 64
+    q, k, v, do = make(lengths, n_q, n_kv, d, seed=12)
+    q, k = q.abs(), k.clone()
+    low = torch.zeros(sum(lengths), dtype=torch.bool, device=DEV)
+    for a in range(0, sum(lengths), 320):
+        low[a + 5] = low[a + 310] = True
+        low[a + 128:a + 256] = True
+    k[low] = torch.finfo(torch.bfloat16).min
+    pack = api.PackedRows(lengths)
+    o, lse = api.packed_attention_fwd(pack, q, k, v, n_q, n_kv, d)
+    want, wl, tol = reference(lengths, q, k, v, n_q, n_kv, d, d ** -0.5)
+    within(o, want, tol, "o")
+    within(lse, wl, 6e-5 + 2.0 ** -22 * wl.abs(), "lse")
+    dq, dk, dv = api.packed_attention_bwd(pack, q, k, v, o, do, lse, n_q, n_kv, d)
+    ref = reference_grad(lengths, q, k, v, o, do, lse, n_q, n_kv, d, d ** -0.5)
+    for name, g, w, t in zip(("dq", "dk", "dv"), (dq, dk, dv), ref[:3], ref[3:]):
+        within(g, w, t, name)
+    assert (dk[low] == 0).all() and (dv[low] == 0).all()
+
+
+def test_gradients_of_rows_that_see_only_scores_below_the_range():
+    """Rows that see nothing above -inf are NaN, in the forward and in their gradients; the rows and keys behind them
+    and the next sequence are as if they were not there."""
+    lengths, n_q, n_kv, d, n = [300, 20], 4, 2, 64, 140
+    q, k, v, do = make(lengths, n_q, n_kv, d)
+    q, k = q.abs(), k.clone()
+    k[:n] = torch.finfo(torch.bfloat16).min
+    pack = api.PackedRows(lengths)
+    o, lse = api.packed_attention_fwd(pack, q, k, v, n_q, n_kv, d)
+    got = api.packed_attention_bwd(pack, q, k, v, o, do, lse, n_q, n_kv, d)
+    assert got[0][:n].isnan().all()
+    cut = [x[n:] for x in (q, k, v, o, do)]
+    ref = reference_grad([300 - n, 20], *cut, lse[:, n:], n_q, n_kv, d, d ** -0.5)
+    for name, g, w, t in zip(("dq", "dk", "dv"), got, ref[:3], ref[3:]):
+        within(g[n:], w, t, name)
