@@ -90,3 +90,43 @@ def test_preference_step_over_packed_rows(n_q, n_kv, d, vocab):
     plp = torch.log_softmax(zl, 1).gather(1, targets.clamp(min=0).long()[:, None])[:, 0]
     (-(w * adv).double() * plp * (targets >= 0)).sum().backward()
     close(pd, zl.grad.cpu().numpy(), TOL, "policy gradient")
+
+
+def test_captured_preference_step():
+    """The run above as one graph: replayed on new inputs it gives the bits of the eager calls."""
+    n_q, n_kv, d, vocab = 8, 2, 128, 2048
+    lengths = [150, 131, 64, 200, 17, 1]
+    pack = api.PackedRows(lengths)
+    n, qd, kvd = pack.total, n_q * d, n_kv * d
+    g = torch.Generator(device=DEV).manual_seed(2)
+    qkv = torch.randn(n, qd + 2 * kvd, generator=g, device=DEV).to(torch.bfloat16)
+    head = (torch.randn(vocab, qd, generator=g, device=DEV) * 0.1).to(torch.bfloat16)
+    targets = torch.randint(0, vocab, (n,), generator=g, device=DEV).to(torch.int32)
+    targets[pack.cu[1:].long() - 1] = -1
+    ref, adv = torch.randn(6, generator=g, device=DEV), torch.randn(n, generator=g, device=DEV)
+    w = torch.full((n,), 1.0 / n, device=DEV)
+    rope = api.Rope(d, 10000.0, scaling=BANDED)
+
+    def step():
+        rq, rk = api.rope_apply(rope, pack.positions, qkv[:, :qd], qkv[:, qd:qd + kvd], n_q, n_kv)
+        v = qkv[:, qd + kvd:]
+        o, lse = api.packed_attention_fwd(pack, rq, rk, v, n_q, n_kv, d)
+        logits = api.gemm_bf16(o, head)
+        f = api.preference_loss_fwd(pack, logits, targets, ref, 0.1)
+        dlogits = api.preference_loss_bwd(pack, logits, targets, f)
+        do = api.gemm_bf16(dlogits, head, b_trans=True)
+        dq, dk, dv = api.packed_attention_bwd(pack, rq, rk, v, o, do, lse, n_q, n_kv, d)
+        dq, dk = api.rope_apply(rope, pack.positions, dq, dk, n_q, n_kv, inverse=True)
+        return (f.loss, f.margin, f.logp, dq, dk, dv) + api.policy_loss(logits, targets, f.logp, None, adv, w, 0.2, 0.2)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for _ in range(2):
+        qkv.copy_(torch.randn(qkv.shape, generator=g, device=DEV))
+        want = [x.clone() for x in step()]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)) and want[3].abs().max() > 0
+    assert api.device_error()[0] == 0
