@@ -603,11 +603,13 @@ int nf4ls_pack_fill(const int32_t* lengths_host, const nf4ls_pack* pack, void* p
  * i, j in the same sequence.  q, o: bf16 [total, n_q * head_dim]; k, v: bf16 [total,
  * n_kv * head_dim]; each with a row stride ld_* in elements (a multiple of 8, at least the
  * row's width).  lse: fp32 [n_q, total], the log-sum-exp of each row of scaled scores.
- * head_dim 64 or 128, n_q a multiple of n_kv, scale > 0.
+ * head_dim 64 or 128, n_q a multiple of n_kv, scale > 0.  Scores may be of any size that
+ * fp32 holds; a row whose scores are all -inf (products beyond fp32) is NaN.
  *
  * The backward takes o and lse of the forward and do (dL/do) and writes dq, dk, dv, the
  * gradients with respect to q, k and v as given (dk and dv summed over the query heads
- * that share them).  ws: nf4ls_packed_attention_ws_bytes, 256-byte aligned, free again
+ * that share them).  It forms the probabilities from lse, which fp32 holds to 2^-24 of its
+ * size: with |lse| of 10^5 they are off by 1 to 2%, far beyond that they mean nothing.  ws: nf4ls_packed_attention_ws_bytes, 256-byte aligned, free again
  * once the call's kernels have finished.  Deterministic: every sum has a fixed
  * order.  No output may overlap an input. */
 typedef struct {

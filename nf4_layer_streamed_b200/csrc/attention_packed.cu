@@ -127,6 +127,7 @@ constexpr int F_THREADS = 192, F_PROD = 4, F_MMA = 5;
 constexpr int F_OFF_Q = 0, F_OFF_K = TILE_BYTES, F_OFF_V = 2 * TILE_BYTES, F_OFF_BAR = 3 * TILE_BYTES;
 constexpr int SMEM_TC = 1024 + F_OFF_BAR + 128;
 constexpr float kRescaleLog2 = 8.0f;  // the reference maximum may trail the true one by this much
+constexpr float kFarLog2 = 16384.0f;  // a scaled maximum of this size is rounded by up to 2^-10
 
 template <int D>
 __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_constant__ FwdParams p) {
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
     const int r = warp * 32 + lane;  // query row in the tile = TMEM lane
     const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
     const float sl = p.scale_log2;
-    float m_run = -INFINITY, l_run = 0.f;
+    float m_run = -INFINITY, ms = -INFINITY, l_run = 0.f;  // the reference maximum, that scaled, the sum
     bool ok = true;
     for (int kt = 0; kt < nk; ++kt) {
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full, kt & 1, abort_flag, p.err, KID_PACKED, 27)))) break;
@@ -273,27 +274,44 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
         for (int e = 0; e < 4; ++e)
           m4[e] = fmaxf(fmaxf(m4[e], __uint_as_float(v[i / 32][i % 32 + e])), __uint_as_float(v[i / 32][i % 32 + 4 + e]));
       float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      mx *= sl;
-      const float m_new = (kt == 0 || mx > m_run + kRescaleLog2) ? fmaxf(mx, m_run) : m_run;
-      const bool resc = kt > 0 && m_new != m_run;
-      if (__any_sync(0xffffffffu, resc)) {
-        // the previous tile's P V product must be in O before O is scaled
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(o_full, (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 28)))) break;
-        tc_fence_after();
-        const float alpha = resc ? fast_exp2(m_run - m_new) : 1.0f;
+      const float mxs = mx * sl, m_old = m_run, ms_old = ms;
+      bool up = mxs > ms + kRescaleLog2;
+      if (up) m_run = mx, ms = mxs;
+      // no score above -inf so far (products beyond fp32): probabilities of 0, not NaN
+      float ref = ms == -INFINITY ? 0.0f : ms;
+      // (the branch of the far rows costs 1% for 16.4k rows, nothing for 2048)
+      if (__builtin_expect(__any_sync(0xffffffffu, (kt > 0 && up) || fabsf(ms) >= kFarLog2), 0)) {  // out of line
+        const bool far = fabsf(ms) >= kFarLog2 && m_run > -INFINITY;
+        if (far && (mx - m_run) * sl > kRescaleLog2) up = true, m_run = mx, ms = mxs;
+        const bool resc = kt > 0 && up;
+        if (__any_sync(0xffffffffu, resc)) {
+          // the previous tile's P V product must be in O before O is scaled
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(o_full, (kt - 1) & 1, abort_flag, p.err, KID_PACKED, 28)))) break;
+          tc_fence_after();
+          const float alpha = resc ? fast_exp2(far ? (m_old - m_run) * sl : ms_old - ms) : 1.0f;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {  // 16 columns at a time: the scores hold the registers
-          uint32_t o[16];
-          tmem_ld16(trow + 128 + c * 16, o);
-          tmem_wait_ld();
+          for (int c = 0; c < D / 16; ++c) {  // 16 columns at a time: the scores hold the registers
+            uint32_t o[16];
+            tmem_ld16(trow + 128 + c * 16, o);
+            tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          tmem_st16(trow + 128 + c * 16, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st16(trow + 128 + c * 16, o);
+          }
+          tmem_wait_st();
+          l_run *= alpha;
         }
-        tmem_wait_st();
-        l_run *= alpha;
+        if (__any_sync(0xffffffffu, far)) {
+          // the fused multiply-add below takes the rounded product of the maximum from the exact one of a score:
+          // with such scores that would leave more than the exponential's range; the difference first
+          const float sub = far ? m_run : 0.0f;
+          ref = far ? 0.0f : ref;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) - sub);
+        }
       }
-      m_run = m_new;
       if (diag && n_rows < TT) {
         // rows of V behind the sequence's end belong to others: zeros, so that a
         // non-finite value there times a probability of 0 stays out of O
@@ -301,8 +319,6 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
         if (r >= n_rows) zero_row<NA>(smem_u32(base + F_OFF_V), r);
         fence_proxy_async_smem();
       }
-      // no score above -inf so far (products beyond fp32): probabilities of 0, not NaN
-      const float ref = m_run == -INFINITY ? 0.0f : m_run;
       const uint64_t sl2 = pack2(sl, sl), nm2 = pack2(-ref, -ref);
       uint64_t acc[2] = {0, 0};
 #pragma unroll
@@ -344,7 +360,7 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
         stage_row32(tile, r, c + 1, v[1], inv);
       }
       if (r < n_rows)
-        p.lse[(size_t)h * p.total + row0 + qt * TT + r] = (m_run + log2f(l_run)) * 0.6931471805599453f;
+        p.lse[(size_t)h * p.total + row0 + qt * TT + r] = (ms + log2f(l_run)) * 0.6931471805599453f;
     }
     fence_proxy_async_smem();
     asm volatile("bar.sync 1, 128;" ::: "memory");

@@ -375,3 +375,39 @@ def test_gradients_of_rows_that_see_only_scores_below_the_range():
     ref = reference_grad([300 - n, 20], *cut, lse[:, n:], n_q, n_kv, d, d ** -0.5)
     for name, g, w, t in zip(("dq", "dk", "dv"), got, ref[:3], ref[3:]):
         within(g[n:], w, t, name)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("power", [20, 36, 100])
+def test_finite_scores_of_any_size(d, power):
+    """Scores of up to 2^114 of either sign, exact in fp32 (a whole number times a power of 2 in every dim): the keys of
+    a row's largest score share the probability and the others have none."""
+    lengths, n_q, n_kv = [300, 1, 77], 4, 2
+    n = sum(lengths)
+    g = torch.Generator(device=DEV).manual_seed(power + d)
+    c = torch.randint(-100, 101, (n, n_kv), generator=g, device=DEV)
+    c[:40] = -c[:40].abs() - 1                            # rows that see nothing but scores far below 0
+    q = torch.full((n, n_q * d), 2.0 ** (power // 2), dtype=torch.bfloat16, device=DEV)
+    k = (c.double() * 2.0 ** (power - power // 2)).to(torch.bfloat16).repeat_interleave(d, 1)
+    v = torch.randn(n, n_kv * d, generator=g, device=DEV).to(torch.bfloat16)
+    o, lse = api.packed_attention_fwd(api.PackedRows(lengths), q, k, v, n_q, n_kv, d)
+    want, wl, tol = reference(lengths, q, k, v, n_q, n_kv, d, d ** -0.5)
+    within(o, want, tol, "o")
+    # fp32: the scale and its product, the product with ln 2 and the result are rounded
+    assert ((lse.double() - wl).abs() <= 2.0 ** -21 * wl.abs() + 6e-5).all()
+
+
+def test_scores_that_grow_far_along_the_keys():
+    """The maximum goes from ordinary scores to ones of 2^50 and on, tile by tile, and elsewhere falls from there."""
+    n, n_q, n_kv, d = 640, 2, 1, 64
+    g = torch.Generator(device=DEV).manual_seed(3)
+    tile = torch.arange(n, device=DEV) // 128
+    v = torch.randn(2 * n, n_kv * d, generator=g, device=DEV).to(torch.bfloat16)
+    q = torch.ones(2 * n, n_q * d, dtype=torch.bfloat16, device=DEV)
+    size = 2.0 ** torch.tensor([-3.0, 4.0, 11.0, 50.0, 60.0], device=DEV)
+    c = torch.randint(1, 101, (2, n), generator=g, device=DEV)
+    k = torch.cat((size[tile] * c[0], size.flip(0)[tile] * c[1]))[:, None].expand(-1, d).to(torch.bfloat16)
+    o, lse = api.packed_attention_fwd(api.PackedRows([n, n]), q, k, v, n_q, n_kv, d)
+    want, wl, tol = reference([n, n], q, k, v, n_q, n_kv, d, d ** -0.5)
+    within(o, want, tol, "o")
+    assert ((lse.double() - wl).abs() <= 2.0 ** -21 * wl.abs() + 6e-5).all()
