@@ -604,7 +604,9 @@ int nf4ls_pack_fill(const int32_t* lengths_host, const nf4ls_pack* pack, void* p
  * n_kv * head_dim]; each with a row stride ld_* in elements (a multiple of 8, at least the
  * row's width).  lse: fp32 [n_q, total], the log-sum-exp of each row of scaled scores.
  * head_dim 64 or 128, n_q a multiple of n_kv, scale > 0.  Scores may be of any size that
- * fp32 holds; a row whose scores are all -inf (products beyond fp32) is NaN.
+ * fp32 holds; a row whose scores are all -inf (products beyond fp32) is NaN.  Within a
+ * sequence the causal mask holds for finite values: a row of k, v, q, o or do that is not
+ * finite may also spoil the results of hidden rows of its 128-row tile (0 times NaN).
  *
  * The backward takes o and lse of the forward and do (dL/do) and writes dq, dk, dv, the
  * gradients with respect to q, k and v as given (dk and dv summed over the query heads
@@ -652,8 +654,9 @@ int nf4ls_packed_attention_bwd(const nf4ls_pack* pack, const nf4ls_packed_heads*
  * nf4ls_rope_apply rotates q [rows, n_q * head_dim] and k [rows, n_kv * head_dim] (bf16,
  * row strides ld_* in elements, multiples of 8) into q_out and k_out in one launch; an
  * output may be its input itself (in place) but may not overlap one otherwise.  Either of
- * n_q and n_kv may be 0.  Positions may be negative and of any size.  The angle is exact
- * to 2^-32 turns at every position. */
+ * n_q and n_kv may be 0.  Positions may be negative and of any size: the angle is reduced
+ * to one turn in whole numbers, to 2^-32 turns at every position, and goes into the fp32
+ * sine and cosine to 2^-25 turns. */
 #define NF4LS_ROPE_NONE   0
 #define NF4LS_ROPE_LINEAR 1
 #define NF4LS_ROPE_BANDED 2
@@ -688,7 +691,7 @@ int nf4ls_rope_apply(const nf4ls_rope_cfg* cfg, const nf4ls_rope_rows* t, nf4ls_
  *
  * Preference loss over pairs of sequences of a packed batch, 2 i preferred to 2 i + 1:
  *   S_s = sum of logp over sequence s;  gap_i = (S_2i - S_2i+1) - (R_2i - R_2i+1) with R the
- *   reference model's sums (ref_logp_dev fp32 [n_seqs]; the adapter-off pass);  h = beta gap;
+ *   reference model's sums (ref_logp_dev fp32 [n_seqs]: seq_logp of its logits);  h = beta gap;
  *   SIGMOID  -(1 - e) log sigmoid(h) - e log sigmoid(-h), e = label_smoothing;
  *   HINGE    max(0, 1 - h);
  *   SQUARED  (gap - 1 / (2 beta))^2;   (these two take no account of label_smoothing)
@@ -707,7 +710,10 @@ int nf4ls_rope_apply(const nf4ls_rope_cfg* cfg, const nf4ls_rope_rows* t, nf4ls_
  * grad_scale; on the border of the clip range the gradient flows.  A NaN in a row's logits,
  * old_logp or advantage makes its loss and its whole gradient row NaN.  ref_logp may be NULL
  * when kl_coef is 0.  logp_dev and row_loss_dev: fp32 [rows], written.
- * Sums run in a fixed order: the same inputs give the same bits. */
+ * Sums run in a fixed order: the same inputs give the same bits.  Gradient rows that start
+ * elsewhere within 16 bytes than their logits rows are written element by element, which is
+ * slower: for logits that are the first columns of wider rows, pass gradient rows of the
+ * same stride. */
 #define NF4LS_PREF_SIGMOID 0
 #define NF4LS_PREF_HINGE   1
 #define NF4LS_PREF_SQUARED 2

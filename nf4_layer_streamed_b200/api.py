@@ -702,7 +702,8 @@ def preference_loss_fwd(pack: PackedRows, logits: torch.Tensor, targets: torch.T
 def preference_loss_bwd(pack: PackedRows, logits: torch.Tensor, targets: torch.Tensor, fwd: PreferenceForward,
                         grad_scale: float = 1.0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gradient of the logits (bf16 [total, vocab]) of the loss that fwd is of.  out: rows to
-    write to; the logits themselves for a gradient in place."""
+    write to; the logits themselves for a gradient in place.  For logits that are the first
+    columns of wider rows, an out of the same row stride is written faster."""
     pack = _need_pack(pack)
     n = pack.total
     ld = _logits2d(logits, "logits", n)
@@ -735,7 +736,8 @@ def policy_loss(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Ten
     [rows], dlogits bf16 [rows, vocab] or None without grad).  old_logp, ref_logp,
     advantages, weights: fp32 [rows] (ref_logp None when kl_coef is 0); the weights carry the
     normalisation, for instance 1 / the number of rows with a target.  out: rows to write the
-    gradient to; the logits themselves for a gradient in place."""
+    gradient to (its stride as for preference_loss_bwd); the logits themselves for a gradient
+    in place."""
     _need(targets, "targets", torch.int32)
     n = targets.numel()
     ld = _logits2d(logits, "logits", n)

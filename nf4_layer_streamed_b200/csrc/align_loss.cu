@@ -26,8 +26,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 // and four: 8000 rows of 16k logits 91 and 113 us (policy), 4000 rows 33 and 39 (statistics),
 // 38 and 42 (gradient); 2048 rows of 49k 38 and 38, 57 and 54.  Rows so long that those in
 // work do not stay in L2 from a policy row's first pass to its second: two blocks an SM of 768
-// threads that hold 96 KB of their row in shared memory, 1999 rows of 128k 177 us instead of
-// 196; of 65k 103 instead of 97.
+// threads that hold 96 KB of their row in shared memory.  1999 rows, four blocks of 512 and
+// two of 768: of 65k 98 and 102 us, 74k 110 and 105, 98k 148 and 134, 128k 195 and 175.  A call
+// without a gradient takes the same blocks for the sake of the same bits, though the smaller
+// ones are faster there (128k 70 and 82 us).
 constexpr int kShortRow = 24576, kLongRow = 98304;  // logits
 
 __device__ __forceinline__ float exp2_fast(float x) {

@@ -111,11 +111,12 @@ __device__ __forceinline__ void store_tile(const CUtensorMap* map, __nv_bfloat16
 //   from; o = O / sum p.
 // Within a tile these depend on one another; the second block's products run meanwhile, and
 // the first half of P V under the second half's exponentials.  16.4k rows of 8B heads, the
-// tensor core's work 444 us: 740 us; 2048 rows: 25.8 us.  A tile is 1024 cycles of the tensor
+// tensor core's work 444 us: 647 us alone, 755 back to back under the power cap; 2048 rows:
+// 26.7 us.  A tile is 1024 cycles of the tensor
 // core and as many of the exponential unit; a block takes 3400 for it, since scores to
 // registers, exponentials, P back and a wait at each hand-over follow one another, and two
-// blocks keep both units 60% busy.  Built and measured beside it (long, short): two tiles of
-// one block taking turns under one issuer, 751 and 31 us; blocks that go through a list of
+// blocks keep both units 59% busy.  Built and measured beside it, when it took 740 and 25.8 us
+// (long, short): two tiles of one block taking turns under one issuer, 751 and 31 us; blocks that go through a list of
 // tiles, 801 and 25.6 us (the list's state spills the scores); a row shared by two warps,
 // 854 and 28 us; three of eight exponentials by a cubic on the multiplier instead of the
 // exponential unit, 3% slower (13 issue slots for 8 cycles of the unit).  Every lane
@@ -401,7 +402,8 @@ __global__ void __launch_bounds__(F_THREADS, 2) k_packed_fwd(const __grid_consta
 // halves, so that the product of the first half runs under the making of the second.  The
 // tiles come through two rings: those that the first and the last product of an item read
 // (K; Q) live longest and have three stages, the others (V; dO) two.  12.2k rows of 8B heads,
-// the tensor core's work of both sides 1258 us: 1600 us, 1820 under the power cap.
+// the tensor core's work of both sides 1258 us: 1555 us alone, 1850 back to back under the
+// power cap.
 // A small kernel before them forms delta = rowsum(dO * O) and puts it beside lse log2e.
 // Accumulation runs in a fixed order (query side: key tiles in order; key side: query heads of
 // the group, then query tiles), so results are bit-reproducible.
@@ -436,9 +438,10 @@ __device__ __forceinline__ bool smem_base(uint8_t* raw, uint8_t** base, int* err
 }
 
 // STATISTICS of the query rows for both sides: delta = rowsum(dO * O), and lse log2(e) beside
-// it, a block per query tile and head.  Bound by memory (2048 rows of 8B heads: 34 MB).
-// With them the two sides need nothing of one another and share the GPU; when the query side
-// formed them, the key side stood behind it (2048 rows 70 us, 63 so).
+// it, a block per query tile and head.  Bound by memory for long batches (12.2k rows of 8B
+// heads 35 us, 70% of the DRAM rate), by the latency of its loads and reductions for short
+// ones (2048 rows 10 us, 40%).  With them the two sides need nothing of one another and share
+// the GPU; when the query side formed them, the key side stood behind it (2048 rows 70 us, 64 so).
 template <int D>
 __global__ void __launch_bounds__(256, 5) k_packed_stats(const StatsParams p) {
   constexpr int L = D / 8, STEP = 256 / L, N = TT / STEP;  // lanes of a row; rows at a time; rows of a thread

@@ -1,7 +1,6 @@
 // Plan of a packed batch: sequences of different lengths whose rows lie one behind the
-// other.  Host only: the caller copies the filled plan to the device once and every
-// packed call of the batch (each layer's forward, recompute and backward, the losses)
-// reads it there.
+// other.  Host only: the caller copies the filled plan to the device once, and every
+// packed call on the batch (attention and its gradients, the preference loss) reads it there.
 #include <algorithm>
 #include <cstring>
 #include <new>
