@@ -386,3 +386,51 @@ def test_grad_scale_scales_every_element(vocab):
     half_loss, half_logp, half = api.policy_loss(*args, grad_scale=0.5)
     check_half(half, d, vocab)
     assert torch.equal(half_loss, loss) and torch.equal(half_logp, logp)
+
+
+def test_captured_behind_other_kinds_of_work():
+    """Launches that may begin early, captured behind a memset, a copy, a join of two streams, and first of all."""
+    vocab, lengths = 5000, [9, 11, 13, 7]
+    x, t, _ = make(40, vocab, seed=2)
+    pack, none = api.PackedRows(lengths), api.PackedRows([0, 0])
+    ref, r = torch.zeros(4, device=DEV), torch.ones(40, device=DEV)
+    f = api.preference_loss_fwd(pack, x, t, ref, 0.1)
+    want = api.preference_loss_bwd(pack, x, t, f)
+    out, y, side = torch.empty_like(x), x.clone(), torch.cuda.Stream()
+    gap = torch.tensor([1.0, 3.0], device=DEV)
+    torch.cuda.synchronize()
+
+    def memset():
+        out.zero_()
+
+    def copy():
+        y.copy_(x)
+
+    def join():
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            out.fill_(1.0)
+        y.copy_(x)
+        torch.cuda.current_stream().wait_stream(side)
+
+    def nothing():
+        pass
+    for before in (memset, copy, join, nothing):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            before()
+            api.preference_loss_bwd(pack, y, t, f, out=out)
+            y2 = y.clone()
+            empty = api.preference_loss_fwd(none, x[:0], t[:0], gap, 0.5)
+            before()
+            loss = api.policy_loss(x[:0], t[:0], r[:0], None, r[:0], r[:0], 0.2, 0.2)[0]
+            full = api.policy_loss(y2, t, r, None, r, r, 0.2, 0.2)
+            api.preference_loss_bwd(pack, y, t, f, out=out)
+        for _ in range(2):
+            y.zero_() if before in (copy, join) else None
+            out.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want), before.__name__
+            assert empty.loss.item() == pytest.approx(math.log1p(math.exp(-1.0)), rel=1e-6) and loss.item() == 0.0
+            assert torch.isfinite(full[0]).all()
